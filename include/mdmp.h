@@ -264,6 +264,127 @@ int mp_energy_forces_heads(const mp_model* m, const mp_heads* heads, const mp_gr
                            double* head_energy, double* energy, float* forces, float* head_atom_energy, void* ws,
                            size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------ block operators ---
+ * The operators of a transformer block on atom rows, for a global block beside
+ * the cutoff layers: a product with its epilogue, a gated feed-forward, attention
+ * between all atoms of each structure, and the norms around a block; each with
+ * its backward pass, for forces and for training.
+ *
+ * Rows: a matrix of n rows is a device pointer and a row stride ld (elements), so
+ * h^0 of a feature array [n][K][C] is (h, K C); rows must be 16-byte aligned and
+ * ld a multiple of 16 bytes.  Features and weight matrices are of feat_dtype
+ * (0 float32, 1 bfloat16); vectors of parameters, positions and slopes and the
+ * gradients of those are float32.  bfloat16: products take bf16 operands with
+ * float32 accumulation, everything else is float32, and each output is rounded
+ * once; an intermediate that is the operand of a second product (hidden units,
+ * attention weights, their gradients) is rounded to bf16 on the way in.  channels
+ * C: 16 (float32 only), 32, 64 or 128.  n = 0 is allowed: no row is touched and
+ * parameter gradients are zeros.  Outputs must not overlap inputs or one another
+ * unless a call says so.  All calls only enqueue work (no host sync, no
+ * allocation, no memset nodes, so they can be captured) and give equal bits for
+ * equal inputs.  ws: device scratch of at least the _ws call's bytes, 16-byte
+ * aligned, used by one call at a time. */
+#define MP_ACT_NONE 0
+#define MP_ACT_SILU 1
+#define MP_ACT_SIGMOID 2
+
+/* y = residual + act(x w^T + bias).  x [n][in], w [out][in] contiguous, bias [out]
+ * (nullable), residual [n][out] (nullable; y may be residual), y [n][out].  in as
+ * channels above; out a multiple of 16 in 16..1024.  act: MP_ACT_*. */
+int mp_linear(int32_t n, int32_t in, int32_t out, int32_t feat_dtype, int32_t act, const void* x, int64_t ldx,
+              const void* w, const float* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
+              hipStream_t stream);
+/* Gradients of mp_linear for dy [n][out] (the residual's gradient is dy itself):
+ * dx [n][in], dw [out][in], dbias [out], each nullable; ws is needed for dw and dbias. */
+int mp_linear_bwd_ws(int32_t n, int32_t in, int32_t out, int32_t feat_dtype, size_t* bytes);
+int mp_linear_bwd(int32_t n, int32_t in, int32_t out, int32_t feat_dtype, int32_t act, const void* x, int64_t ldx,
+                  const void* w, const float* bias, const void* dy, int64_t lddy, void* dx, int64_t lddx, void* dw,
+                  float* dbias, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* y = residual + (act(x w_gate^T) * (x w_up^T)) w_down^T, the hidden units never in
+ * memory.  w_gate, w_up [hidden][C], w_down [C][hidden] contiguous, 16-byte aligned;
+ * hidden a multiple of 32 in 32..4096; act MP_ACT_SILU or MP_ACT_SIGMOID.  residual
+ * nullable; y may be residual. */
+int mp_gated_ffn(int32_t n, int32_t channels, int32_t hidden, int32_t feat_dtype, int32_t act, const void* x,
+                 int64_t ldx, const void* w_gate, const void* w_up, const void* w_down, const void* residual,
+                 int64_t ldr, void* y, int64_t ldy, hipStream_t stream);
+/* Gradients of mp_gated_ffn for dy [n][C]: dx [n][C] (nullable), and dw_gate, dw_up,
+ * dw_down (all three or none; ws is needed for them). */
+int mp_gated_ffn_bwd_ws(int32_t n, int32_t channels, int32_t hidden, int32_t feat_dtype, size_t* bytes);
+int mp_gated_ffn_bwd(int32_t n, int32_t channels, int32_t hidden, int32_t feat_dtype, int32_t act, const void* x,
+                     int64_t ldx, const void* w_gate, const void* w_up, const void* w_down, const void* dy,
+                     int64_t lddy, void* dx, int64_t lddx, void* dw_gate, void* dw_up, void* dw_down, void* ws,
+                     size_t ws_bytes, hipStream_t stream);
+
+/* The norm after a block, its gate and residual scale, and the norm before the next
+ * block.  With rms(t)^2 = mean_c t_c^2 + eps:
+ *   y = x + scale * sigmoid(gate) * (w_post * b / rms(b)),   u = w_pre * y / rms(y)
+ * x (residual stream), b (block output) and gate (pre-activations) are rows of C;
+ * scale, w_post, w_pre float32 [C], 16-byte aligned.  gate null: no gate; scale
+ * null: 1; w_post null: b itself, not normed; w_pre null: no u.  u is formed from y
+ * before y is rounded.  eps >= 1e-30.  y may be x or b. */
+typedef struct {
+  int32_t n, channels, feat_dtype;
+  float eps;
+  const void* x;
+  int64_t ldx;
+  const void* b;
+  int64_t ldb;
+  const void* gate;
+  int64_t ldg;
+  const float* scale;
+  const float* w_post;
+  const float* w_pre;
+} mp_norm_args;
+int mp_norm_block(const mp_norm_args* a, void* y, int64_t ldy, void* u, int64_t ldu, hipStream_t stream);
+/* Gradients for dy, du (one may be null: zero): dx, db, dgate rows, dscale, dw_post,
+ * dw_pre [C]; each nullable.  ws is needed for the parameter gradients.  dx may be
+ * dy, db may be du. */
+int mp_norm_block_bwd_ws(int32_t n, int32_t channels, int32_t feat_dtype, size_t* bytes);
+int mp_norm_block_bwd(const mp_norm_args* a, const void* dy, int64_t lddy, const void* du, int64_t lddu, void* dx,
+                      int64_t lddx, void* db, int64_t lddb, void* dgate, int64_t lddg, float* dscale, float* dw_post,
+                      float* dw_pre, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Attention between all atoms of each structure, beyond the cutoff.  For atom i of
+ * structure b and head k (channels k d .. k d + d - 1, d = C / heads):
+ *   t_ij = q_i^k . k_j^k / sqrt(d),   s_ij = cap tanh(t_ij / cap)  (cap = 0: t_ij)
+ *   a_ij = softmax_j(s_ij - slope_k r_ij) over the atoms j of b with mask_j != 0
+ *   out_i = sum_j a_ij v_j
+ * r_ij = |x_j - x_i|, minimum image if box_L > 0 (positions may be unwrapped).  An
+ * atom whose structure has no unmasked atom gets zeros.  Masked atoms' keys and
+ * values are not used, whatever they hold (their own rows of out are written), and
+ * structures do not see one another.  The atoms of structure b are rows
+ * struct_ptr[b] .. struct_ptr[b+1] - 1 (device, int32 [n_struct + 1], struct_ptr[0] =
+ * 0, ascending, empty structures allowed); rows at or past struct_ptr[n_struct] are
+ * left as they are in every output.  pos and slope both null: no distance term.
+ * heads: C / heads is 16, 32 or 64. */
+typedef struct {
+  int32_t n, n_struct, channels, heads, feat_dtype;
+  float cap, box_L;
+  const int32_t* struct_ptr;
+  const float* pos;     /* [n][3] or null */
+  const float* slope;   /* [heads] or null */
+  const uint8_t* mask;  /* [n] or null: every atom */
+  const void* q;
+  int64_t ldq;
+  const void* k;
+  int64_t ldk;
+  const void* v;
+  int64_t ldv;
+} mp_attention_args;
+/* saved (nullable): float32 of mp_structure_attention_saved count, what the backward
+ * pass needs of this call (with it, bf16 attention weights enter the sum with twice
+ * the bits, so out may differ from a call without it in its last bit). */
+int mp_structure_attention_saved(int32_t n, int32_t channels, int32_t heads, int32_t feat_dtype, int64_t* floats);
+int mp_structure_attention(const mp_attention_args* a, void* out, int64_t ldo, float* saved, hipStream_t stream);
+/* Gradients for dout: dq, dk, dv rows; dpos [n][3] and dslope [heads] float32 (nullable;
+ * need pos and slope).  out: the forward's output. */
+int mp_structure_attention_bwd_ws(int32_t n, int32_t n_struct, int32_t channels, int32_t heads, size_t* bytes);
+int mp_structure_attention_bwd(const mp_attention_args* a, const void* out, int64_t ldo, const float* saved,
+                               const void* dout, int64_t lddo, void* dq, int64_t lddq, void* dk, int64_t lddk,
+                               void* dv, int64_t lddv, float* dpos, float* dslope, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+
 /* ---------------------------------------------------------------- MD -------
  * NVE velocity Verlet with skin-triggered rebuilds (Tessera abstract: a
  * conservative skin lets each rebuild interval replay as one captured

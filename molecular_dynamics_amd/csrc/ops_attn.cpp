@@ -1,0 +1,140 @@
+// C ABI of the attention between all atoms of each structure.
+#include <cmath>
+
+#include "ops_api.hpp"
+#include "ops_attn.hpp"
+
+namespace mdmp {
+namespace ops {
+namespace {
+
+// Structures of up to this many atoms on average: one wave per 16 atoms walks its structure
+// alone.  Longer ones: four waves share the 16 atoms and split the other side, which fills
+// the chip with a quarter of the atoms and quarters each wave's walk.
+constexpr int kSplitAbove = 64;
+
+int check_shape(const char* who, int32_t n, int32_t channels, int32_t heads, int32_t dt) {
+  MP_TRY(check_width(who, channels, dt));
+  if (n < 0) return arg_error(std::string(who) + ": n must be >= 0");
+  const int dh = heads >= 1 && channels % heads == 0 ? channels / heads : 0;
+  if (dh != 16 && dh != 32 && dh != 64) return arg_error(std::string(who) + ": channels / heads must be 16, 32 or 64");
+  return MP_OK;
+}
+
+int attn_args(const char* who, const mp_attention_args* a, AttnArgs& A) {
+  if (!a) return arg_error(std::string(who) + ": null arguments");
+  MP_TRY(check_shape(who, a->n, a->channels, a->heads, a->feat_dtype));
+  if (a->n_struct < 0) return arg_error(std::string(who) + ": n_struct must be >= 0");
+  if (!(a->cap >= 0) || !std::isfinite(a->cap)) return arg_error(std::string(who) + ": cap must be finite and >= 0");
+  if (!(a->box_L >= 0) || !std::isfinite(a->box_L))
+    return arg_error(std::string(who) + ": box_L must be finite and >= 0 (0: open boundary)");
+  if ((a->pos != nullptr) != (a->slope != nullptr))
+    return arg_error(std::string(who) + ": give both pos and slope, or neither");
+  if ((int64_t)a->n / 16 + a->n_struct > INT32_MAX) return arg_error(std::string(who) + ": too many structures");
+  A = AttnArgs{};
+  A.n = a->n, A.n_struct = a->n_struct;
+  A.sptr = a->struct_ptr, A.pos = a->pos, A.slope = a->slope, A.mask = a->mask;
+  A.q = a->q, A.k = a->k, A.v = a->v;
+  A.ldq = a->ldq, A.ldk = a->ldk, A.ldv = a->ldv;
+  A.to_fix = a->box_L > 0 ? 4294967296.0 / (double)a->box_L : 0.0;
+  A.unit = a->box_L > 0 ? (float)((double)a->box_L / 4294967296.0) : 1.0f;
+  A.scale = (float)(1.0 / std::sqrt((double)(a->channels / a->heads)));
+  A.cap = a->cap;
+  if (a->n == 0 || a->n_struct == 0) return MP_OK;
+  if (!a->struct_ptr) return arg_error(std::string(who) + ": null struct_ptr");
+  if (!a->q || !a->k || !a->v) return arg_error(std::string(who) + ": null q, k or v");
+  const int C = a->channels, es = a->feat_dtype == 1 ? 2 : 4;
+  if (!rows_ok(a->q, a->ldq, C, es) || !rows_ok(a->k, a->ldk, C, es) || !rows_ok(a->v, a->ldv, C, es))
+    return arg_error(std::string(who) +
+                     ": rows of q, k and v must be 16-byte aligned, with a row stride of at least their width and a "
+                     "multiple of 16 bytes");
+  return MP_OK;
+}
+
+int launch(const mp_attention_args* a, const AttnArgs& A, int what, hipStream_t st) {
+  const bool split = (int64_t)a->n > (int64_t)kSplitAbove * a->n_struct;
+  const int dh = a->channels / a->heads;
+  return a->feat_dtype == 1 ? launch_attn_bf16(A, a->channels, dh, split, what, st)
+                            : launch_attn_f32(A, a->channels, dh, split, what, st);
+}
+
+// saved: [n][C] unrounded output (bf16 features only), then [n][H] base-2 log-sums
+int64_t saved_o32(int64_t n, int C, int dt) { return dt == 1 ? n * C : 0; }
+
+}  // namespace
+}  // namespace ops
+}  // namespace mdmp
+
+using namespace mdmp;
+
+extern "C" int mp_structure_attention_saved(int32_t n, int32_t channels, int32_t heads, int32_t dt, int64_t* floats) {
+  MP_TRY(ops::check_shape("mp_structure_attention_saved", n, channels, heads, dt));
+  if (!floats) return arg_error("mp_structure_attention_saved: null floats");
+  *floats = ops::saved_o32(n, channels, dt) + (int64_t)n * heads;
+  return MP_OK;
+}
+
+extern "C" int mp_structure_attention(const mp_attention_args* a, void* out, int64_t ldo, float* saved,
+                                      hipStream_t st) {
+  ops::AttnArgs A;
+  MP_TRY(ops::attn_args("mp_structure_attention", a, A));
+  if (a->n == 0 || a->n_struct == 0) return MP_OK;
+  if (!out) return arg_error("mp_structure_attention: null out");
+  MP_ROWS("mp_structure_attention", "out", out, ldo, a->channels, a->feat_dtype);
+  if ((uintptr_t)saved & 15) return arg_error("mp_structure_attention: saved must be 16-byte aligned");
+  A.out = out, A.ldo = ldo;
+  if (saved) {
+    A.o32 = a->feat_dtype == 1 ? saved : nullptr;
+    A.lse = saved + ops::saved_o32(a->n, a->channels, a->feat_dtype);
+  }
+  ProfScope p("structure_attention", st);
+  return ops::launch(a, A, 0, st);
+}
+
+extern "C" int mp_structure_attention_bwd_ws(int32_t n, int32_t n_struct, int32_t channels, int32_t heads,
+                                             size_t* bytes) {
+  MP_TRY(ops::check_shape("mp_structure_attention_bwd_ws", n, channels, heads, 0));
+  if (n_struct < 0 || !bytes) return arg_error("mp_structure_attention_bwd_ws: bad arguments");
+  Arena ar(nullptr, 0, true);
+  ar.take<float>((int64_t)n * heads);
+  ar.take<float>(((int64_t)n / 16 + n_struct) * heads);
+  *bytes = ar.off;
+  return MP_OK;
+}
+
+extern "C" int mp_structure_attention_bwd(const mp_attention_args* a, const void* out, int64_t ldo, const float* saved,
+                                          const void* dout, int64_t lddo, void* dq, int64_t lddq, void* dk,
+                                          int64_t lddk, void* dv, int64_t lddv, float* dpos, float* dslope, void* ws,
+                                          size_t ws_bytes, hipStream_t st) {
+  ops::AttnArgs A;
+  MP_TRY(ops::attn_args("mp_structure_attention_bwd", a, A));
+  if ((dpos || dslope) && !a->pos) return arg_error("mp_structure_attention_bwd: dpos and dslope need pos and slope");
+  const int C = a->channels, H = a->heads, dt = a->feat_dtype;
+  if (a->n == 0 || a->n_struct == 0)  // no pair: the sum over nothing
+    return dslope ? ops::reduce_rows(nullptr, 0, H, H, dslope, false, st) : MP_OK;
+  if (!out || !saved || !dout || !dq || !dk || !dv)
+    return arg_error("mp_structure_attention_bwd: null out, saved, dout, dq, dk or dv");
+  MP_ROWS("mp_structure_attention_bwd", "out", out, ldo, C, dt);
+  MP_ROWS("mp_structure_attention_bwd", "dout", dout, lddo, C, dt);
+  MP_ROWS("mp_structure_attention_bwd", "dq", dq, lddq, C, dt);
+  MP_ROWS("mp_structure_attention_bwd", "dk", dk, lddk, C, dt);
+  MP_ROWS("mp_structure_attention_bwd", "dv", dv, lddv, C, dt);
+  if ((uintptr_t)saved & 15) return arg_error("mp_structure_attention_bwd: saved must be 16-byte aligned");
+  if (!ws || ((uintptr_t)ws & 15)) return arg_error("mp_structure_attention_bwd: workspace null or not 16-byte aligned");
+  const int64_t slots = (int64_t)a->n / 16 + a->n_struct;
+  Arena ar(ws, ws_bytes);
+  A.dsum = ar.take<float>((int64_t)a->n * H);
+  float* part = ar.take<float>(slots * H);
+  if (!ar.ok()) return arg_error("mp_structure_attention_bwd: workspace too small");
+  A.o = out, A.ldo = ldo, A.dout = dout, A.lddo = lddo;
+  A.dq = dq, A.lddq = lddq, A.dk = dk, A.lddk = lddk, A.dv = dv, A.lddv = lddv;
+  A.o32 = const_cast<float*>(dt == 1 ? saved : nullptr);
+  A.lse = const_cast<float*>(saved + ops::saved_o32(a->n, C, dt));
+  A.dpos = dpos;
+  A.dslope_part = dslope ? part : nullptr;
+  ProfScope p("structure_attention_bwd", st);
+  MP_TRY(ops::launch(a, A, 1, st));
+  MP_TRY(ops::launch(a, A, 2, st));
+  if (dslope) MP_TRY(ops::reduce_rows(part, slots, H, H, dslope, false, st));
+  return MP_OK;
+}

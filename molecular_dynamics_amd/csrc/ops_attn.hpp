@@ -1,0 +1,756 @@
+// Attention between all atoms of each structure: kernels (see ops_attn_api.hip for the calls).
+//
+// Scores are held in base 2: x = log2(e) (s - slope r), p = 2^(x - m).
+//
+// Layout.  A wave owns 16 atoms of one structure (queries in the forward and the row pass,
+// keys in the column pass) as the columns of its MFMA tiles and walks the other side CK atoms
+// at a time.  Scores are formed transposed, S[other][own] = K Q^T, so a lane holds scores of
+// ONE own atom against 4 (x NT) others, in tile order: softmax weights and score gradients
+// are the next product's operand without leaving their lanes, and the distance of a pair is
+// formed once and used by every head (all C channels are in the wave).  The waves of a block
+// own the same 16 atoms and take every KW-th step of the other side; their sums are joined
+// in LDS in wave order, so equal inputs give equal bits.
+//
+// A wave never straddles structures: tile slots are numbered so that structure b owns slots
+// s_b / 16 + b .. (floor), which needs no pass over the sizes; the structure of a slot is found
+// by a 64-way search.  At most one slot per structure stays empty.
+//
+// Masked atoms and rows past the structure are staged as zeros and their scores set to -inf,
+// so nothing they hold (NaN, infinities) reaches another atom.
+//
+// Bound: VALU (per score one exp, with a cap exp and reciprocal more, at a quarter of the
+// rate, beside ~10 plain operations), not MFMA: at 32 channels per head a score costs 128
+// matrix operations, 1/8 of its VALU time.
+#pragma once
+#include "ops.hpp"
+
+namespace mdmp {
+namespace ops {
+
+struct AttnArgs {
+  int n, n_struct;
+  const int32_t* sptr;
+  const float* pos;
+  const float* slope;
+  const uint8_t* mask;
+  const void *q, *k, *v, *o, *dout;
+  int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
+  double to_fix;    // 2^32 / box_L, 0: open
+  float unit;       // length of one unit of a coordinate difference (box_L / 2^32, or 1)
+  float scale;      // 1 / sqrt(d)
+  float cap;        // 0: none
+  void *out, *dq, *dk, *dv;
+  float *lse, *o32;    // saved: [n][H] base-2 log-sum, [n][C] unrounded output (bf16 only)
+  float *dpos, *dslope_part, *dsum;  // [n][3]; [slots][H]; [n][H] sum_c dout out
+};
+
+// Coordinates as 32-bit words.  Periodic: fixed point in units of box_L / 2^32, so the
+// difference of two wraps into the minimum image by itself, with the border decided to 2^-32
+// of the box; open: the floats themselves.
+struct P3 {
+  uint32_t x, y, z;
+};
+__device__ __forceinline__ uint32_t coord(float x, double to_fix) {
+  return to_fix > 0 ? (uint32_t)(int64_t)rint((double)x * to_fix) : __float_as_uint(x);
+}
+__device__ __forceinline__ P3 load_pos(const AttnArgs& A, int i, bool on) {
+  if (!on || !A.pos) return P3{0u, 0u, 0u};
+  const float* p = A.pos + 3 * (int64_t)i;
+  return P3{coord(p[0], A.to_fix), coord(p[1], A.to_fix), coord(p[2], A.to_fix)};
+}
+// other - own
+__device__ __forceinline__ void diff(const P3& own, const u4& o, bool fix, float& dx, float& dy, float& dz) {
+  if (fix) {
+    dx = (float)(int32_t)(o.x - own.x);
+    dy = (float)(int32_t)(o.y - own.y);
+    dz = (float)(int32_t)(o.z - own.z);
+  } else {
+    dx = __uint_as_float(o.x) - __uint_as_float(own.x);
+    dy = __uint_as_float(o.y) - __uint_as_float(own.y);
+    dz = __uint_as_float(o.z) - __uint_as_float(own.z);
+  }
+}
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// tanh(y).  1 - 2 / (e^2y + 1) has an absolute error of about 1e-7; float32 features take the
+// series (to y^9, 8e-9 at the border) where that is no longer small against y.
+template <class T>
+__device__ __forceinline__ float tanh_of(float y) {
+  const float e = 1.0f - 2.0f * rcp(ex2(y * (2.0f * kLog2e)) + 1.0f);
+  if constexpr (sizeof(T) == 2) return e;
+  const float w = y * y;
+  const float p = fmaf(w, fmaf(w, fmaf(w, fmaf(w, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
+  return fabsf(y) < 0.25f ? y * p : e;
+}
+
+// Structure and row range of tile slot `slot` (R rows per slot); false: the slot is empty.
+// Row bounds are clamped to [0, n], so no struct_ptr can lead out of the arrays.
+template <int R>
+__device__ __forceinline__ bool find_slot(const AttnArgs& A, int slot, int lane, int& row0, int& s, int& e) {
+  int lo = 0, hi = A.n_struct - 1;
+  while (lo < hi) {
+    const int step = (hi - lo + 64) / 64;  // ceil((hi - lo + 1) / 64)
+    const int b = lo + lane * step;
+    const bool le = b <= hi && min(max(A.sptr[min(b, hi)], 0), A.n) / R + b <= slot;
+    const int k = __popcll(__ballot(le));
+    if (k == 0) return false;
+    lo += (k - 1) * step;
+    hi = min(hi, lo + step - 1);
+  }
+  s = min(max(A.sptr[lo], 0), A.n);
+  e = min(max(A.sptr[lo + 1], s), A.n);
+  const int t = slot - (s / R + lo);
+  row0 = s + t * R;
+  return t >= 0 && row0 < e;
+}
+
+// The CK atoms from k0 on of the other side: one bit each, whether they take part
+template <int CK>
+__device__ __forceinline__ uint64_t live(const AttnArgs& A, int k0, int e, int lane, bool masked) {
+  const bool on = lane < CK && k0 + lane < e && (!masked || !A.mask || A.mask[k0 + lane] != 0);
+  return __ballot(on);
+}
+template <int CK>
+constexpr uint64_t all_live() {
+  return (1ull << CK) - 1;
+}
+
+// CK rows of a matrix into one wave's LDS tile, rows without their bit as zeros
+template <class T, int C, int RS>
+struct WaveTile {
+  static constexpr int CK = MF<T>::CK, EV = MF<T>::EV, VPR = C / EV, IT = CK * VPR / 64;
+  static_assert(CK * VPR % 64 == 0, "whole waves");
+  u4 v[IT];
+  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int64_t k0, uint64_t on, int lane) {
+#pragma unroll
+    for (int j = 0; j < IT; ++j) {
+      const int x = lane + 64 * j, r = x / VPR, c = (x % VPR) * EV;
+      v[j] = ld16<u4>(src + (k0 + r) * ld + c, (on >> r) & 1);
+    }
+  }
+  __device__ __forceinline__ void put(T* dst, int lane) const {
+#pragma unroll
+    for (int j = 0; j < IT; ++j) {
+      const int x = lane + 64 * j;
+      *(u4*)(dst + (x / VPR) * RS + (x % VPR) * EV) = v[j];
+    }
+  }
+};
+
+// rows of a matrix as MFMA operands in natural order: frag[t][ch] = row k0 + 16 t + i
+template <class T, int C, int NTL>
+__device__ __forceinline__ void load_frags(typename MF<T>::F (&f)[NTL][C / MF<T>::CK], const T* src, int64_t ld,
+                                           int64_t k0, uint64_t on, int i, int g) {
+  using M = MF<T>;
+#pragma unroll
+  for (int t = 0; t < NTL; ++t) {
+    const T* p = src + (k0 + 16 * t + i) * ld + M::EV * g;
+    const bool o = (on >> (16 * t + i)) & 1;
+#pragma unroll
+    for (int ch = 0; ch < C / M::CK; ++ch) f[t][ch] = ld16<typename M::F>(p + ch * M::CK, o);
+  }
+}
+
+// sum over head h's channels of the product of an operand pair: acc += A B over the channel
+// chunks of the head.  Heads narrower than a chunk (bf16, 16 channels) take the chunk with
+// the other head's lane groups of one operand zeroed.
+template <class T, int DH, int NC>
+__device__ __forceinline__ f4 head_mma(f4 acc, const typename MF<T>::F (&a)[NC], const typename MF<T>::F (&b)[NC],
+                                       int h, int g) {
+  using M = MF<T>;
+  if constexpr (DH >= M::CK) {
+#pragma unroll
+    for (int c = 0; c < DH / M::CK; ++c) acc = M::mma(acc, a[h * (DH / M::CK) + c], b[h * (DH / M::CK) + c]);
+  } else {
+    static_assert(DH * 2 == M::CK, "two heads in a chunk");
+    const typename M::F bh = (g >> 1) == (h & 1) ? b[h / 2] : zero16<typename M::F>();
+    acc = M::mma(acc, a[h / 2], bh);
+  }
+  return acc;
+}
+
+// per own atom and head: sum over the lane's values of a channel sum that is spread over lane
+// groups; every lane group gets the total
+template <class T, int DH>
+__device__ __forceinline__ bool lane_in_head(int ch, int g, int h) {
+  if constexpr (DH >= MF<T>::CK)
+    return ch / (DH / MF<T>::CK) == h;
+  else
+    return 2 * ch + (g >> 1) == h;
+}
+
+template <class T, int C>
+struct AttnDims {
+  static constexpr int CK = MF<T>::CK, RS = C + 16 / (int)sizeof(T), OS = C + 4;
+};
+
+// ------------------------------------------------------------------------------ forward
+template <class T, int C, int DH, int KW>
+__global__ __launch_bounds__(64 * KW) void k_attn_fwd(AttnArgs A) {
+  using M = MF<T>;
+  using D = AttnDims<T, C>;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
+  constexpr int TILE = CK * RS * sizeof(T) + CK * 16, SLAB = 16 * OS * 4;
+  constexpr int WB = KW > 1 && SLAB > TILE ? SLAB : TILE;
+  __shared__ __align__(16) char s_w[KW][WB];
+  __shared__ float s_m[KW > 1 ? KW : 1][2][H][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  int row0, s, e;
+  if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
+  const int row = row0 + i;
+  const bool fix = A.to_fix > 0;
+  typename M::F qf[1][NC];
+  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, row0 + 16 <= e ? 0xffffull : (1ull << (e - row0)) - 1, i, g);
+  const P3 own = load_pos(A, row, row < e);
+  float slope[H], m[H], l[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    slope[h] = A.slope ? A.slope[h] * (kLog2e * A.unit) : 0.f;
+    m[h] = -INFINITY;
+    l[h] = 0.f;
+  }
+  f4 acc[C / 16];
+#pragma unroll
+  for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
+  T* vs = (T*)s_w[wave];
+  u4* ps = (u4*)(s_w[wave] + CK * RS * sizeof(T));
+  const float sc = A.cap > 0 ? A.scale / A.cap : A.scale * kLog2e, capl = A.cap * kLog2e;
+
+  for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
+    const uint64_t on = live<CK>(A, k0, e, lane, true);
+    WaveTile<T, C, RS> tv;
+    tv.fetch((const T*)A.v, A.ldv, k0, on, lane);
+    typename M::F kf[NT][NC];
+    load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, k0, on, i, g);
+    if (A.pos && lane < CK) {
+      const P3 p = load_pos(A, k0 + lane, (on >> lane) & 1);
+      ps[lane] = u4{p.x, p.y, p.z, 0u};
+    }
+    tv.put(vs, lane);
+    wave_sync();
+    f4 r[NT];
+    if (A.pos) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float dx, dy, dz;
+          diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
+          r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      f4 x[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
+        if (A.cap > 0) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[t][q] = capl * tanh_of<T>(x[t][q] * sc);
+        } else {
+          x[t] *= sc;
+        }
+        if (A.pos) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[t][q] = fmaf(-slope[h], r[t][q], x[t][q]);
+        }
+        if (on != all_live<CK>()) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (!((on >> (16 * t + 4 * g + q)) & 1)) x[t][q] = -INFINITY;
+        }
+      }
+      // the running maximum is raised only when a score passes it by 8 (p <= 2^8): the sums
+      // are exact relative to any reference, so most steps need no exchange and no rescale
+      float lm = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) lm = fmaxf(lm, fmaxf(fmaxf(x[t].x, x[t].y), fmaxf(x[t].z, x[t].w)));
+      if (__any(lm > m[h] + 8.0f)) {
+        const float mn = fmaxf(m[h], gmax(lm));
+        const float al = mn == -INFINITY ? 1.0f : ex2(m[h] - mn);
+        m[h] = mn;
+        l[h] *= al;
+#pragma unroll
+        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] *= al;
+      }
+      const float mu = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[t][q] = ex2(x[t][q] - mu);
+        l[h] += (x[t].x + x[t].y) + (x[t].z + x[t].w);
+      }
+      const typename M::F p = M::pack(x);
+      if (sizeof(T) == 2 && A.o32) {
+        // for a backward pass the weights enter as two bf16 values, p and its remainder
+        // (2^-18): o32, and with it dsum and the float32 gradients, keep float32's quality
+        f4 y[NT];
+        M::unpack(p, y);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) y[t] = x[t] - y[t];
+        const typename M::F p2 = M::pack(y);
+#pragma unroll
+        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
+          const typename M::F f = ldt<RS>(vs, 0, 16 * ct, lane);
+          acc[ct] = M::mma(M::mma(acc[ct], f, p2), f, p);
+        }
+      } else {
+#pragma unroll
+        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct)
+          acc[ct] = M::mma(acc[ct], ldt<RS>(vs, 0, 16 * ct, lane), p);
+      }
+    }
+    wave_sync();
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) l[h] = gsum(l[h]);
+
+  if constexpr (KW == 1) {
+    if (row >= e) return;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const float inv = l[h] > 0.f || l[h] != l[h] ? 1.0f / l[h] : 0.f;
+#pragma unroll
+      for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
+        acc[ct] *= inv;
+        const int c = 16 * ct + 4 * g;
+        st4((T*)A.out + (int64_t)row * A.ldo + c, acc[ct]);
+        if (A.o32) st4(A.o32 + (int64_t)row * C + c, acc[ct]);
+      }
+      if (A.lse && g == 0) A.lse[(int64_t)row * H + h] = l[h] > 0.f || l[h] != l[h] ? m[h] + log2f(l[h]) : INFINITY;
+    }
+  } else {
+    float* slab = (float*)s_w[wave];
+#pragma unroll
+    for (int ct = 0; ct < C / 16; ++ct) *(f4*)(slab + i * OS + 16 * ct + 4 * g) = acc[ct];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (g == 0) {
+        s_m[wave][0][h][i] = m[h];
+        s_m[wave][1][h][i] = l[h];
+      }
+    __syncthreads();
+    for (int x = threadIdx.x; x < 16 * (C / EV); x += 64 * KW) {
+      const int ri = x / (C / EV), c = (x % (C / EV)) * EV, h = c / DH;
+      if (row0 + ri >= e) break;
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) mm = fmaxf(mm, s_m[w][0][h][ri]);
+      f4 o[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const float mw = s_m[w][0][h][ri], f = mw == -INFINITY && mm != -INFINITY ? 0.f : (mm == -INFINITY ? 1.0f : ex2(mw - mm));
+        ll = fmaf(f, s_m[w][1][h][ri], ll);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[t] += f * *(const f4*)((const float*)s_w[w] + ri * OS + c + 4 * t);
+      }
+      const bool any = ll > 0.f || ll != ll;
+      const float inv = any ? 1.0f / ll : 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        o[t] *= inv;
+        if (A.o32) st4(A.o32 + (int64_t)(row0 + ri) * C + c + 4 * t, o[t]);
+      }
+      st_row<T>((T*)A.out + (int64_t)(row0 + ri) * A.ldo + c, o);
+      if (A.lse && c % DH == 0) A.lse[(int64_t)(row0 + ri) * H + h] = any ? mm + log2f(ll) : INFINITY;
+    }
+  }
+}
+
+// Score, softmax weight and score gradient of one lane's 4 pairs:
+//   p = 2^(x - lse), dl = p (dp - dsum); ds = dl times the cap's slope 1 - tanh^2
+template <class T>
+__device__ __forceinline__ void pair_grad(const AttnArgs& A, float sc, float capl, f4 sraw, f4 dp, f4 r, float slope,
+                                          f4 lse, f4 dsum, uint64_t on, int k, f4& p, f4& dl, f4& ds) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float x, f = 1.0f;
+    if (A.cap > 0) {
+      const float th = tanh_of<T>(sraw[q] * sc);
+      x = capl * th;
+      f = fmaf(-th, th, 1.0f);
+    } else {
+      x = sraw[q] * sc;
+    }
+    if (A.pos) x = fmaf(-slope, r[q], x);
+    const bool o = (on >> (k + q)) & 1;
+    p[q] = o ? ex2(x - lse[q]) : 0.f;
+    dl[q] = o ? p[q] * (dp[q] - dsum[q]) : 0.f;
+    ds[q] = dl[q] * f;
+  }
+}
+
+// ------------------------------------------------------------------------------ row pass
+// For 16 queries: dsum_i = sum_c dout out (per head), dq_i = scale sum_j ds_ij k_j, the queries'
+// side of the position gradient, and the block's partial of dslope.  out enters unrounded (o32)
+// so that dsum, and with it the float32 gradients, do not carry bf16's rounding.
+template <class T, int C, int DH, int KW>
+__global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
+  using M = MF<T>;
+  using D = AttnDims<T, C>;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
+  constexpr int TILE = CK * RS * sizeof(T) + CK * 16, SLAB = 16 * OS * 4;
+  constexpr int WB = KW > 1 && SLAB > TILE ? SLAB : TILE;
+  __shared__ __align__(16) char s_w[KW][WB];
+  __shared__ float s_p[KW][3][16];
+  __shared__ float s_s[KW][H];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  int row0, s, e;
+  if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) {
+    if (A.dslope_part && threadIdx.x < H) A.dslope_part[(int64_t)blockIdx.x * H + threadIdx.x] = 0.f;
+    return;
+  }
+  const int row = row0 + i;
+  const bool fix = A.to_fix > 0;
+  const uint64_t own_on = row0 + 16 <= e ? 0xffffull : (1ull << (e - row0)) - 1;
+  typename M::F qf[1][NC], of[1][NC];
+  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, own_on, i, g);
+  load_frags<T, C, 1>(of, (const T*)A.dout, A.lddo, row0, own_on, i, g);
+  const P3 own = load_pos(A, row, row < e);
+  float slope[H], lse[H], dsum[H], dsl[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    slope[h] = A.slope ? A.slope[h] * (kLog2e * A.unit) : 0.f;
+    lse[h] = row < e ? A.lse[(int64_t)row * H + h] : INFINITY;
+    dsum[h] = dsl[h] = 0.f;
+  }
+#pragma unroll
+  for (int ch = 0; ch < NC; ++ch) {
+    f4 a[NT];
+    M::unpack(of[0][ch], a);
+    float d = 0.f;
+    if (row < e) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float* op = sizeof(T) == 2 ? A.o32 + (int64_t)row * C : (const float*)A.o + (int64_t)row * A.ldo;
+        const f4 o = *(const f4*)(op + ch * CK + EV * g + 4 * t);
+        d = fmaf(a[t].x, o.x, fmaf(a[t].y, o.y, fmaf(a[t].z, o.z, fmaf(a[t].w, o.w, d))));
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) dsum[h] += lane_in_head<T, DH>(ch, g, h) ? d : 0.f;
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    dsum[h] = gsum(dsum[h]);
+    if (wave == 0 && g == 0 && row < e) A.dsum[(int64_t)row * H + h] = dsum[h];
+  }
+  f4 acc[C / 16];
+#pragma unroll
+  for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
+  float px = 0.f, py = 0.f, pz = 0.f;
+  T* ks = (T*)s_w[wave];
+  u4* ps = (u4*)(s_w[wave] + CK * RS * sizeof(T));
+  const float sc = A.cap > 0 ? A.scale / A.cap : A.scale * kLog2e, capl = A.cap * kLog2e;
+
+  for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
+    const uint64_t on = live<CK>(A, k0, e, lane, true);
+    WaveTile<T, C, RS> tk;
+    tk.fetch((const T*)A.k, A.ldk, k0, on, lane);
+    typename M::F vf[NT][NC];
+    load_frags<T, C, NT>(vf, (const T*)A.v, A.ldv, k0, on, i, g);
+    if (A.pos && lane < CK) {
+      const P3 p = load_pos(A, k0 + lane, (on >> lane) & 1);
+      ps[lane] = u4{p.x, p.y, p.z, 0u};
+    }
+    tk.put(ks, lane);
+    wave_sync();
+    f4 r[NT], wgt[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
+      if (A.pos) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float dx, dy, dz;
+          diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
+          r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      f4 ds[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        typename M::F kf[NC];
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) kf[ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
+        const f4 z = f4{0.f, 0.f, 0.f, 0.f};
+        const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
+        f4 p, dl;
+        const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
+        pair_grad<T>(A, sc, capl, x, dp, r[t], slope[h], L, S, on, 16 * t + 4 * g, p, dl, ds[t]);
+        if (A.pos) {
+          const float sl = A.slope[h];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
+            dsl[h] = fmaf(-dl[q], r[t][q], dsl[h]);
+          }
+        }
+      }
+      const typename M::F pd = M::pack(ds);
+#pragma unroll
+      for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] = M::mma(acc[ct], ldt<RS>(ks, 0, 16 * ct, lane), pd);
+    }
+    if (A.dpos) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float dx, dy, dz;
+          diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
+          const float f = r[t][q] > 0.f ? wgt[t][q] * rcp(r[t][q]) : 0.f;
+          px = fmaf(f, dx, px), py = fmaf(f, dy, py), pz = fmaf(f, dz, pz);
+        }
+    }
+    wave_sync();
+  }
+  if (A.dslope_part) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      dsl[h] = row < e ? dsl[h] : 0.f;
+      dsl[h] = group_sum<64>(dsl[h]);
+      if (lane == 0) s_s[wave][h] = dsl[h];
+    }
+  }
+  px = gsum(px), py = gsum(py), pz = gsum(pz);
+  if (g == 0) s_p[wave][0][i] = px, s_p[wave][1][i] = py, s_p[wave][2][i] = pz;
+  if constexpr (KW > 1) {
+    float* slab = (float*)s_w[wave];
+#pragma unroll
+    for (int ct = 0; ct < C / 16; ++ct) *(f4*)(slab + i * OS + 16 * ct + 4 * g) = acc[ct];
+  }
+  __syncthreads();
+  if (A.dslope_part && threadIdx.x < H) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) v += s_s[w][threadIdx.x];
+    A.dslope_part[(int64_t)blockIdx.x * H + threadIdx.x] = v * A.unit;
+  }
+  if (A.dpos && threadIdx.x < 48) {
+    const int ri = threadIdx.x / 3, a = threadIdx.x % 3;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) v += s_p[w][a][ri];
+    if (row0 + ri < e) A.dpos[3 * (int64_t)row0 + threadIdx.x] = v;
+  }
+  if constexpr (KW == 1) {
+    if (row >= e) return;
+#pragma unroll
+    for (int ct = 0; ct < C / 16; ++ct) st4((T*)A.dq + (int64_t)row * A.lddq + 16 * ct + 4 * g, acc[ct] * A.scale);
+  } else {
+    for (int x = threadIdx.x; x < 16 * (C / EV); x += 64 * KW) {
+      const int ri = x / (C / EV), c = (x % (C / EV)) * EV;
+      if (row0 + ri >= e) break;
+      f4 o[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        o[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < KW; ++w) o[t] += *(const f4*)((const float*)s_w[w] + ri * OS + c + 4 * t);
+        o[t] *= A.scale;
+      }
+      st_row<T>((T*)A.dq + (int64_t)(row0 + ri) * A.lddq + c, o);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ column pass
+// For 16 keys: dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij dout_i, and the keys' side of the
+// position gradient, added to what the row pass wrote.
+template <class T, int C, int DH, int KW>
+__global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
+  using M = MF<T>;
+  using D = AttnDims<T, C>;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
+  constexpr int TB = CK * RS * sizeof(T);
+  constexpr int TILE = 2 * TB + CK * 16 + 2 * H * CK * 4, SLAB = 2 * 16 * OS * 4;
+  constexpr int WB = KW > 1 && SLAB > TILE ? SLAB : TILE;
+  __shared__ __align__(16) char s_w[KW][WB];
+  __shared__ float s_p[KW][3][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  int row0, s, e;
+  if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
+  const int row = row0 + i;
+  const bool fix = A.to_fix > 0;
+  const uint64_t own_on = live<16>(A, row0, e, lane, true);
+  const bool own_live = (own_on >> i) & 1;
+  typename M::F kf[1][NC], vf[1][NC];
+  load_frags<T, C, 1>(kf, (const T*)A.k, A.ldk, row0, own_on, i, g);
+  load_frags<T, C, 1>(vf, (const T*)A.v, A.ldv, row0, own_on, i, g);
+  const P3 own = load_pos(A, row, own_live);
+  float slope[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) slope[h] = A.slope ? A.slope[h] * (kLog2e * A.unit) : 0.f;
+  f4 ak[C / 16], av[C / 16];
+#pragma unroll
+  for (int ct = 0; ct < C / 16; ++ct) ak[ct] = av[ct] = f4{0.f, 0.f, 0.f, 0.f};
+  float px = 0.f, py = 0.f, pz = 0.f;
+  T *qs = (T*)s_w[wave], *os = (T*)(s_w[wave] + TB);
+  u4* ps = (u4*)(s_w[wave] + 2 * TB);
+  float *ls = (float*)(s_w[wave] + 2 * TB + CK * 16), *ss = ls + H * CK;
+  const float sc = A.cap > 0 ? A.scale / A.cap : A.scale * kLog2e, capl = A.cap * kLog2e;
+
+  if (own_on != 0) {
+    for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
+      const uint64_t on = live<CK>(A, k0, e, lane, false);
+      WaveTile<T, C, RS> tq, to;
+      tq.fetch((const T*)A.q, A.ldq, k0, on, lane);
+      to.fetch((const T*)A.dout, A.lddo, k0, on, lane);
+      if (lane < CK) {
+        const bool l = (on >> lane) & 1;
+        if (A.pos) {
+          const P3 p = load_pos(A, k0 + lane, l);
+          ps[lane] = u4{p.x, p.y, p.z, 0u};
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          ls[h * CK + lane] = l ? A.lse[(int64_t)(k0 + lane) * H + h] : INFINITY;
+          ss[h * CK + lane] = l ? A.dsum[(int64_t)(k0 + lane) * H + h] : 0.f;
+        }
+      }
+      tq.put(qs, lane);
+      to.put(os, lane);
+      wave_sync();
+      f4 r[NT], wgt[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
+        if (A.pos) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float dx, dy, dz;
+            diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
+            r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+          }
+        }
+      }
+      const uint64_t own_bits = own_live ? ~0ull : 0ull;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        f4 p[NT], ds[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          typename M::F qf[NC], of[NC];
+#pragma unroll
+          for (int ch = 0; ch < NC; ++ch) {
+            qf[ch] = *(const typename M::F*)(qs + (16 * t + i) * RS + ch * CK + EV * g);
+            of[ch] = *(const typename M::F*)(os + (16 * t + i) * RS + ch * CK + EV * g);
+          }
+          const f4 z = f4{0.f, 0.f, 0.f, 0.f};
+          const f4 x = head_mma<T, DH, NC>(z, qf, kf[0], h, g), dp = head_mma<T, DH, NC>(z, of, vf[0], h, g);
+          const f4 L = *(const f4*)(ls + h * CK + 16 * t + 4 * g), S = *(const f4*)(ss + h * CK + 16 * t + 4 * g);
+          f4 dl;
+          pair_grad<T>(A, sc, capl, x, dp, r[t], slope[h], L, S, own_bits, 16 * t + 4 * g, p[t], dl, ds[t]);
+          if (A.pos) {
+            const float sl = A.slope[h];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
+          }
+        }
+        const typename M::F pp = M::pack(p), pd = M::pack(ds);
+#pragma unroll
+        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
+          av[ct] = M::mma(av[ct], ldt<RS>(os, 0, 16 * ct, lane), pp);
+          ak[ct] = M::mma(ak[ct], ldt<RS>(qs, 0, 16 * ct, lane), pd);
+        }
+      }
+      if (A.dpos) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float dx, dy, dz;
+            diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
+            const float f = r[t][q] > 0.f ? wgt[t][q] * rcp(r[t][q]) : 0.f;
+            px = fmaf(f, dx, px), py = fmaf(f, dy, py), pz = fmaf(f, dz, pz);
+          }
+      }
+      wave_sync();
+    }
+  }
+  px = gsum(px), py = gsum(py), pz = gsum(pz);
+  if (g == 0) s_p[wave][0][i] = px, s_p[wave][1][i] = py, s_p[wave][2][i] = pz;
+  if constexpr (KW > 1) {
+    float* slab = (float*)s_w[wave];
+#pragma unroll
+    for (int ct = 0; ct < C / 16; ++ct) {
+      *(f4*)(slab + i * OS + 16 * ct + 4 * g) = ak[ct];
+      *(f4*)(slab + (16 + i) * OS + 16 * ct + 4 * g) = av[ct];
+    }
+  }
+  __syncthreads();
+  if (A.dpos && threadIdx.x < 48) {
+    const int ri = threadIdx.x / 3, a = threadIdx.x % 3;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) v += s_p[w][a][ri];
+    if (row0 + ri < e) A.dpos[3 * (int64_t)row0 + threadIdx.x] += v;
+  }
+  if constexpr (KW == 1) {
+    if (row >= e) return;
+#pragma unroll
+    for (int ct = 0; ct < C / 16; ++ct) {
+      st4((T*)A.dk + (int64_t)row * A.lddk + 16 * ct + 4 * g, ak[ct] * A.scale);
+      st4((T*)A.dv + (int64_t)row * A.lddv + 16 * ct + 4 * g, av[ct]);
+    }
+  } else {
+    for (int x = threadIdx.x; x < 16 * (C / EV); x += 64 * KW) {
+      const int ri = x / (C / EV), c = (x % (C / EV)) * EV;
+      if (row0 + ri >= e) break;
+      f4 o[NT], u[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        o[t] = u[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          o[t] += *(const f4*)((const float*)s_w[w] + ri * OS + c + 4 * t);
+          u[t] += *(const f4*)((const float*)s_w[w] + (16 + ri) * OS + c + 4 * t);
+        }
+        o[t] *= A.scale;
+      }
+      st_row<T>((T*)A.dk + (int64_t)(row0 + ri) * A.lddk + c, o);
+      st_row<T>((T*)A.dv + (int64_t)(row0 + ri) * A.lddv + c, u);
+    }
+  }
+}
+
+// what: 0 forward, 1 row pass, 2 column pass
+int launch_attn_bf16(const AttnArgs& A, int C, int dh, bool split, int what, hipStream_t st);
+int launch_attn_f32(const AttnArgs& A, int C, int dh, bool split, int what, hipStream_t st);
+
+template <class T, int C, int DH>
+int launch_attn_c(const AttnArgs& A, bool split, int what, hipStream_t st) {
+  const unsigned blocks = (unsigned)(A.n / 16 + A.n_struct);
+  constexpr int KW = 4;
+  switch (what) {
+    case 0:
+      if (split)
+        k_attn_fwd<T, C, DH, KW><<<blocks, 64 * KW, 0, st>>>(A);
+      else
+        k_attn_fwd<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
+      break;
+    case 1:
+      if (split)
+        k_attn_row<T, C, DH, KW><<<blocks, 64 * KW, 0, st>>>(A);
+      else
+        k_attn_row<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
+      break;
+    default:
+      if (split)
+        k_attn_col<T, C, DH, KW><<<blocks, 64 * KW, 0, st>>>(A);
+      else
+        k_attn_col<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
+  }
+  MP_CHECK_LAUNCH();
+  return MP_OK;
+}
+
+}  // namespace ops
+}  // namespace mdmp

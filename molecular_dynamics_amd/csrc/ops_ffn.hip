@@ -1,0 +1,466 @@
+// Gated feed-forward block y = residual + (act(x Wg^T) * (x Wu^T)) Wd^T and its gradients.
+#include "ops_api.hpp"
+
+namespace mdmp {
+namespace ops {
+namespace {
+
+struct FfnArgs {
+  int64_t n, ldx, ldr, ldy, lddx;  // ldy: stride of y (forward) or dy (backward)
+  int hidden;
+  ActAB ab;
+  const void *x, *wg, *wu, *wd, *res, *dy;
+  void *y, *dx;
+  float* part;  // [splits][3 C hidden]: dWg [hidden][C], dWu [hidden][C], dWd [C][hidden]
+  int64_t rows_per_split;
+};
+
+constexpr int pad_of(int esize) { return 16 / esize; }
+
+// One chunk of CK hidden units of the three matrices, in LDS: rows of Wg and Wu (CK x C)
+// and columns of Wd (C x CK)
+template <class T, int C>
+struct Chunk {
+  using M = MF<T>;
+  static constexpr int CK = M::CK, RS = C + pad_of(sizeof(T)), RD = CK + pad_of(sizeof(T));
+  static constexpr int SIZE = 2 * CK * RS + C * RD;
+  Tile<T, CK, C, RS, 256> g, u;
+  Tile<T, C, CK, RD, 256> d;
+  __device__ __forceinline__ void fetch(const FfnArgs& A, int h0, int tid) {
+    g.fetch((const T*)A.wg + (int64_t)h0 * C, C, CK, tid);
+    u.fetch((const T*)A.wu + (int64_t)h0 * C, C, CK, tid);
+    d.fetch((const T*)A.wd + h0, A.hidden, C, tid);
+  }
+  __device__ __forceinline__ void put(T* s, int tid) const {
+    g.put(s, tid);
+    u.put(s + CK * RS, tid);
+    d.put(s + 2 * CK * RS, tid);
+  }
+};
+
+template <class T, int C, int AT>
+__device__ __forceinline__ void load_rows(typename MF<T>::F (&f)[AT][C / MF<T>::CK], const void* x, int64_t ld,
+                                          int64_t a0, int64_t n, int i, int g) {
+  using M = MF<T>;
+#pragma unroll
+  for (int at = 0; at < AT; ++at) {
+    const int64_t a = a0 + 16 * at + i;
+    const T* p = (const T*)x + a * ld + M::EV * g;
+#pragma unroll
+    for (int ch = 0; ch < C / M::CK; ++ch) f[at][ch] = ld16<typename M::F>(p + ch * M::CK, a < n);
+  }
+}
+
+// Forward.  A wave keeps 16 AT atoms' rows in registers and walks the hidden units CK at a
+// time: D[hid][a] = Wg x and Wu x with the hidden rows taken in the order nat_row, so a lane
+// ends with EV consecutive hidden units of its atom, which after act(.) * (.) are the
+// operand of D[c][a] += Wd h as they stand.  Hidden units live in registers only.  The
+// weights of a chunk are shared by the block's four waves through LDS (two buffers, the next
+// chunk's loads in flight during the products).  Bound: the matrix products and, beside
+// them, the sigmoid of every hidden unit (exp and reciprocal at a quarter of the VALU rate).
+template <class T, int C, int AT>
+__global__ __launch_bounds__(256) void k_ffn(FfnArgs A) {
+  using M = MF<T>;
+  using CH = Chunk<T, C>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = CH::RS, RD = CH::RD;
+  extern __shared__ __align__(16) char s_raw[];
+  T* s = (T*)s_raw;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int64_t a0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
+  typename M::F xf[AT][NC];
+  load_rows<T, C, AT>(xf, A.x, A.ldx, a0, A.n, i, g);
+  f4 acc[AT][NC][NT];
+#pragma unroll
+  for (int at = 0; at < AT; ++at)
+#pragma unroll
+    for (int p = 0; p < NC; ++p)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[at][p][t] = f4{0.f, 0.f, 0.f, 0.f};
+  CH ck;
+  ck.fetch(A, 0, threadIdx.x);
+  ck.put(s, threadIdx.x);
+  __syncthreads();
+  int b = 0;
+  for (int h0 = 0; h0 < A.hidden; h0 += CK, b ^= 1) {
+    const T *wg = s + b * CH::SIZE, *wu = wg + CK * RS, *wd = wu + CK * RS;
+    if (h0 + CK < A.hidden) ck.fetch(A, h0 + CK, threadIdx.x);
+    f4 zg[AT][NT], zu[AT][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int at = 0; at < AT; ++at) zg[at][t] = zu[at][t] = f4{0.f, 0.f, 0.f, 0.f};
+      const int row = nat_row<T>(t, i) * RS + EV * g;
+#pragma unroll
+      for (int ch = 0; ch < NC; ++ch) {
+        const typename M::F fg = *(const typename M::F*)(wg + row + ch * CK);
+        const typename M::F fu = *(const typename M::F*)(wu + row + ch * CK);
+#pragma unroll
+        for (int at = 0; at < AT; ++at) {
+          zg[at][t] = M::mma(zg[at][t], fg, xf[at][ch]);
+          zu[at][t] = M::mma(zu[at][t], fu, xf[at][ch]);
+        }
+      }
+    }
+    typename M::F h[AT];
+#pragma unroll
+    for (int at = 0; at < AT; ++at) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) zg[at][t][r] = act_val(zg[at][t][r], A.ab) * zu[at][t][r];
+      h[at] = M::pack(zg[at]);
+    }
+#pragma unroll
+    for (int p = 0; p < NC; ++p)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const typename M::F f = *(const typename M::F*)(wd + (p * CK + nat_row<T>(t, i)) * RD + EV * g);
+#pragma unroll
+        for (int at = 0; at < AT; ++at) acc[at][p][t] = M::mma(acc[at][p][t], f, h[at]);
+      }
+    if (h0 + CK < A.hidden) ck.put(s + (b ^ 1) * CH::SIZE, threadIdx.x);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int at = 0; at < AT; ++at) {
+    const int64_t a = a0 + 16 * at + i;
+    if (a >= A.n) continue;
+#pragma unroll
+    for (int p = 0; p < NC; ++p) {
+      const int c = p * CK + EV * g;
+      if (A.res) {
+        f4 q[NT];
+        M::unpack(*(const typename M::F*)((const T*)A.res + a * A.ldr + c), q);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[at][p][t] += q[t];
+      }
+      st_row<T>((T*)A.y + a * A.ldy + c, acc[at][p]);
+    }
+  }
+}
+
+// gradients of the hidden pre-activations: with h = act(zg) zu,
+//   dzu = dh act(zg),  dzg = dh zu act'(zg)
+__device__ __forceinline__ void hidden_grad(float zg, float zu, float dh, ActAB ab, float& h, float& dzg, float& dzu) {
+  float v, e;
+  act_both(zg, ab, v, e);
+  h = v * zu;
+  dzu = dh * v;
+  dzg = dh * zu * e;
+}
+
+// dx: the forward's first two products, dh = Wd^T dy (Wd read transposed from the same LDS
+// chunk), the hidden gradients in registers, and D[c][a] += Wg^T dzg + Wu^T dzu (the same
+// rows of Wg and Wu, read transposed).
+template <class T, int C, int AT>
+__global__ __launch_bounds__(256) void k_ffn_dx(FfnArgs A) {
+  using M = MF<T>;
+  using CH = Chunk<T, C>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = CH::RS, RD = CH::RD;
+  extern __shared__ __align__(16) char s_raw[];
+  T* s = (T*)s_raw;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int64_t a0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
+  typename M::F xf[AT][NC], df[AT][NC];
+  load_rows<T, C, AT>(xf, A.x, A.ldx, a0, A.n, i, g);
+  load_rows<T, C, AT>(df, A.dy, A.ldy, a0, A.n, i, g);
+  f4 acc[AT][NC][NT];
+#pragma unroll
+  for (int at = 0; at < AT; ++at)
+#pragma unroll
+    for (int p = 0; p < NC; ++p)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[at][p][t] = f4{0.f, 0.f, 0.f, 0.f};
+  CH ck;
+  ck.fetch(A, 0, threadIdx.x);
+  ck.put(s, threadIdx.x);
+  __syncthreads();
+  int b = 0;
+  for (int h0 = 0; h0 < A.hidden; h0 += CK, b ^= 1) {
+    const T *wg = s + b * CH::SIZE, *wu = wg + CK * RS, *wd = wu + CK * RS;
+    if (h0 + CK < A.hidden) ck.fetch(A, h0 + CK, threadIdx.x);
+    f4 zg[AT][NT], zu[AT][NT], dh[AT][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int at = 0; at < AT; ++at) zg[at][t] = zu[at][t] = dh[at][t] = f4{0.f, 0.f, 0.f, 0.f};
+      const int row = nat_row<T>(t, i) * RS + EV * g;
+#pragma unroll
+      for (int ch = 0; ch < NC; ++ch) {
+        const typename M::F fg = *(const typename M::F*)(wg + row + ch * CK);
+        const typename M::F fu = *(const typename M::F*)(wu + row + ch * CK);
+        const typename M::F fd = ldtn_nat<RD>(wd, ch * CK, 0, t, lane);
+#pragma unroll
+        for (int at = 0; at < AT; ++at) {
+          zg[at][t] = M::mma(zg[at][t], fg, xf[at][ch]);
+          zu[at][t] = M::mma(zu[at][t], fu, xf[at][ch]);
+          dh[at][t] = M::mma(dh[at][t], fd, df[at][ch]);
+        }
+      }
+    }
+    typename M::F dg[AT], du[AT];
+#pragma unroll
+    for (int at = 0; at < AT; ++at) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float h, a, c;
+          hidden_grad(zg[at][t][r], zu[at][t][r], dh[at][t][r], A.ab, h, a, c);
+          zg[at][t][r] = a;
+          zu[at][t][r] = c;
+        }
+      dg[at] = M::pack(zg[at]);
+      du[at] = M::pack(zu[at]);
+    }
+#pragma unroll
+    for (int p = 0; p < NC; ++p)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const typename M::F fg = ldtn_nat<RS>(wg, 0, p, t, lane), fu = ldtn_nat<RS>(wu, 0, p, t, lane);
+#pragma unroll
+        for (int at = 0; at < AT; ++at)
+          acc[at][p][t] = M::mma(M::mma(acc[at][p][t], fg, dg[at]), fu, du[at]);
+      }
+    if (h0 + CK < A.hidden) ck.put(s + (b ^ 1) * CH::SIZE, threadIdx.x);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int at = 0; at < AT; ++at) {
+    const int64_t a = a0 + 16 * at + i;
+    if (a >= A.n) continue;
+#pragma unroll
+    for (int p = 0; p < NC; ++p) st_row<T>((T*)A.dx + a * A.lddx + p * CK + EV * g, acc[at][p]);
+  }
+}
+
+// dWg, dWu, dWd over one split of the rows.  A wave owns 16 hidden units: their rows of Wg,
+// Wu and Wd^T stay in registers, CK atoms' x and dy pass through LDS.  The hidden values are
+// formed with the atoms as rows, which is tile order for the contraction over atoms:
+//   dWg[hid][c] += dzg^T x,  dWu[hid][c] += dzu^T x,  dWd[c][hid] += dy^T h,
+// x and dy read transposed from LDS.
+template <class T, int C>
+__global__ __launch_bounds__(256) void k_ffn_dw(FfnArgs A) {
+  using M = MF<T>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + pad_of(sizeof(T));
+  __shared__ __align__(16) T s_x[2][CK * RS];
+  __shared__ __align__(16) T s_d[2][CK * RS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int hw = blockIdx.x * 64 + 16 * wave, hid = hw + i;
+  const bool on = hw < A.hidden;
+  typename M::F fg[NC], fu[NC], fd[NC];
+  if (on) {
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch) {
+      const int c0 = ch * CK + EV * g;
+      fg[ch] = *(const typename M::F*)((const T*)A.wg + (int64_t)hid * C + c0);
+      fu[ch] = *(const typename M::F*)((const T*)A.wu + (int64_t)hid * C + c0);
+      T t[EV];
+#pragma unroll
+      for (int j = 0; j < EV; ++j) t[j] = ((const T*)A.wd)[(int64_t)(c0 + j) * A.hidden + hid];
+      fd[ch] = __builtin_bit_cast(typename M::F, t);
+    }
+  }
+  f4 ag[C / 16], au[C / 16], ad[C / 16];
+#pragma unroll
+  for (int ct = 0; ct < C / 16; ++ct) ag[ct] = au[ct] = ad[ct] = f4{0.f, 0.f, 0.f, 0.f};
+  const int64_t r0 = (int64_t)blockIdx.y * A.rows_per_split, r1 = min(A.n, r0 + A.rows_per_split);
+  Tile<T, CK, C, RS, 256> tx, td;
+  auto fetch = [&](int64_t r) {
+    const int rows = (int)min<int64_t>(CK, r1 - r);
+    tx.fetch((const T*)A.x + r * A.ldx, A.ldx, rows, threadIdx.x);
+    td.fetch((const T*)A.dy + r * A.ldy, A.ldy, rows, threadIdx.x);
+  };
+  if (r0 < r1) {
+    fetch(r0);
+    tx.put(s_x[0], threadIdx.x);
+    td.put(s_d[0], threadIdx.x);
+  }
+  __syncthreads();
+  int b = 0;
+  for (int64_t r = r0; r < r1; r += CK, b ^= 1) {
+    if (r + CK < r1) fetch(r + CK);
+    if (on) {
+      const T *xs = s_x[b], *ds = s_d[b];
+      f4 h[NT], zg[NT], zu[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        f4 dh = f4{0.f, 0.f, 0.f, 0.f};
+        zg[t] = zu[t] = dh;
+        const int row = (16 * t + i) * RS + EV * g;
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+          const typename M::F fx = *(const typename M::F*)(xs + row + ch * CK);
+          const typename M::F fy = *(const typename M::F*)(ds + row + ch * CK);
+          zg[t] = M::mma(zg[t], fx, fg[ch]);
+          zu[t] = M::mma(zu[t], fx, fu[ch]);
+          dh = M::mma(dh, fy, fd[ch]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float a, c, e;
+          hidden_grad(zg[t][q], zu[t][q], dh[q], A.ab, e, a, c);
+          h[t][q] = e;
+          zg[t][q] = a;
+          zu[t][q] = c;
+        }
+      }
+      const typename M::F ph = M::pack(h), pg = M::pack(zg), pu = M::pack(zu);
+#pragma unroll
+      for (int ct = 0; ct < C / 16; ++ct) {
+        const typename M::F fx = ldt<RS>(xs, 0, 16 * ct, lane), fy = ldt<RS>(ds, 0, 16 * ct, lane);
+        ag[ct] = M::mma(ag[ct], pg, fx);
+        au[ct] = M::mma(au[ct], pu, fx);
+        ad[ct] = M::mma(ad[ct], fy, ph);
+      }
+    }
+    if (r + CK < r1) {
+      tx.put(s_x[b ^ 1], threadIdx.x);
+      td.put(s_d[b ^ 1], threadIdx.x);
+    }
+    __syncthreads();
+  }
+  if (!on) return;
+  float* p = A.part + (int64_t)blockIdx.y * 3 * C * A.hidden;
+  float* pu = p + (int64_t)C * A.hidden;
+  float* pd = pu + (int64_t)C * A.hidden;
+#pragma unroll
+  for (int ct = 0; ct < C / 16; ++ct)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      p[(int64_t)(hw + 4 * g + q) * C + 16 * ct + i] = ag[ct][q];
+      pu[(int64_t)(hw + 4 * g + q) * C + 16 * ct + i] = au[ct][q];
+      pd[(int64_t)(16 * ct + 4 * g + q) * A.hidden + hid] = ad[ct][q];
+    }
+}
+
+// Splits of the rows for the weight gradients: about 512 blocks in all, each with at least
+// 128 rows (a split costs three partial matrices written and read once)
+int64_t ffn_splits(int64_t n, int hidden) {
+  const int64_t nb = cdiv(hidden, 64);
+  return std::max<int64_t>(1, std::min<int64_t>(512 / nb, cdiv(n, 128)));
+}
+
+template <class T, int C>
+int launch_ffn_c(FfnArgs A, int what, hipStream_t st) {
+  constexpr int AT = sizeof(T) == 2 ? 2 : 1;
+  constexpr size_t lds = 2 * Chunk<T, C>::SIZE * sizeof(T);
+  static_assert(lds <= 65536, "two weight chunks in LDS");
+  if (what == 2) {
+    const int64_t S = ffn_splits(A.n, A.hidden);
+    A.rows_per_split = cdiv(cdiv(A.n, S), MF<T>::CK) * MF<T>::CK;
+    k_ffn_dw<T, C><<<dim3((unsigned)cdiv(A.hidden, 64), (unsigned)S), 256, 0, st>>>(A);
+  } else {
+    const bool few = cdiv(A.n, 64 * AT) < 256;
+    const unsigned blocks = (unsigned)cdiv(A.n, few ? 64 : 64 * AT);
+    if (what == 0) {
+      if (few)
+        k_ffn<T, C, 1><<<blocks, 256, lds, st>>>(A);
+      else
+        k_ffn<T, C, AT><<<blocks, 256, lds, st>>>(A);
+    } else {
+      if (few)
+        k_ffn_dx<T, C, 1><<<blocks, 256, lds, st>>>(A);
+      else
+        k_ffn_dx<T, C, AT><<<blocks, 256, lds, st>>>(A);
+    }
+  }
+  MP_CHECK_LAUNCH();
+  return MP_OK;
+}
+
+int launch_ffn(const FfnArgs& A, int C, bool bf16, int what, hipStream_t st) {
+  if (bf16) switch (C) {
+      case 32: return launch_ffn_c<uint16_t, 32>(A, what, st);
+      case 64: return launch_ffn_c<uint16_t, 64>(A, what, st);
+      default: return launch_ffn_c<uint16_t, 128>(A, what, st);
+    }
+  switch (C) {
+    case 16: return launch_ffn_c<float, 16>(A, what, st);
+    case 32: return launch_ffn_c<float, 32>(A, what, st);
+    case 64: return launch_ffn_c<float, 64>(A, what, st);
+    default: return launch_ffn_c<float, 128>(A, what, st);
+  }
+}
+
+int check_ffn(const char* who, int32_t n, int32_t channels, int32_t hidden, int32_t dt, int32_t act) {
+  MP_TRY(check_width(who, channels, dt));
+  if (n < 0) return arg_error(std::string(who) + ": n must be >= 0");
+  if (hidden < 32 || hidden > 4096 || hidden % 32)
+    return arg_error(std::string(who) + ": hidden must be a multiple of 32 in 32..4096");
+  if (act != MP_ACT_SILU && act != MP_ACT_SIGMOID) return arg_error(std::string(who) + ": act must be SiLU or sigmoid");
+  return MP_OK;
+}
+
+FfnArgs ffn_args(int32_t n, int32_t hidden, int32_t act, const void* x, int64_t ldx, const void* wg, const void* wu,
+                 const void* wd) {
+  FfnArgs A{};
+  A.n = n, A.hidden = hidden;
+  A.ab = act == MP_ACT_SILU ? ActAB{1.f, 0.f} : ActAB{0.f, 1.f};
+  A.x = x, A.ldx = ldx, A.wg = wg, A.wu = wu, A.wd = wd;
+  return A;
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace mdmp
+
+using namespace mdmp;
+
+extern "C" int mp_gated_ffn(int32_t n, int32_t channels, int32_t hidden, int32_t dt, int32_t act, const void* x,
+                            int64_t ldx, const void* wg, const void* wu, const void* wd, const void* residual,
+                            int64_t ldr, void* y, int64_t ldy, hipStream_t st) {
+  MP_TRY(ops::check_ffn("mp_gated_ffn", n, channels, hidden, dt, act));
+  if (n == 0) return MP_OK;
+  if (!x || !wg || !wu || !wd || !y) return arg_error("mp_gated_ffn: null x, weights or y");
+  if (((uintptr_t)wg | (uintptr_t)wu | (uintptr_t)wd) & 15)
+    return arg_error("mp_gated_ffn: weights must be 16-byte aligned");
+  MP_ROWS("mp_gated_ffn", "x", x, ldx, channels, dt);
+  MP_ROWS("mp_gated_ffn", "y", y, ldy, channels, dt);
+  if (residual) MP_ROWS("mp_gated_ffn", "residual", residual, ldr, channels, dt);
+  ops::FfnArgs A = ops::ffn_args(n, hidden, act, x, ldx, wg, wu, wd);
+  A.res = residual, A.ldr = ldr, A.y = y, A.ldy = ldy;
+  ProfScope p("gated_ffn", st);
+  return ops::launch_ffn(A, channels, dt == 1, 0, st);
+}
+
+extern "C" int mp_gated_ffn_bwd_ws(int32_t n, int32_t channels, int32_t hidden, int32_t dt, size_t* bytes) {
+  MP_TRY(ops::check_ffn("mp_gated_ffn_bwd_ws", n, channels, hidden, dt, MP_ACT_SILU));
+  if (!bytes) return arg_error("mp_gated_ffn_bwd_ws: null bytes");
+  *bytes = align_up(sizeof(float) * 3 * (size_t)channels * hidden * ops::ffn_splits(n, hidden));
+  return MP_OK;
+}
+
+extern "C" int mp_gated_ffn_bwd(int32_t n, int32_t channels, int32_t hidden, int32_t dt, int32_t act, const void* x,
+                                int64_t ldx, const void* wg, const void* wu, const void* wd, const void* dy,
+                                int64_t lddy, void* dx, int64_t lddx, void* dwg, void* dwu, void* dwd, void* ws,
+                                size_t ws_bytes, hipStream_t st) {
+  MP_TRY(ops::check_ffn("mp_gated_ffn_bwd", n, channels, hidden, dt, act));
+  const bool grads = dwg || dwu || dwd;
+  if (grads && !(dwg && dwu && dwd)) return arg_error("mp_gated_ffn_bwd: give all three weight gradients or none");
+  if (n > 0) {
+    if (!x || !wg || !wu || !wd || !dy) return arg_error("mp_gated_ffn_bwd: null x, weights or dy");
+    if (((uintptr_t)wg | (uintptr_t)wu | (uintptr_t)wd) & 15)
+      return arg_error("mp_gated_ffn_bwd: weights must be 16-byte aligned");
+    MP_ROWS("mp_gated_ffn_bwd", "x", x, ldx, channels, dt);
+    MP_ROWS("mp_gated_ffn_bwd", "dy", dy, lddy, channels, dt);
+    if (dx) MP_ROWS("mp_gated_ffn_bwd", "dx", dx, lddx, channels, dt);
+  }
+  ops::FfnArgs A = ops::ffn_args(n, hidden, act, x, ldx, wg, wu, wd);
+  A.dy = dy, A.ldy = lddy, A.dx = dx, A.lddx = lddx;
+  if (grads) {
+    size_t need = 0;
+    MP_TRY(mp_gated_ffn_bwd_ws(n, channels, hidden, dt, &need));
+    if (!ws || ((uintptr_t)ws & 15)) return arg_error("mp_gated_ffn_bwd: workspace null or not 16-byte aligned");
+    if (ws_bytes < need) return arg_error("mp_gated_ffn_bwd: workspace too small");
+    A.part = (float*)ws;
+  }
+  ProfScope p("gated_ffn_bwd", st);
+  if (n > 0 && dx) MP_TRY(ops::launch_ffn(A, channels, dt == 1, 1, st));
+  if (!grads) return MP_OK;
+  if (n > 0) MP_TRY(ops::launch_ffn(A, channels, dt == 1, 2, st));
+  const int64_t S = n > 0 ? ops::ffn_splits(n, hidden) : 0, N = (int64_t)channels * hidden;
+  void* out[3] = {dwg, dwu, dwd};
+  for (int k = 0; k < 3; ++k) MP_TRY(ops::reduce_rows(A.part + k * N, S, N, 3 * N, out[k], dt == 1, st));
+  return MP_OK;
+}

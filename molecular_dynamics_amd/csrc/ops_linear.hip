@@ -1,0 +1,405 @@
+// y = residual + act(x W^T + bias) on atom rows, and its gradients.
+#include "ops_api.hpp"
+
+namespace mdmp {
+namespace ops {
+namespace {
+
+struct LinArgs {
+  int64_t n, ldx, ldr, ldy, lddx;  // ldy: stride of y (forward) or dy (backward)
+  int out;
+  bool act;
+  ActAB ab;
+  const void *x, *w, *res, *dy;
+  const float* bias;
+  void *y, *dx;
+  float *part, *part_b;  // [splits][out][C], [splits][out]
+  int64_t rows_per_split;
+};
+
+constexpr int PADE(int esize) { return 16 / esize; }
+
+// Forward: D[o][a] = sum_c W[o][c] x[a][c].  A wave keeps the rows of 16 AT atoms in registers
+// as one operand and walks the outputs CK at a time, the other operand read straight from W
+// (at most 256 KB, so L1/L2 hold it).  W's rows are taken in the order nat_row, which leaves
+// EV consecutive outputs of an atom in each lane: bias, activation, residual and the 16-byte
+// stores follow without an exchange.  gridDim.y splits the outputs when there are few rows.
+// Bound: HBM (the y rows).
+template <class T, int C, int AT>
+__global__ __launch_bounds__(256) void k_linear(LinArgs A) {
+  using M = MF<T>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int64_t a0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
+  if (a0 >= A.n) return;
+  typename M::F xf[AT][NC];
+#pragma unroll
+  for (int at = 0; at < AT; ++at) {
+    const int64_t a = a0 + 16 * at + i;
+    const T* p = (const T*)A.x + a * A.ldx + EV * g;
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch) xf[at][ch] = ld16<typename M::F>(p + ch * M::CK, a < A.n);
+  }
+  const int ngr = (A.out + OG - 1) / OG;
+  const int per = (ngr + gridDim.y - 1) / gridDim.y;
+  const int g0 = blockIdx.y * per, g1 = min(ngr, g0 + per);
+  for (int og = g0; og < g1; ++og) {
+    const int o0 = og * OG, oe = o0 + EV * g;
+    f4 acc[AT][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = min(o0 + nat_row<T>(t, i), A.out - 1);
+      const T* wp = (const T*)A.w + (int64_t)row * C + EV * g;
+      typename M::F wf[NC];
+#pragma unroll
+      for (int ch = 0; ch < NC; ++ch) wf[ch] = *(const typename M::F*)(wp + ch * M::CK);
+#pragma unroll
+      for (int at = 0; at < AT; ++at) {
+        f4 s = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) s = M::mma(s, wf[ch], xf[at][ch]);
+        acc[at][t] = s;
+      }
+    }
+    if (oe >= A.out) continue;
+    if (A.bias) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const f4 b = f4{A.bias[oe + 4 * t], A.bias[oe + 4 * t + 1], A.bias[oe + 4 * t + 2], A.bias[oe + 4 * t + 3]};
+#pragma unroll
+        for (int at = 0; at < AT; ++at) acc[at][t] += b;
+      }
+    }
+    if (A.act) {
+#pragma unroll
+      for (int at = 0; at < AT; ++at)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[at][t][r] = act_val(acc[at][t][r], A.ab);
+    }
+#pragma unroll
+    for (int at = 0; at < AT; ++at) {
+      const int64_t a = a0 + 16 * at + i;
+      if (a >= A.n) continue;
+      if (A.res) {
+        f4 q[NT];
+        M::unpack(*(const typename M::F*)((const T*)A.res + a * A.ldr + oe), q);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[at][t] += q[t];
+      }
+      st_row<T>((T*)A.y + a * A.ldy + oe, acc[at]);
+    }
+  }
+}
+
+// dx: D[c][a] = sum_o W[o][c] dz[a][o], dz = dy act'(z), z formed again by the forward's
+// product.  Both operands of dz sit as EV consecutive outputs per lane (natural order), so
+// dz goes from result to operand in registers.  W passes through LDS CK rows at a time,
+// read there by rows (z) and transposed (dx).  Bound: HBM (dy rows) without an activation.
+template <class T, int C, int AT>
+__global__ __launch_bounds__(256) void k_linear_dx(LinArgs A) {
+  using M = MF<T>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK, RS = C + PADE(sizeof(T)), NG = C / M::CK;
+  __shared__ __align__(16) T s_w[2][OG * RS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int64_t a0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
+  typename M::F xf[AT][NC];
+  if (A.act) {
+#pragma unroll
+    for (int at = 0; at < AT; ++at) {
+      const int64_t a = a0 + 16 * at + i;
+      const T* p = (const T*)A.x + a * A.ldx + EV * g;
+#pragma unroll
+      for (int ch = 0; ch < NC; ++ch) xf[at][ch] = ld16<typename M::F>(p + ch * M::CK, a < A.n);
+    }
+  }
+  f4 dx[AT][NG][NT];
+#pragma unroll
+  for (int at = 0; at < AT; ++at)
+#pragma unroll
+    for (int p = 0; p < NG; ++p)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) dx[at][p][t] = f4{0.f, 0.f, 0.f, 0.f};
+  const int ngr = (A.out + OG - 1) / OG;
+  Tile<T, OG, C, RS, 256> tw;
+  tw.fetch((const T*)A.w, C, A.out, threadIdx.x);
+  tw.put(s_w[0], threadIdx.x);
+  __syncthreads();
+  for (int og = 0; og < ngr; ++og) {
+    const int o0 = og * OG, oe = o0 + EV * g;
+    const T* w = s_w[og & 1];
+    if (og + 1 < ngr) tw.fetch((const T*)A.w + (int64_t)(o0 + OG) * C, C, A.out - o0 - OG, threadIdx.x);
+    typename M::F dz[AT];
+#pragma unroll
+    for (int at = 0; at < AT; ++at) {
+      const int64_t a = a0 + 16 * at + i;
+      dz[at] = ld16<typename M::F>((const T*)A.dy + a * A.ldy + oe, a < A.n && oe < A.out);
+    }
+    if (A.act) {
+#pragma unroll
+      for (int at = 0; at < AT; ++at) {
+        f4 z[NT], d[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          z[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ch = 0; ch < NC; ++ch)
+            z[t] = M::mma(z[t], *(const typename M::F*)(w + nat_row<T>(t, i) * RS + ch * M::CK + EV * g), xf[at][ch]);
+        }
+        M::unpack(dz[at], d);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float b = A.bias && oe < A.out ? A.bias[oe + 4 * t + r] : 0.f;
+            float v, e;
+            act_both(z[t][r] + b, A.ab, v, e);
+            d[t][r] *= e;
+          }
+        dz[at] = M::pack(d);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < NG; ++p)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const typename M::F wt = ldtn_nat<RS>(w, 0, p, t, lane);
+#pragma unroll
+        for (int at = 0; at < AT; ++at) dx[at][p][t] = M::mma(dx[at][p][t], wt, dz[at]);
+      }
+    if (og + 1 < ngr) tw.put(s_w[(og + 1) & 1], threadIdx.x);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int at = 0; at < AT; ++at) {
+    const int64_t a = a0 + 16 * at + i;
+    if (a >= A.n) continue;
+#pragma unroll
+    for (int p = 0; p < NG; ++p) st_row<T>((T*)A.dx + a * A.lddx + p * M::CK + EV * g, dx[at][p]);
+  }
+}
+
+// dW, dbias: D[o][c] = sum_a dz[a][o] x[a][c] over one split of the rows.  A wave owns 16
+// outputs and all C channels; CK atoms at a time pass through LDS.  z is formed with the
+// atoms as rows, which is tile order for the contraction over atoms, the order in which dy
+// and x are read transposed.  Each split writes its own partial, added up in split order.
+// Bound: HBM (x and dy rows).
+template <class T, int C>
+__global__ __launch_bounds__(256) void k_linear_dw(LinArgs A) {
+  using M = MF<T>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + PADE(sizeof(T));
+  constexpr int OB = 64, RO = OB + PADE(sizeof(T));
+  __shared__ __align__(16) T s_x[2][CK * RS];
+  __shared__ __align__(16) T s_d[2][CK * RO];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int ob = blockIdx.x * OB, o = ob + 16 * wave + i;
+  const bool on = ob + 16 * wave < A.out;
+  typename M::F wf[NC];
+  float bias = 0.f, db = 0.f;
+  if (on && A.act) {
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch)
+      wf[ch] = *(const typename M::F*)((const T*)A.w + (int64_t)o * C + ch * CK + EV * g);
+    if (A.bias) bias = A.bias[o];
+  }
+  f4 acc[C / 16];
+#pragma unroll
+  for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
+  const int64_t r0 = (int64_t)blockIdx.y * A.rows_per_split, r1 = min(A.n, r0 + A.rows_per_split);
+  Tile<T, CK, C, RS, 256> tx;
+  // the block's 64 columns of dy; columns past the last output read as zeros
+  constexpr int VPD = OB / EV, ITD = (CK * VPD + 255) / 256;
+  u4 vd[ITD];
+  auto fetch = [&](int64_t r) {
+    tx.fetch((const T*)A.x + r * A.ldx, A.ldx, (int)min<int64_t>(CK, r1 - r), threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < ITD; ++k) {
+      const int x = threadIdx.x + k * 256, rr = x / VPD, c = (x % VPD) * EV;
+      vd[k] = ld16<u4>((const T*)A.dy + (r + rr) * A.ldy + ob + c, x < CK * VPD && r + rr < r1 && ob + c < A.out);
+    }
+  };
+  auto put = [&](int b) {
+    tx.put(s_x[b], threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < ITD; ++k) {
+      const int x = threadIdx.x + k * 256, rr = x / VPD, c = (x % VPD) * EV;
+      if (x < CK * VPD) *(u4*)(s_d[b] + rr * RO + c) = vd[k];
+    }
+  };
+  if (r0 < r1) {
+    fetch(r0);
+    put(0);
+  }
+  __syncthreads();
+  int b = 0;
+  for (int64_t r = r0; r < r1; r += CK, b ^= 1) {
+    if (r + CK < r1) fetch(r + CK);
+    if (on) {
+      const T *xs = s_x[b], *ds = s_d[b];
+      typename M::F dz = ldt<RO>(ds, 0, 16 * wave, lane);
+      f4 d[NT];
+      M::unpack(dz, d);
+      if (A.act) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          f4 z = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ch = 0; ch < NC; ++ch)
+            z = M::mma(z, *(const typename M::F*)(xs + (16 * t + i) * RS + ch * CK + EV * g), wf[ch]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v, e;
+            act_both(z[q] + bias, A.ab, v, e);
+            d[t][q] *= e;
+          }
+        }
+        dz = M::pack(d);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) db += (d[t].x + d[t].y) + (d[t].z + d[t].w);
+#pragma unroll
+      for (int ct = 0; ct < C / 16; ++ct) acc[ct] = M::mma(acc[ct], dz, ldt<RS>(xs, 0, 16 * ct, lane));
+    }
+    if (r + CK < r1) put(b ^ 1);
+    __syncthreads();
+  }
+  if (!on) return;
+  float* p = A.part + ((int64_t)blockIdx.y * A.out + ob + 16 * wave) * C;
+#pragma unroll
+  for (int ct = 0; ct < C / 16; ++ct)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) p[(4 * g + q) * C + 16 * ct + i] = acc[ct][q];
+  db = gsum(db);
+  if (g == 0) A.part_b[(int64_t)blockIdx.y * A.out + o] = db;
+}
+
+// Splits of the rows for dW: about 512 blocks in all, each with at least 128 rows (a split
+// costs a partial matrix written and read once)
+int64_t dw_splits(int64_t n, int out) {
+  const int64_t nb = cdiv(out, 64);
+  return std::max<int64_t>(1, std::min<int64_t>(512 / nb, cdiv(n, 128)));
+}
+
+template <class T>
+int launch_linear(const LinArgs& A0, int C, int what, hipStream_t st) {
+  LinArgs A = A0;
+  constexpr int AT = sizeof(T) == 2 ? 2 : 1;
+  const int ngr = (int)cdiv(A.out, MF<T>::CK);
+  // few rows: one 16-atom tile per wave and the outputs split over gridDim.y
+  const bool few = cdiv(A.n, 64 * AT) < 512;
+  const int64_t bx = few ? cdiv(A.n, 64) : cdiv(A.n, 64 * AT);
+  const int by = (int)std::max<int64_t>(1, std::min<int64_t>(ngr, 512 / bx));
+  const int64_t S = dw_splits(A.n, A.out);
+  A.rows_per_split = cdiv(cdiv(A.n, S), MF<T>::CK) * MF<T>::CK;
+#define MP_CASE(CC)                                                                         \
+  case CC:                                                                                  \
+    if (what == 0) {                                                                        \
+      if (few)                                                                              \
+        k_linear<T, CC, 1><<<dim3((unsigned)bx, by), 256, 0, st>>>(A);                      \
+      else                                                                                  \
+        k_linear<T, CC, AT><<<dim3((unsigned)bx, by), 256, 0, st>>>(A);                     \
+    } else if (what == 1) {                                                                 \
+      k_linear_dx<T, CC, 1><<<(unsigned)cdiv(A.n, 64), 256, 0, st>>>(A);                    \
+    } else {                                                                                \
+      k_linear_dw<T, CC><<<dim3((unsigned)cdiv(A.out, 64), (unsigned)S), 256, 0, st>>>(A);  \
+    }                                                                                       \
+    break;
+  switch (C) {
+    MP_CASE(32)
+    MP_CASE(64)
+    MP_CASE(128)
+    default:
+      if constexpr (sizeof(T) == 4) {
+        switch (C) { MP_CASE(16) }
+      }
+  }
+#undef MP_CASE
+  MP_CHECK_LAUNCH();
+  return MP_OK;
+}
+
+int check_linear(const char* who, int32_t n, int32_t in, int32_t out, int32_t dt, int32_t act) {
+  MP_TRY(check_width(who, in, dt));
+  if (n < 0) return arg_error(std::string(who) + ": n must be >= 0");
+  if (out < 16 || out > 1024 || out % 16) return arg_error(std::string(who) + ": out must be a multiple of 16 in 16..1024");
+  if (act < MP_ACT_NONE || act > MP_ACT_SIGMOID) return arg_error(std::string(who) + ": unknown activation");
+  return MP_OK;
+}
+
+LinArgs lin_args(int32_t n, int32_t out, int32_t act, const void* x, int64_t ldx, const void* w, const float* bias) {
+  LinArgs A{};
+  A.n = n, A.out = out;
+  A.act = act != MP_ACT_NONE;
+  A.ab = act == MP_ACT_SILU ? ActAB{1.f, 0.f} : ActAB{0.f, 1.f};
+  A.x = x, A.ldx = ldx, A.w = w, A.bias = bias;
+  return A;
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace mdmp
+
+using namespace mdmp;
+
+extern "C" int mp_linear(int32_t n, int32_t in, int32_t out, int32_t dt, int32_t act, const void* x, int64_t ldx,
+                         const void* w, const float* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                         hipStream_t st) {
+  MP_TRY(ops::check_linear("mp_linear", n, in, out, dt, act));
+  if (n == 0) return MP_OK;
+  if (!x || !w || !y) return arg_error("mp_linear: null x, w or y");
+  if ((uintptr_t)w & 15) return arg_error("mp_linear: w must be 16-byte aligned");
+  MP_ROWS("mp_linear", "x", x, ldx, in, dt);
+  MP_ROWS("mp_linear", "y", y, ldy, out, dt);
+  if (residual) MP_ROWS("mp_linear", "residual", residual, ldr, out, dt);
+  ops::LinArgs A = ops::lin_args(n, out, act, x, ldx, w, bias);
+  A.res = residual, A.ldr = ldr, A.y = y, A.ldy = ldy;
+  ProfScope p("linear", st);
+  return dt == 1 ? ops::launch_linear<uint16_t>(A, in, 0, st) : ops::launch_linear<float>(A, in, 0, st);
+}
+
+extern "C" int mp_linear_bwd_ws(int32_t n, int32_t in, int32_t out, int32_t dt, size_t* bytes) {
+  MP_TRY(ops::check_linear("mp_linear_bwd_ws", n, in, out, dt, 0));
+  if (!bytes) return arg_error("mp_linear_bwd_ws: null bytes");
+  const int64_t S = ops::dw_splits(n, out);
+  Arena a(nullptr, 0, true);
+  a.take<float>(S * out * in);
+  a.take<float>(S * out);
+  *bytes = a.off;
+  return MP_OK;
+}
+
+extern "C" int mp_linear_bwd(int32_t n, int32_t in, int32_t out, int32_t dt, int32_t act, const void* x, int64_t ldx,
+                             const void* w, const float* bias, const void* dy, int64_t lddy, void* dx, int64_t lddx,
+                             void* dw, float* dbias, void* ws, size_t ws_bytes, hipStream_t st) {
+  MP_TRY(ops::check_linear("mp_linear_bwd", n, in, out, dt, act));
+  if (n > 0) {
+    if (!x || !w || !dy) return arg_error("mp_linear_bwd: null x, w or dy");
+    if ((uintptr_t)w & 15) return arg_error("mp_linear_bwd: w must be 16-byte aligned");
+    MP_ROWS("mp_linear_bwd", "x", x, ldx, in, dt);
+    MP_ROWS("mp_linear_bwd", "dy", dy, lddy, out, dt);
+    if (dx) MP_ROWS("mp_linear_bwd", "dx", dx, lddx, in, dt);
+  }
+  ops::LinArgs A = ops::lin_args(n, out, act, x, ldx, w, bias);
+  A.dy = dy, A.ldy = lddy, A.dx = dx, A.lddx = lddx;
+  int64_t S = 0;
+  if (dw || dbias) {
+    if (!ws || ((uintptr_t)ws & 15)) return arg_error("mp_linear_bwd: workspace null or not 16-byte aligned");
+    Arena a(ws, ws_bytes);
+    S = ops::dw_splits(n, out);
+    A.part = a.take<float>(S * out * in);
+    A.part_b = a.take<float>(S * out);
+    if (!a.ok()) return arg_error("mp_linear_bwd: workspace too small");
+  }
+  ProfScope p("linear_bwd", st);
+  auto go = [&](int what) {
+    return dt == 1 ? ops::launch_linear<uint16_t>(A, in, what, st) : ops::launch_linear<float>(A, in, what, st);
+  };
+  if (n > 0 && dx) MP_TRY(go(1));
+  if (!A.part) return MP_OK;
+  if (n > 0) MP_TRY(go(2));
+  if (n == 0) S = 0;  // no rows: sums over nothing, zeros
+  if (dw) MP_TRY(ops::reduce_rows(A.part, S, (int64_t)out * in, (int64_t)out * in, dw, dt == 1, st));
+  if (dbias) MP_TRY(ops::reduce_rows(A.part_b, S, out, out, dbias, false, st));
+  return MP_OK;
+}

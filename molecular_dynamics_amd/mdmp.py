@@ -37,6 +37,10 @@ EXPORTS = ["mp_version", "mp_last_error", "mp_model_num_weights", "mp_model_crea
            "mp_heads_destroy", "mp_energy_forces_heads", "mp_md_create",
            "mp_md_set_state", "mp_md_step", "mp_md_use_graphs", "mp_md_set_langevin", "mp_md_step_nvt",
            "mp_md_get_state", "mp_md_destroy",
+           "mp_linear", "mp_linear_bwd_ws", "mp_linear_bwd", "mp_gated_ffn", "mp_gated_ffn_bwd_ws",
+           "mp_gated_ffn_bwd", "mp_norm_block", "mp_norm_block_bwd_ws", "mp_norm_block_bwd",
+           "mp_structure_attention_saved", "mp_structure_attention", "mp_structure_attention_bwd_ws",
+           "mp_structure_attention_bwd",
            "mp_profile_enable",
            "mp_profile_reset", "mp_profile_read"]
 
@@ -58,6 +62,22 @@ class mp_graph(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("box_L", ctypes.c_float), ("pos", ctypes.c_void_p),
                 ("species", ctypes.c_void_p), ("row_ptr", ctypes.c_void_p), ("col", ctypes.c_void_p),
                 ("rev", ctypes.c_void_p), ("n_edges", ctypes.c_int64)]
+
+
+class mp_norm_args(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("channels", ctypes.c_int32), ("feat_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("b", ctypes.c_void_p),
+                ("ldb", ctypes.c_int64), ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p)]
+
+
+class mp_attention_args(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("n_struct", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("feat_dtype", ctypes.c_int32), ("cap", ctypes.c_float),
+                ("box_L", ctypes.c_float), ("struct_ptr", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("slope", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("ldq", ctypes.c_int64), ("k", ctypes.c_void_p), ("ldk", ctypes.c_int64), ("v", ctypes.c_void_p),
+                ("ldv", ctypes.c_int64)]
 
 
 _vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -96,6 +116,24 @@ _sig = {
     "mp_md_step_nvt": ([_vp, _i32, _vp, _vp, _vp], ctypes.c_int),
     "mp_md_get_state": ([_vp, _vp, _vp, _P(_i64), _P(_i32), _P(_i32), _P(_f32), _vp], ctypes.c_int),
     "mp_md_destroy": ([_vp], ctypes.c_int),
+    "mp_linear": ([_i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp], ctypes.c_int),
+    "mp_linear_bwd_ws": ([_i32, _i32, _i32, _i32, _P(_sz)], ctypes.c_int),
+    "mp_linear_bwd": ([_i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _sz,
+                       _vp], ctypes.c_int),
+    "mp_gated_ffn": ([_i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp],
+                     ctypes.c_int),
+    "mp_gated_ffn_bwd_ws": ([_i32, _i32, _i32, _i32, _P(_sz)], ctypes.c_int),
+    "mp_gated_ffn_bwd": ([_i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                          _vp, _vp, _sz, _vp], ctypes.c_int),
+    "mp_norm_block": ([_P(mp_norm_args), _vp, _i64, _vp, _i64, _vp], ctypes.c_int),
+    "mp_norm_block_bwd_ws": ([_i32, _i32, _i32, _P(_sz)], ctypes.c_int),
+    "mp_norm_block_bwd": ([_P(mp_norm_args), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                           _vp, _sz, _vp], ctypes.c_int),
+    "mp_structure_attention_saved": ([_i32, _i32, _i32, _i32, _P(_i64)], ctypes.c_int),
+    "mp_structure_attention": ([_P(mp_attention_args), _vp, _i64, _vp, _vp], ctypes.c_int),
+    "mp_structure_attention_bwd_ws": ([_i32, _i32, _i32, _i32, _P(_sz)], ctypes.c_int),
+    "mp_structure_attention_bwd": ([_P(mp_attention_args), _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                    _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     "mp_profile_enable": ([ctypes.c_int], ctypes.c_int),
     "mp_profile_reset": ([], ctypes.c_int),
     "mp_profile_read": ([ctypes.c_char_p, _P(ctypes.c_double), _P(_i64)], ctypes.c_int),
@@ -377,6 +415,254 @@ def energy_forces_heads(model, heads, g, perm=None, ws=None):
            "mp_energy_forces_heads")
     _check(_lib.mp_energy_forces_status(_ptr(ws), _stream()), "mp_energy_forces_status")
     return e_heads, float(energy.item()), forces, e_atoms
+
+
+# ---------------------------------------------------------------- block operators
+# Rows are 2-d cuda tensors of float32 or bfloat16 (torch.bfloat16, or its bits as int16, as in
+# feat_dtype), unit stride in the second dimension and any row stride of a multiple of 16 bytes:
+# h[:, 0] of a feature tensor [n, K, C] is such a matrix.  Outputs are of the rows' dtype unless
+# said otherwise, allocated here when not given.  All calls enqueue on the current stream.
+
+ACTS = {"none": 0, "silu": 1, "sigmoid": 2}  # MP_ACT_* of mdmp.h
+
+
+def _need(ok, where, what):
+    if not ok:
+        raise ValueError(f"{where}: {what}")
+
+
+def _rows(where, name, t, n=None, width=None, like=None):
+    """(pointer, row stride) of a matrix of rows, checked."""
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2, where, f"{name} must be a 2-d cuda tensor")
+    _need(t.device.index == torch.cuda.current_device(), where, f"{name} must be on the current device")
+    _need(t.dtype in (torch.float32, torch.bfloat16, torch.int16), where, f"{name} must be float32 or bfloat16")
+    rows, cols = t.shape
+    if like is not None:
+        _need(t.dtype == like.dtype, where, f"{name} must have the dtype of the other rows")
+    _need(n is None or rows == n, where, f"{name} must have {n} rows")
+    _need(width is None or cols == width, where, f"{name} must have {width} columns")
+    s0, s1 = t.stride()
+    _need(s1 == 1 or cols == 1, where, f"{name} must have unit stride along a row")
+    return t.data_ptr(), (s0 if rows > 1 else max(s0, cols) if (s0 * t.element_size()) % 16 == 0 else cols)
+
+
+def _vec(where, name, t, size, dtype=None):
+    """pointer of a contiguous float32 (or given dtype) device array, None allowed."""
+    import torch
+    if t is None:
+        return None
+    _need(t.is_cuda and t.device.index == torch.cuda.current_device() and t.is_contiguous(), where,
+          f"{name} must be a contiguous tensor on the current device")
+    _need(t.dtype == (dtype or torch.float32), where, f"{name} must be {dtype or torch.float32}")
+    _need(tuple(t.shape) == tuple(size), where, f"{name} must have shape {tuple(size)}")
+    return t.data_ptr()
+
+
+def _is_bf16(t):
+    import torch
+    return 0 if t.dtype == torch.float32 else 1
+
+
+def _new_rows(n, width, like):
+    import torch
+    return torch.empty(n, width, dtype=like.dtype, device=like.device)
+
+
+def _wsbytes(fn, where, *args):
+    nbytes = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(nbytes)), where)
+    return nbytes.value
+
+
+def _act_id(where, act):
+    _need(act in ACTS, where, f"unknown activation {act!r}")
+    return ACTS[act]
+
+
+def linear(x, weight, bias=None, act="none", residual=None, out=None):
+    """residual + act(x weight^T + bias): x [n][in], weight [out][in], bias float32 [out] -> [n][out].
+    out may be residual."""
+    n, k = x.shape
+    o = weight.shape[0]
+    xp, ldx = _rows("linear", "x", x)
+    wp = _vec("linear", "weight", weight, (o, k), x.dtype)
+    bp = _vec("linear", "bias", bias, (o,))
+    rp, ldr = _rows("linear", "residual", residual, n, o, x) if residual is not None else (None, 0)
+    out = _new_rows(n, o, x) if out is None else out
+    yp, ldy = _rows("linear", "out", out, n, o, x)
+    _check(_lib.mp_linear(n, k, o, _is_bf16(x), _act_id("linear", act), xp, ldx, wp, bp, rp, ldr, yp, ldy, _stream()),
+           "mp_linear")
+    return out
+
+
+def linear_bwd(x, weight, dy, bias=None, act="none", weight_grads=True):
+    """(dx, dweight, dbias) of linear for dy [n][out]; the residual's gradient is dy.  dbias is
+    float32, None without a bias; without weight_grads (forces only) dweight and dbias are None."""
+    import torch
+    n, k = x.shape
+    o = weight.shape[0]
+    xp, ldx = _rows("linear_bwd", "x", x)
+    wp = _vec("linear_bwd", "weight", weight, (o, k), x.dtype)
+    bp = _vec("linear_bwd", "bias", bias, (o,))
+    dp, ldd = _rows("linear_bwd", "dy", dy, n, o, x)
+    dx = _new_rows(n, k, x)
+    dw = db = ws = None
+    if weight_grads:
+        dw = torch.empty_like(weight)
+        db = torch.empty(o, dtype=torch.float32, device=x.device) if bias is not None else None
+        ws = _ws(_wsbytes(_lib.mp_linear_bwd_ws, "mp_linear_bwd_ws", n, k, o, _is_bf16(x)))
+    _check(_lib.mp_linear_bwd(n, k, o, _is_bf16(x), _act_id("linear_bwd", act), xp, ldx, wp, bp, dp, ldd,
+                              dx.data_ptr(), k, _ptr(dw), _ptr(db), _ptr(ws), ws.numel() if ws is not None else 0,
+                              _stream()), "mp_linear_bwd")
+    return dx, dw, db
+
+
+def gated_ffn(x, w_gate, w_up, w_down, act="silu", residual=None, out=None):
+    """residual + (act(x w_gate^T) * (x w_up^T)) w_down^T: x [n][C], w_gate and w_up [hidden][C],
+    w_down [C][hidden] -> [n][C].  out may be residual."""
+    n, c = x.shape
+    f = w_gate.shape[0]
+    xp, ldx = _rows("gated_ffn", "x", x)
+    w = [_vec("gated_ffn", k, t, s, x.dtype) for k, t, s in
+         (("w_gate", w_gate, (f, c)), ("w_up", w_up, (f, c)), ("w_down", w_down, (c, f)))]
+    rp, ldr = _rows("gated_ffn", "residual", residual, n, c, x) if residual is not None else (None, 0)
+    out = _new_rows(n, c, x) if out is None else out
+    yp, ldy = _rows("gated_ffn", "out", out, n, c, x)
+    _check(_lib.mp_gated_ffn(n, c, f, _is_bf16(x), _act_id("gated_ffn", act), xp, ldx, *w, rp, ldr, yp, ldy,
+                             _stream()), "mp_gated_ffn")
+    return out
+
+
+def gated_ffn_bwd(x, w_gate, w_up, w_down, dy, act="silu", weight_grads=True):
+    """(dx, dw_gate, dw_up, dw_down) of gated_ffn for dy [n][C]; the residual's gradient is dy.
+    Without weight_grads (forces only) the last three are None."""
+    import torch
+    n, c = x.shape
+    f = w_gate.shape[0]
+    xp, ldx = _rows("gated_ffn_bwd", "x", x)
+    w = [_vec("gated_ffn_bwd", k, t, s, x.dtype) for k, t, s in
+         (("w_gate", w_gate, (f, c)), ("w_up", w_up, (f, c)), ("w_down", w_down, (c, f)))]
+    dp, ldd = _rows("gated_ffn_bwd", "dy", dy, n, c, x)
+    dx = _new_rows(n, c, x)
+    g, ws = [None] * 3, None
+    if weight_grads:
+        g = [torch.empty_like(t) for t in (w_gate, w_up, w_down)]
+        ws = _ws(_wsbytes(_lib.mp_gated_ffn_bwd_ws, "mp_gated_ffn_bwd_ws", n, c, f, _is_bf16(x)))
+    _check(_lib.mp_gated_ffn_bwd(n, c, f, _is_bf16(x), _act_id("gated_ffn_bwd", act), xp, ldx, *w, dp, ldd,
+                                 dx.data_ptr(), c, *[_ptr(t) for t in g], _ptr(ws),
+                                 ws.numel() if ws is not None else 0, _stream()), "mp_gated_ffn_bwd")
+    return (dx, *g)
+
+
+def _norm_args(where, x, b, scale, gate, w_post, w_pre, eps):
+    n, c = x.shape
+    xp, ldx = _rows(where, "x", x)
+    bp, ldb = _rows(where, "b", b, n, c, x)
+    gp, ldg = _rows(where, "gate", gate, n, c, x) if gate is not None else (None, 0)
+    return mp_norm_args(n, c, _is_bf16(x), eps, xp, ldx, bp, ldb, gp, ldg, _vec(where, "scale", scale, (c,)),
+                        _vec(where, "w_post", w_post, (c,)), _vec(where, "w_pre", w_pre, (c,)))
+
+
+def norm_block(x, b, scale=None, gate=None, w_post=None, w_pre=None, eps=1e-6, out=None):
+    """(y, u): y = x + scale * sigmoid(gate) * (w_post * b / rms(b)) and u = w_pre * y / rms(y), the
+    norm after a block with its gate and residual scale and the norm before the next block.
+    scale, w_post, w_pre float32 [C] or None (no factor; no norm of b; u = None); gate rows or None.
+    out (for y) may be x or b."""
+    n, c = x.shape
+    a = _norm_args("norm_block", x, b, scale, gate, w_post, w_pre, eps)
+    y = _new_rows(n, c, x) if out is None else out
+    yp, ldy = _rows("norm_block", "out", y, n, c, x)
+    u = _new_rows(n, c, x) if w_pre is not None else None
+    _check(_lib.mp_norm_block(ctypes.byref(a), yp, ldy, _ptr(u), c, _stream()), "mp_norm_block")
+    return y, u
+
+
+def norm_block_bwd(x, b, dy, du=None, scale=None, gate=None, w_post=None, w_pre=None, eps=1e-6, param_grads=True):
+    """Gradients of norm_block for dy and du (either may be None: zero) as a dict: dx, db, dgate
+    (rows) and dscale, dw_post, dw_pre (float32); None for what was not given."""
+    import torch
+    w = "norm_block_bwd"
+    n, c = x.shape
+    a = _norm_args(w, x, b, scale, gate, w_post, w_pre, eps)
+    dyp, lddy = _rows(w, "dy", dy, n, c, x) if dy is not None else (None, 0)
+    dup, lddu = _rows(w, "du", du, n, c, x) if du is not None else (None, 0)
+    g = {"dx": _new_rows(n, c, x), "db": _new_rows(n, c, x), "dgate": _new_rows(n, c, x) if gate is not None else None}
+    ws = None
+    for k, p in (("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
+        g[k] = torch.empty(c, dtype=torch.float32, device=x.device) if p is not None and param_grads else None
+        if g[k] is not None and ws is None:
+            ws = _ws(_wsbytes(_lib.mp_norm_block_bwd_ws, "mp_norm_block_bwd_ws", n, c, _is_bf16(x)))
+    _check(_lib.mp_norm_block_bwd(ctypes.byref(a), dyp, lddy, dup, lddu, _ptr(g["dx"]), c, _ptr(g["db"]), c,
+                                  _ptr(g["dgate"]), c, _ptr(g["dscale"]), _ptr(g["dw_post"]), _ptr(g["dw_pre"]),
+                                  _ptr(ws), ws.numel() if ws is not None else 0, _stream()), "mp_norm_block_bwd")
+    return g
+
+
+def _attention_args(where, q, k, v, struct_ptr, heads, pos, slope, L, mask, cap):
+    import torch
+    n, c = q.shape
+    qp, ldq = _rows(where, "q", q)
+    kp, ldk = _rows(where, "k", k, n, c, q)
+    vp, ldv = _rows(where, "v", v, n, c, q)
+    sp = _vec(where, "struct_ptr", struct_ptr, (struct_ptr.numel(),), torch.int32)
+    _need(struct_ptr.numel() >= 1, where, "struct_ptr must hold n_struct + 1 entries")
+    if mask is not None and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    return mp_attention_args(n, struct_ptr.numel() - 1, c, heads, _is_bf16(q), cap, L, sp,
+                             _vec(where, "pos", pos, (n, 3)), _vec(where, "slope", slope, (heads,)),
+                             _vec(where, "mask", mask, (n,), torch.uint8), qp, ldq, kp, ldk, vp, ldv)
+
+
+def structure_attention(q, k, v, struct_ptr, heads, pos=None, slope=None, L=0.0, mask=None, cap=0.0, out=None,
+                        save=False):
+    """Softmax attention between all atoms of each structure (rows struct_ptr[b] .. struct_ptr[b+1]-1 of
+    q, k, v [n][C]; int32, device): scores q.k / sqrt(C / heads), capped by cap tanh(./cap) if cap > 0,
+    minus slope[head] times the distance of the pair (pos float32 [n][3], slope float32 [heads]; minimum
+    image if L > 0), over the atoms with mask != 0 (bool or uint8 [n]).  Rows past the last structure are
+    not written (an out allocated here holds anything there).  save: returns (out, saved), saved for
+    structure_attention_bwd."""
+    import torch
+    n, c = q.shape
+    a = _attention_args("structure_attention", q, k, v, struct_ptr, heads, pos, slope, L, mask, cap)
+    out = _new_rows(n, c, q) if out is None else out
+    op, ldo = _rows("structure_attention", "out", out, n, c, q)
+    saved = None
+    if save:
+        m = ctypes.c_int64(0)
+        _check(_lib.mp_structure_attention_saved(n, c, heads, a.feat_dtype, ctypes.byref(m)),
+               "mp_structure_attention_saved")
+        saved = torch.empty(m.value, dtype=torch.float32, device=q.device)
+    _check(_lib.mp_structure_attention(ctypes.byref(a), op, ldo, _ptr(saved), _stream()), "mp_structure_attention")
+    return (out, saved) if save else out
+
+
+def structure_attention_bwd(q, k, v, struct_ptr, heads, out, saved, dout, pos=None, slope=None, L=0.0, mask=None,
+                            cap=0.0, dq=None, dk=None, dv=None, dpos=None):
+    """Gradients of structure_attention for dout as a dict: dq, dk, dv (rows), dpos float32 [n][3] and
+    dslope float32 [heads] (None without pos).  out, saved: what the forward call returned.  dq, dk, dv
+    and dpos may be given to be written into (column slices of one matrix, say).  Rows past the last
+    structure are not written (tensors allocated here hold anything there)."""
+    import torch
+    w = "structure_attention_bwd"
+    n, c = q.shape
+    a = _attention_args(w, q, k, v, struct_ptr, heads, pos, slope, L, mask, cap)
+    op, ldo = _rows(w, "out", out, n, c, q)
+    dp, ldd = _rows(w, "dout", dout, n, c, q)
+    m = ctypes.c_int64(0)
+    _check(_lib.mp_structure_attention_saved(n, c, heads, a.feat_dtype, ctypes.byref(m)),
+           "mp_structure_attention_saved")
+    sp = _vec(w, "saved", saved, (m.value,))
+    g = {key: _new_rows(n, c, q) if t is None else t for key, t in (("dq", dq), ("dk", dk), ("dv", dv))}
+    rows = [x for key in ("dq", "dk", "dv") for x in _rows(w, key, g[key], n, c, q)]
+    g["dpos"] = torch.empty(n, 3, dtype=torch.float32, device=q.device) if pos is not None and dpos is None else dpos
+    g["dslope"] = torch.empty(heads, dtype=torch.float32, device=q.device) if pos is not None else None
+    ws = _ws(_wsbytes(_lib.mp_structure_attention_bwd_ws, "mp_structure_attention_bwd_ws", n, a.n_struct, c, heads))
+    _check(_lib.mp_structure_attention_bwd(ctypes.byref(a), op, ldo, sp, dp, ldd, *rows,
+                                           _vec(w, "dpos", g["dpos"], (n, 3)), _ptr(g["dslope"]), _ptr(ws),
+                                           ws.numel(), _stream()),
+           "mp_structure_attention_bwd")
+    return g
 
 
 class MD:
