@@ -385,6 +385,34 @@ int mp_structure_attention_bwd(const mp_attention_args* a, const void* out, int6
                                void* dv, int64_t lddv, float* dpos, float* dslope, void* ws, size_t ws_bytes,
                                hipStream_t stream);
 
+/* Global blocks between the last layer and the readout of an energy evaluation, made
+ * of the block operators: attention beyond the cutoff over each structure, then a
+ * feed-forward, on the scalars x = h^0 of the last layer.  Block t (d = C / heads):
+ *   u = w_1 x / rms(x);  q, k, v = W_qkv u;  o = W_o attention(q, k, v; cap, slope)
+ *   x = x + s_1 * (p_1 * o / rms(o));  u = w_2 x / rms(x)
+ *   f = (SiLU(W_gate u) * (W_up u)) W_down;  x = x + s_2 * (p_2 * f / rms(f))
+ * (eps 1e-6).  Weight blob, float32, per block: w_1 [C], W_qkv [3C][C], slope [heads],
+ * W_o [C][C], p_1 [C], s_1 [C], w_2 [C], W_gate [hidden][C], W_up [hidden][C], W_down
+ * [C][hidden], p_2 [C], s_2 [C].  heads, hidden, cap as for the operators; 1 <= n_blocks
+ * <= MP_MAX_BLOCKS; the model's channels and feat_dtype must be ones the operators take. */
+#define MP_MAX_BLOCKS 16
+typedef struct mp_mixer mp_mixer;
+int mp_mixer_num_weights(const mp_model* m, int32_t n_blocks, int32_t heads, int32_t hidden, int64_t* n);
+int mp_mixer_create(const mp_model* m, int32_t n_blocks, int32_t heads, int32_t hidden, float cap,
+                    const float* host_weights, int64_t n_weights, mp_mixer** out);
+int mp_mixer_destroy(mp_mixer* mixer);
+/* mp_energy_forces with the mixer's blocks before the readout; forces by one reverse pass
+ * through readout, blocks and layers, the blocks' distance term included.  struct_ptr
+ * (device, int32 [n_struct + 1], ascending, struct_ptr[n_struct] = n): the structures, in
+ * the graph's slot order ({0, n} for one box).  atom_energy nullable.  ws: at least
+ * mp_energy_forces_mixer_ws bytes, 256-byte aligned; mp_energy_forces_status reads its
+ * flag.  MP_ERR_ARG if the mixer was made for other channels or feat_dtype. */
+int mp_energy_forces_mixer_ws(const mp_model* m, const mp_mixer* mixer, int32_t n, int32_t n_struct, int64_t n_edges,
+                              size_t* bytes);
+int mp_energy_forces_mixer(const mp_model* m, const mp_mixer* mixer, const mp_graph* g, const int32_t* struct_ptr,
+                           int32_t n_struct, const int32_t* perm, double* energy, float* forces, float* atom_energy,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---------------------------------------------------------------- MD -------
  * NVE velocity Verlet with skin-triggered rebuilds (Tessera abstract: a
  * conservative skin lets each rebuild interval replay as one captured

@@ -22,7 +22,7 @@ COMMON = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fconstexpr-st
 # strength-reduced pointer per array across the tile loop (fewer live registers)
 PER_FILE = {"neighbors.hip": ["-ffp-contract=off"], "model.hip": ["-mllvm", "-disable-lsr"]}
 SOURCES = ["neighbors.hip", "model.hip", "md.hip", "noalloc.hip", "api.cpp", "prof.cpp", "ops_norm.hip",
-           "ops_linear.hip", "ops_ffn.hip", "ops_attn_bf16.hip", "ops_attn_f32.hip", "ops_attn.cpp"]
+           "ops_linear.hip", "ops_ffn.hip", "ops_attn_bf16.hip", "ops_attn_f32.hip", "ops_attn.cpp", "mixer.hip"]
 
 
 def _compile(src):

@@ -427,6 +427,13 @@ extern "C" int mp_energy_forces_ws(const mp_model* m, int32_t n, int64_t n_edges
   return MP_OK;
 }
 
+size_t mdmp::ef_bytes(const mp_model* m, int32_t n, int64_t cap) {
+  Plan P = make_plan(m, n, cap);
+  Arena a(nullptr, 0, true);
+  carve_ef(a, P, true);
+  return a.off;
+}
+
 extern "C" int mp_layer_forward_ws(const mp_model* m, int32_t n, int64_t n_edges, size_t* bytes) {
   if (!m || !bytes || n < 1 || n_edges < 0) return arg_error("mp_layer_forward_ws: bad arguments");
   Plan P = make_plan(m, n, n_edges);
@@ -474,7 +481,7 @@ static int layer_mode(int t, int T) { return (t == 0 ? 1 : 0) | (t == T - 1 ? 2 
 // non-finite outputs.
 int ef_enqueue(const mp_model* m, const mp_graph* g, int64_t cap, const int32_t* perm, double* energy, float* forces,
                float* atom_energy, void* ws, size_t ws_bytes, int32_t** flag_out, hipStream_t st,
-               const mp_heads* heads, double* head_energy) {
+               const mp_heads* heads, double* head_energy, const MixRun* mix) {
   MP_TRY(check_graph(m, g));
   if (!energy || !forces || !ws) return arg_error("null energy/forces/ws");
   if (g->n_edges > cap) return arg_error("graph has more edges than the workspace capacity");
@@ -492,6 +499,7 @@ int ef_enqueue(const mp_model* m, const mp_graph* g, int64_t cap, const int32_t*
     MP_TRY(dispatch_layer_fwd(P, A, m->layers[t], w.h, w.h, (char*)w.ht + fb * t, w.q + (size_t)t * P.n * P.C,
                               (char*)w.m + fb * t, layer_mode(t, P.T), st));
   }
+  if (mix) MP_TRY(mixer_forward(*mix, P, g, w.h, st));
   float* e_atoms = atom_energy ? atom_energy : w.e_atoms;
   MP_TRY(fill_zero(w.flag, sizeof(int32_t), st));
   if (heads) {
@@ -508,6 +516,7 @@ int ef_enqueue(const mp_model* m, const mp_graph* g, int64_t cap, const int32_t*
     MP_TRY(launch_energy(e_atoms, P.n, energy, w.flag, st));
     MP_TRY(dispatch_readout_bwd(P, 1, w.h, m->wrT, m->wr, m->wout, nullptr, w.g_h, st));
   }
+  if (mix) MP_TRY(mixer_backward(*mix, P, g, w.g_h, st));
   // reverse pass through the layers
   MP_TRY(fill_zero(w.gd, sizeof(float) * (size_t)gd_floats(P), st));
   BwdArgs B{};
@@ -526,6 +535,7 @@ int ef_enqueue(const mp_model* m, const mp_graph* g, int64_t cap, const int32_t*
     MP_TRY(dispatch_layer_bwd(P, A, m->layers[t], B, w.g_h, layer_mode(t, P.T), t > 0, st));
   }
   MP_TRY(launch_forces(P, g, w.G, w.gd, perm, forces, w.flag, st));
+  if (mix) MP_TRY(mixer_forces(*mix, P, perm, forces, w.flag, st));
   if (flag_out) *flag_out = w.flag;
   return MP_OK;
 }

@@ -4,6 +4,7 @@
 
 struct mp_model;
 struct mp_heads;
+struct mp_mixer;
 
 namespace mdmp {
 
@@ -62,6 +63,16 @@ constexpr int kGeoFloats = 16;
 inline int gd_half_slots(const Plan& P) { return (P.ncb + 1) / 2; }
 // floats of the geometry-gradient partials: two halves of [cap][half slots][3]
 inline int64_t gd_floats(const Plan& P) { return 2 * (int64_t)gd_half_slots(P) * P.cap * 3; }
+
+// one evaluation's global blocks: the mixer, the structures and the workspace behind
+// the evaluation's own
+struct MixRun {
+  const mp_mixer* mixer;
+  const int32_t* struct_ptr;
+  int32_t n_struct;
+  void* ws;
+  size_t ws_bytes;
+};
 
 struct Geo {
   int32_t *aend, *a_j, *a_r, *amap, *arev;  // a_r: padded index of the reverse edge
@@ -129,7 +140,15 @@ int fill_zero(void* p, size_t bytes, hipStream_t st);
 // lam-weighted sum, whose gradient the reverse pass follows
 int ef_enqueue(const mp_model* m, const mp_graph* g, int64_t cap, const int32_t* perm, double* energy, float* forces,
                float* atom_energy, void* ws, size_t ws_bytes, int32_t** flag_out, hipStream_t st,
-               const mp_heads* heads = nullptr, double* head_energy = nullptr);
+               const mp_heads* heads = nullptr, double* head_energy = nullptr, const MixRun* mix = nullptr);
+// bytes of ef_enqueue's own workspace, a multiple of 256: what a mixer's follows
+size_t ef_bytes(const mp_model* m, int32_t n, int64_t cap);
+// global blocks between the last layer and the readout: rows 0 of h [n][K][C] are replaced
+// (forward), rows 0 of g_h [n][K][C] are replaced (backward) and the blocks' own position
+// gradients taken off the forces
+int mixer_forward(const MixRun& R, const Plan& P, const mp_graph* g, void* h, hipStream_t st);
+int mixer_backward(const MixRun& R, const Plan& P, const mp_graph* g, float* g_h, hipStream_t st);
+int mixer_forces(const MixRun& R, const Plan& P, const int32_t* perm, float* forces, int32_t* flag, hipStream_t st);
 
 }  // namespace mdmp
 

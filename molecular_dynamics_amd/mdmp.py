@@ -40,7 +40,8 @@ EXPORTS = ["mp_version", "mp_last_error", "mp_model_num_weights", "mp_model_crea
            "mp_linear", "mp_linear_bwd_ws", "mp_linear_bwd", "mp_gated_ffn", "mp_gated_ffn_bwd_ws",
            "mp_gated_ffn_bwd", "mp_norm_block", "mp_norm_block_bwd_ws", "mp_norm_block_bwd",
            "mp_structure_attention_saved", "mp_structure_attention", "mp_structure_attention_bwd_ws",
-           "mp_structure_attention_bwd",
+           "mp_structure_attention_bwd", "mp_mixer_num_weights", "mp_mixer_create", "mp_mixer_destroy",
+           "mp_energy_forces_mixer_ws", "mp_energy_forces_mixer",
            "mp_profile_enable",
            "mp_profile_reset", "mp_profile_read"]
 
@@ -134,6 +135,11 @@ _sig = {
     "mp_structure_attention_bwd_ws": ([_i32, _i32, _i32, _i32, _P(_sz)], ctypes.c_int),
     "mp_structure_attention_bwd": ([_P(mp_attention_args), _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                     _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "mp_mixer_num_weights": ([_vp, _i32, _i32, _i32, _P(_i64)], ctypes.c_int),
+    "mp_mixer_create": ([_vp, _i32, _i32, _i32, _f32, _vp, _i64, _P(_vp)], ctypes.c_int),
+    "mp_mixer_destroy": ([_vp], ctypes.c_int),
+    "mp_energy_forces_mixer_ws": ([_vp, _vp, _i32, _i32, _i64, _P(_sz)], ctypes.c_int),
+    "mp_energy_forces_mixer": ([_vp, _vp, _P(mp_graph), _vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     "mp_profile_enable": ([ctypes.c_int], ctypes.c_int),
     "mp_profile_reset": ([], ctypes.c_int),
     "mp_profile_read": ([ctypes.c_char_p, _P(ctypes.c_double), _P(_i64)], ctypes.c_int),
@@ -663,6 +669,58 @@ def structure_attention_bwd(q, k, v, struct_ptr, heads, out, saved, dout, pos=No
                                            ws.numel(), _stream()),
            "mp_structure_attention_bwd")
     return g
+
+
+class Mixer:
+    """Global blocks (structure attention and a gated feed-forward) between a model's last layer and
+    its readout (mp_mixer_create); weights: host float32 blob in the order of mdmp.h."""
+
+    def __init__(self, model, n_blocks, heads, hidden, weights, cap=0.0):
+        w = np.ascontiguousarray(weights, np.float32)
+        h = ctypes.c_void_p(0)
+        _check(_lib.mp_mixer_create(model.h, n_blocks, heads, hidden, cap, w.ctypes.data, w.size, ctypes.byref(h)),
+               "mp_mixer_create")
+        self.h, self.model, self.n_blocks = h, model, n_blocks
+
+    @staticmethod
+    def num_weights(model, n_blocks, heads, hidden):
+        n = ctypes.c_int64(0)
+        _check(_lib.mp_mixer_num_weights(model.h, n_blocks, heads, hidden, ctypes.byref(n)), "mp_mixer_num_weights")
+        return n.value
+
+    def close(self):
+        if self.h:
+            _lib.mp_mixer_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def energy_forces_mixer(model, mixer, g, struct_ptr=None, perm=None, atom_energy=None, ws=None):
+    """mp_energy_forces_mixer: (energy (float), forces [n][3]).  struct_ptr: cuda int32 [B + 1], the
+    structures of the graph (None: the whole graph is one)."""
+    import torch
+    if struct_ptr is None:
+        struct_ptr = torch.tensor([0, g.n], dtype=torch.int32, device="cuda")
+    nst = struct_ptr.numel() - 1
+    if ws is None:
+        nbytes = ctypes.c_size_t(0)
+        _check(_lib.mp_energy_forces_mixer_ws(model.h, mixer.h, g.n, nst, max(g.n_edges, 1), ctypes.byref(nbytes)),
+               "mp_energy_forces_mixer_ws")
+        ws = _ws(nbytes.value)
+    sp = _vec("energy_forces_mixer", "struct_ptr", struct_ptr, (nst + 1,), torch.int32)
+    energy = torch.zeros(1, dtype=torch.float64, device="cuda")
+    forces = torch.empty(g.n, 3, dtype=torch.float32, device="cuda")
+    gs = g.struct()
+    _check(_lib.mp_energy_forces_mixer(model.h, mixer.h, ctypes.byref(gs), sp, nst, _ptr(perm), _ptr(energy),
+                                       _ptr(forces), _ptr(atom_energy), _ptr(ws), ws.numel(), _stream()),
+           "mp_energy_forces_mixer")
+    _check(_lib.mp_energy_forces_status(_ptr(ws), _stream()), "mp_energy_forces_status")
+    return float(energy.item()), forces
 
 
 class MD:

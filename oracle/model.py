@@ -345,6 +345,74 @@ def energy_heads(cfg, weights, head_wr, head_wout, lam, pos, species, L, row_ptr
     return out
 
 
+def mixer_layout(C, heads, hidden):
+    """One global block's weights: (name, rows, cols), float32 row-major, in blob order."""
+    return [("w1", 1, C), ("wqkv", 3 * C, C), ("slope", 1, heads), ("wo", C, C), ("p1", 1, C), ("s1", 1, C),
+            ("w2", 1, C), ("wg", hidden, C), ("wu", hidden, C), ("wd", C, hidden), ("p2", 1, C), ("s2", 1, C)]
+
+
+def mixer_blocks(x, weights, n_blocks, heads, hidden, cap, P, Ld, struct_ptr, eps=1e-6):
+    """Global blocks on the scalars x [N, C]: attention between all atoms of each structure
+    (scores capped by cap tanh(./cap) if cap > 0, minus slope times the distance), then a gated
+    feed-forward, each between a norm before and a norm and residual scale after."""
+    C = x.shape[1]
+    d = C // heads
+    w = torch.as_tensor(np.asarray(weights, np.float32).astype(np.float64))
+    off = 0
+
+    def rms(v):
+        return v / torch.sqrt((v * v).mean(1, keepdim=True) + eps)
+
+    for _ in range(n_blocks):
+        W = {}
+        for name, r, c in mixer_layout(C, heads, hidden):
+            W[name] = w[off:off + r * c].reshape(r, c)
+            off += r * c
+        qkv = (rms(x) * W["w1"]) @ W["wqkv"].T
+        att = []
+        for a, b in zip(struct_ptr[:-1], struct_ptr[1:]):
+            if a == b:
+                continue
+            q, k, v = (qkv[a:b, j * C:(j + 1) * C].reshape(b - a, heads, d).permute(1, 0, 2) for j in range(3))
+            s = (q @ k.transpose(1, 2)) / np.sqrt(d)
+            if cap > 0:
+                s = cap * torch.tanh(s / cap)
+            D = P[a:b][None, :, :] - P[a:b][:, None, :]
+            if Ld is not None:
+                D = D - Ld * torch.round((D / Ld).detach())
+            same = torch.eye(b - a, dtype=torch.bool)
+            r = torch.sqrt((D * D).sum(-1) + same.to(D.dtype)) * (~same)
+            att.append((torch.softmax(s - W["slope"].reshape(-1, 1, 1) * r, 2) @ v).permute(1, 0, 2).reshape(b - a, C))
+        o = torch.cat(att) @ W["wo"].T
+        x = x + W["s1"] * W["p1"] * rms(o)
+        u = rms(x) * W["w2"]
+        f = (F.silu(u @ W["wg"].T) * (u @ W["wu"].T)) @ W["wd"].T
+        x = x + W["s2"] * W["p2"] * rms(f)
+    return x
+
+
+def energy_mixer(cfg, weights, mixer, n_blocks, heads, hidden, cap, pos, species, L, row_ptr, col, struct_ptr,
+                 forces=True):
+    """`energy` with global blocks (`mixer_blocks`) between the last layer's scalars and the readout."""
+    prm = Params(cfg, weights)
+    cgs = cg_table(cfg.lmax)
+    Ld = None if L is None else float(np.float32(L))
+    P = torch.tensor(_as_f64(pos), requires_grad=forces)
+    row, colt = _active_edges(P, Ld, row_ptr, col, cfg.cutoff)
+    r, rhat = edge_geometry(P, Ld, row, colt)
+    h = embed(cfg, prm, species)
+    for t in range(cfg.layers):
+        h = layer(cfg, prm.layers[t], h, r, rhat, row, colt, P.shape[0], cgs)
+    x = mixer_blocks(h[0][:, :, 0], mixer, n_blocks, heads, hidden, cap, P, Ld, [int(s) for s in struct_ptr])
+    Ea = readout(prm, x[:, :, None])
+    E = Ea.sum()
+    out = {"E": float(E.detach()), "E_atoms": Ea.detach().numpy()}
+    if forces:
+        (g,) = torch.autograd.grad(E, P)
+        out["F"] = (-g).numpy()
+    return out
+
+
 def to_flat(h):
     """list over l of [N, C, 2l+1] -> numpy [N, K, C] with k = l^2 + m + l."""
     return torch.cat([x.permute(0, 2, 1) for x in h], dim=1).numpy()
