@@ -272,7 +272,7 @@ int mp_energy_forces_heads(const mp_model* m, const mp_heads* heads, const mp_gr
  *
  * Rows: a matrix of n rows is a device pointer and a row stride ld (elements), so
  * h^0 of a feature array [n][K][C] is (h, K C); rows must be 16-byte aligned and
- * ld a multiple of 16 bytes.  Features and weight matrices are of feat_dtype
+ * ld a multiple of 16 bytes (attention: at most 2^24).  Features and weight matrices are of feat_dtype
  * (0 float32, 1 bfloat16); vectors of parameters, positions and slopes and the
  * gradients of those are float32.  bfloat16: products take bf16 operands with
  * float32 accumulation, everything else is float32, and each output is rounded

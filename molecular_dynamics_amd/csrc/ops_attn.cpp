@@ -13,6 +13,9 @@ namespace {
 // the chip with a quarter of the atoms and quarters each wave's walk.
 constexpr int kSplitAbove = 64;
 
+// the kernels address the rows of one step by 32-bit offsets from a 64-bit base
+constexpr int64_t kMaxLd = 1 << 24;
+
 int check_shape(const char* who, int32_t n, int32_t channels, int32_t heads, int32_t dt) {
   MP_TRY(check_width(who, channels, dt));
   if (n < 0) return arg_error(std::string(who) + ": n must be >= 0");
@@ -44,6 +47,7 @@ int attn_args(const char* who, const mp_attention_args* a, AttnArgs& A) {
   if (!a->struct_ptr) return arg_error(std::string(who) + ": null struct_ptr");
   if (!a->q || !a->k || !a->v) return arg_error(std::string(who) + ": null q, k or v");
   const int C = a->channels, es = a->feat_dtype == 1 ? 2 : 4;
+  if (a->ldq > kMaxLd || a->ldk > kMaxLd || a->ldv > kMaxLd) return arg_error(std::string(who) + ": row stride above 2^24");
   if (!rows_ok(a->q, a->ldq, C, es) || !rows_ok(a->k, a->ldk, C, es) || !rows_ok(a->v, a->ldv, C, es))
     return arg_error(std::string(who) +
                      ": rows of q, k and v must be 16-byte aligned, with a row stride of at least their width and a "
@@ -114,6 +118,7 @@ extern "C" int mp_structure_attention_bwd(const mp_attention_args* a, const void
     return dslope ? ops::reduce_rows(nullptr, 0, H, H, dslope, false, st) : MP_OK;
   if (!out || !saved || !dout || !dq || !dk || !dv)
     return arg_error("mp_structure_attention_bwd: null out, saved, dout, dq, dk or dv");
+  if (lddo > ops::kMaxLd) return arg_error("mp_structure_attention_bwd: row stride above 2^24");
   MP_ROWS("mp_structure_attention_bwd", "out", out, ldo, C, dt);
   MP_ROWS("mp_structure_attention_bwd", "dout", dout, lddo, C, dt);
   MP_ROWS("mp_structure_attention_bwd", "dq", dq, lddq, C, dt);

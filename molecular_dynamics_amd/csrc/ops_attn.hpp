@@ -84,6 +84,9 @@ __device__ __forceinline__ float tanh_of(float y) {
   return fabsf(y) < 0.25f ? y * p : e;
 }
 
+// a value that is equal in every lane, as a scalar
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // Structure and row range of tile slot `slot` (R rows per slot); false: the slot is empty.
 // Row bounds are clamped to [0, n], so no struct_ptr can lead out of the arrays.
 template <int R>
@@ -98,8 +101,8 @@ __device__ __forceinline__ bool find_slot(const AttnArgs& A, int slot, int lane,
     lo += (k - 1) * step;
     hi = min(hi, lo + step - 1);
   }
-  s = min(max(A.sptr[lo], 0), A.n);
-  e = min(max(A.sptr[lo + 1], s), A.n);
+  s = uniform(min(max(A.sptr[lo], 0), A.n));
+  e = uniform(min(max(A.sptr[lo + 1], s), A.n));
   const int t = slot - (s / R + lo);
   row0 = s + t * R;
   return t >= 0 && row0 < e;
@@ -116,39 +119,54 @@ constexpr uint64_t all_live() {
   return (1ull << CK) - 1;
 }
 
-// CK rows of a matrix into one wave's LDS tile, rows without their bit as zeros
+// CK rows of a matrix from row k0 on: a wave's copy in LDS (one tile, rows of RS), or MFMA
+// operands in natural order, frag[t][ch] = row 16 t + i.  Row k0 is the same for the wave, so an
+// address is a scalar base and a 32-bit lane offset (rows are at most 2^24 elements long).
+// Rows past the structure (rows < CK of them left) are read as its last row, and cleared where
+// their contents matter by the caller.
 template <class T, int C, int RS>
 struct WaveTile {
-  static constexpr int CK = MF<T>::CK, EV = MF<T>::EV, VPR = C / EV, IT = CK * VPR / 64;
-  static_assert(CK * VPR % 64 == 0, "whole waves");
+  static constexpr int CK = MF<T>::CK, EV = MF<T>::EV, VPR = C / EV, IT = CK * VPR / 64, RJ = 64 / VPR;
+  static_assert(CK * VPR % 64 == 0 && 64 % VPR == 0, "whole waves");
   u4 v[IT];
-  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int64_t k0, uint64_t on, int lane) {
+  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int64_t k0, int rows, int lane) {
+    const T* p = src + k0 * ld;
+    const uint32_t r = lane / VPR, c = (lane % VPR) * EV;
+    if (rows >= CK) {
+      const uint32_t off = r * (uint32_t)ld + c;
 #pragma unroll
-    for (int j = 0; j < IT; ++j) {
-      const int x = lane + 64 * j, r = x / VPR, c = (x % VPR) * EV;
-      v[j] = ld16<u4>(src + (k0 + r) * ld + c, (on >> r) & 1);
+      for (int j = 0; j < IT; ++j) v[j] = *(const u4*)(p + j * RJ * ld + off);
+    } else {
+#pragma unroll
+      for (int j = 0; j < IT; ++j) v[j] = *(const u4*)(p + min(r + j * RJ, (uint32_t)rows - 1) * (uint32_t)ld + c);
     }
+  }
+  // rows without their bit become zeros
+  __device__ __forceinline__ void clear(uint64_t on, int lane) {
+    const uint32_t m = (uint32_t)on >> (lane / VPR);
+#pragma unroll
+    for (int j = 0; j < IT; ++j)
+      if (!((m >> (j * RJ)) & 1)) v[j] = u4{0u, 0u, 0u, 0u};
   }
   __device__ __forceinline__ void put(T* dst, int lane) const {
 #pragma unroll
-    for (int j = 0; j < IT; ++j) {
-      const int x = lane + 64 * j;
-      *(u4*)(dst + (x / VPR) * RS + (x % VPR) * EV) = v[j];
-    }
+    for (int j = 0; j < IT; ++j) *(u4*)(dst + (lane / VPR + j * RJ) * RS + (lane % VPR) * EV) = v[j];
   }
 };
-
-// rows of a matrix as MFMA operands in natural order: frag[t][ch] = row k0 + 16 t + i
+// chunks c0 .. c1 - 1 of the operands of NTL tiles
 template <class T, int C, int NTL>
 __device__ __forceinline__ void load_frags(typename MF<T>::F (&f)[NTL][C / MF<T>::CK], const T* src, int64_t ld,
-                                           int64_t k0, uint64_t on, int i, int g) {
+                                           int64_t k0, int rows, int i, int g, int c0 = 0, int c1 = C / MF<T>::CK) {
   using M = MF<T>;
+  const T* p = src + k0 * ld;
 #pragma unroll
   for (int t = 0; t < NTL; ++t) {
-    const T* p = src + (k0 + 16 * t + i) * ld + M::EV * g;
-    const bool o = (on >> (16 * t + i)) & 1;
+    uint32_t r = 16 * t + i;
+    if (rows < 16 * NTL) r = min(r, (uint32_t)rows - 1);
+    const uint32_t off = r * (uint32_t)ld + M::EV * g;
 #pragma unroll
-    for (int ch = 0; ch < C / M::CK; ++ch) f[t][ch] = ld16<typename M::F>(p + ch * M::CK, o);
+    for (int ch = 0; ch < C / M::CK; ++ch)
+      if (ch >= c0 && ch < c1) f[t][ch] = *(const typename M::F*)(p + off + ch * M::CK);
   }
 }
 
@@ -185,52 +203,113 @@ struct AttnDims {
   static constexpr int CK = MF<T>::CK, RS = C + 16 / (int)sizeof(T), OS = C + 4;
 };
 
+// one head's channel chunk range: chunk ch belongs to the operands of head h alone (heads of a
+// chunk or more), or is the last to be read by head h
+template <class T, int DH>
+constexpr int chunk_first(int h) {
+  return DH >= MF<T>::CK ? h * (DH / MF<T>::CK) : h / 2;
+}
+template <class T, int DH>
+constexpr int chunk_end(int h) {
+  return DH >= MF<T>::CK ? (h + 1) * (DH / MF<T>::CK) : (h + 1) / 2;
+}
+
+// Scores in the reference of a lane's query: x = log2(e) s + b.  bf16 features: tanh(y) =
+// 1 - 2 / (e^2y + 1), whose leading 1 is the same for every key and left out of x (and so out of
+// the saved log-sums: the backward passes form x by this function too).
+struct Score {
+  float sc, k;  // x = k f(sc S) + b
+  bool cap;
+};
+template <class T>
+__device__ __forceinline__ Score score_of(const AttnArgs& A) {
+  if (!(A.cap > 0)) return Score{A.scale * kLog2e, 1.0f, false};
+  if constexpr (sizeof(T) == 2) return Score{A.scale / A.cap * (2.0f * kLog2e), -2.0f * A.cap * kLog2e, true};
+  return Score{A.scale / A.cap, A.cap * kLog2e, true};
+}
+// the capped part of x over k: bf16 1 / (e^2y + 1) = (1 - tanh y) / 2, float32 tanh y
+template <class T>
+__device__ __forceinline__ float cap_of(float s, float sc) {
+  if constexpr (sizeof(T) == 2) return rcp(ex2(s * sc) + 1.0f);
+  return tanh_of<T>(s * sc);
+}
+template <class T>
+__device__ __forceinline__ float score(const Score& Z, float s, float b) {
+  return Z.cap ? fmaf(Z.k, cap_of<T>(s, Z.sc), b) : fmaf(s, Z.sc, b);
+}
+
 // ------------------------------------------------------------------------------ forward
-template <class T, int C, int DH, int KW>
-__global__ __launch_bounds__(64 * KW) void k_attn_fwd(AttnArgs A) {
+template <class T, int C, int DH, int KW, bool SAVE>
+__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 128 ? 2 : 3)))
+void k_attn_fwd(AttnArgs A) {
   using M = MF<T>;
   using D = AttnDims<T, C>;
   constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
   constexpr int TILE = CK * RS * sizeof(T) + CK * 16, SLAB = 16 * OS * 4;
   constexpr int WB = KW > 1 && SLAB > TILE ? SLAB : TILE;
+  constexpr bool BF = sizeof(T) == 2;
   __shared__ __align__(16) char s_w[KW][WB];
   __shared__ float s_m[KW > 1 ? KW : 1][2][H][16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = KW > 1 ? uniform(threadIdx.x >> 6) : 0, i = lane & 15, g = lane >> 4;
   int row0, s, e;
   if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
   const int row = row0 + i;
-  const bool fix = A.to_fix > 0;
+  const bool fix = A.to_fix > 0, dist = A.pos != nullptr;
   typename M::F qf[1][NC];
-  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, row0 + 16 <= e ? 0xffffull : (1ull << (e - row0)) - 1, i, g);
+  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, row < e);
-  float slope[H], m[H], l[H];
+  // thr: a score above it (in the reference m) raises the reference; -inf until there is one
+  float m[H], thr[H];
+  f4 l[H];  // bf16: every element the sum over all keys; float32: per-lane sums in l.x
 #pragma unroll
   for (int h = 0; h < H; ++h) {
-    slope[h] = A.slope ? A.slope[h] * (kLog2e * A.unit) : 0.f;
-    m[h] = -INFINITY;
-    l[h] = 0.f;
+    m[h] = 0.f;
+    thr[h] = -INFINITY;
+    l[h] = f4{0.f, 0.f, 0.f, 0.f};
   }
   f4 acc[C / 16];
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
   T* vs = (T*)s_w[wave];
   u4* ps = (u4*)(s_w[wave] + CK * RS * sizeof(T));
-  const float sc = A.cap > 0 ? A.scale / A.cap : A.scale * kLog2e, capl = A.cap * kLog2e;
+  const Score Z = score_of<T>(A);
+  typename M::F ones;
+  if constexpr (BF) ones = __builtin_bit_cast(typename M::F, u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+
+  // A step's loads are issued during the step before: values and coordinates at its start, each
+  // head's keys as soon as its scores have read the ones they replace
+  WaveTile<T, C, RS> tv;
+  typename M::F kf[NT][NC];
+  P3 kp{0u, 0u, 0u};
+  uint64_t on = live<CK>(A, s + CK * wave, e, lane, true);
+  auto fetch_v = [&](int k0, uint64_t b) {
+    tv.fetch((const T*)A.v, A.ldv, k0, e - k0, lane);
+    if (dist && lane < CK) kp = load_pos(A, k0 + lane, (b >> lane) & 1);
+  };
+  if (s + CK * wave < e) {
+    fetch_v(s + CK * wave, on);
+    load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, s + CK * wave, e - s - CK * wave, i, g);
+  }
 
   for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
-    const uint64_t on = live<CK>(A, k0, e, lane, true);
-    WaveTile<T, C, RS> tv;
-    tv.fetch((const T*)A.v, A.ldv, k0, on, lane);
-    typename M::F kf[NT][NC];
-    load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, k0, on, i, g);
-    if (A.pos && lane < CK) {
-      const P3 p = load_pos(A, k0 + lane, (on >> lane) & 1);
-      ps[lane] = u4{p.x, p.y, p.z, 0u};
-    }
+    const int kn = k0 + CK * KW;
+    const bool part = on != all_live<CK>();
+    const uint64_t on_n = live<CK>(A, kn, e, lane, true);
+    if (part) tv.clear(on, lane);
     tv.put(vs, lane);
+    if (dist && lane < CK) ps[lane] = u4{kp.x, kp.y, kp.z, 0u};
     wave_sync();
+    if (kn < e) fetch_v(kn, on_n);
+    const uint32_t bits = (uint32_t)on >> (4 * g);
+    bool lv[NT][4];
     f4 r[NT];
-    if (A.pos) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      r[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) lv[t][q] = (bits >> (16 * t + q)) & 1;
+    }
+    if (dist) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -244,46 +323,57 @@ __global__ __launch_bounds__(64 * KW) void k_attn_fwd(AttnArgs A) {
     for (int h = 0; h < H; ++h) {
       f4 x[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
-        if (A.cap > 0) {
+      for (int t = 0; t < NT; ++t) x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
+      if (kn < e)
+        load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, kn, e - kn, i, g, chunk_first<T, DH>(h), chunk_end<T, DH>(h));
+      const float sl = dist ? A.slope[h] * (kLog2e * A.unit) : 0.f;
+      if (Z.cap) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) x[t][q] = capl * tanh_of<T>(x[t][q] * sc);
-        } else {
-          x[t] *= sc;
-        }
-        if (A.pos) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) x[t][q] = fmaf(-slope[h], r[t][q], x[t][q]);
-        }
-        if (on != all_live<CK>()) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (!((on >> (16 * t + 4 * g + q)) & 1)) x[t][q] = -INFINITY;
-        }
+          for (int q = 0; q < 4; ++q) x[t][q] = cap_of<T>(x[t][q], Z.sc);
       }
-      // the running maximum is raised only when a score passes it by 8 (p <= 2^8): the sums
-      // are exact relative to any reference, so most steps need no exchange and no rescale
+      const float kk = Z.cap ? Z.k : Z.sc;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[t][q] = fmaf(kk, x[t][q], fmaf(-sl, r[t][q], -m[h]));
+      if (part) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[t][q] = lv[t][q] ? x[t][q] : -INFINITY;
+      }
+      // the reference is raised only when a score passes it by 8 (p <= 2^8): the sums are exact
+      // relative to any reference, so most steps need no exchange and no rescale
       float lm = -INFINITY;
 #pragma unroll
       for (int t = 0; t < NT; ++t) lm = fmaxf(lm, fmaxf(fmaxf(x[t].x, x[t].y), fmaxf(x[t].z, x[t].w)));
-      if (__any(lm > m[h] + 8.0f)) {
-        const float mn = fmaxf(m[h], gmax(lm));
-        const float al = mn == -INFINITY ? 1.0f : ex2(m[h] - mn);
-        m[h] = mn;
-        l[h] *= al;
+      if (__any(lm > thr[h])) {
+        const float mt = gmax(lm);
+        const bool first = thr[h] == -INFINITY;
+        const float d = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f), al = ex2(-d);
+        if (mt > -INFINITY) thr[h] = 8.0f;
+        m[h] += d;
+        if (!first) {
+          l[h] *= al;
 #pragma unroll
-        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] *= al;
+          for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] *= al;
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[t] -= d;
       }
-      const float mu = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[t][q] = ex2(x[t][q] - mu);
-        l[h] += (x[t].x + x[t].y) + (x[t].z + x[t].w);
+        for (int q = 0; q < 4; ++q) x[t][q] = ex2(x[t][q]);
+        if constexpr (!BF) l[h].x += (x[t].x + x[t].y) + (x[t].z + x[t].w);
       }
       const typename M::F p = M::pack(x);
-      if (sizeof(T) == 2 && A.o32) {
+      // bf16: the sum of the weights is a product with ones, off the VALU and of the same rounded
+      // weights that the values get
+      if constexpr (BF) l[h] = M::mma(l[h], ones, p);
+      if constexpr (BF && SAVE) {
         // for a backward pass the weights enter as two bf16 values, p and its remainder
         // (2^-18): o32, and with it dsum and the float32 gradients, keep float32's quality
         f4 y[NT];
@@ -291,6 +381,7 @@ __global__ __launch_bounds__(64 * KW) void k_attn_fwd(AttnArgs A) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) y[t] = x[t] - y[t];
         const typename M::F p2 = M::pack(y);
+        l[h] = M::mma(l[h], ones, p2);
 #pragma unroll
         for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
           const typename M::F f = ldt<RS>(vs, 0, 16 * ct, lane);
@@ -302,16 +393,20 @@ __global__ __launch_bounds__(64 * KW) void k_attn_fwd(AttnArgs A) {
           acc[ct] = M::mma(acc[ct], ldt<RS>(vs, 0, 16 * ct, lane), p);
       }
     }
+    on = on_n;
     wave_sync();
   }
 #pragma unroll
-  for (int h = 0; h < H; ++h) l[h] = gsum(l[h]);
+  for (int h = 0; h < H; ++h) {
+    if constexpr (!BF) l[h].x = gsum(l[h].x);
+    if (thr[h] == -INFINITY) m[h] = -INFINITY;
+  }
 
   if constexpr (KW == 1) {
     if (row >= e) return;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const float inv = l[h] > 0.f || l[h] != l[h] ? 1.0f / l[h] : 0.f;
+      const float inv = l[h].x > 0.f || l[h].x != l[h].x ? 1.0f / l[h].x : 0.f;
 #pragma unroll
       for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
         acc[ct] *= inv;
@@ -319,7 +414,7 @@ __global__ __launch_bounds__(64 * KW) void k_attn_fwd(AttnArgs A) {
         st4((T*)A.out + (int64_t)row * A.ldo + c, acc[ct]);
         if (A.o32) st4(A.o32 + (int64_t)row * C + c, acc[ct]);
       }
-      if (A.lse && g == 0) A.lse[(int64_t)row * H + h] = l[h] > 0.f || l[h] != l[h] ? m[h] + log2f(l[h]) : INFINITY;
+      if (A.lse && g == 0) A.lse[(int64_t)row * H + h] = l[h].x > 0.f || l[h].x != l[h].x ? m[h] + log2f(l[h].x) : INFINITY;
     }
   } else {
     float* slab = (float*)s_w[wave];
@@ -329,7 +424,7 @@ __global__ __launch_bounds__(64 * KW) void k_attn_fwd(AttnArgs A) {
     for (int h = 0; h < H; ++h)
       if (g == 0) {
         s_m[wave][0][h][i] = m[h];
-        s_m[wave][1][h][i] = l[h];
+        s_m[wave][1][h][i] = l[h].x;
       }
     __syncthreads();
     for (int x = threadIdx.x; x < 16 * (C / EV); x += 64 * KW) {
@@ -364,23 +459,30 @@ __global__ __launch_bounds__(64 * KW) void k_attn_fwd(AttnArgs A) {
 // Score, softmax weight and score gradient of one lane's 4 pairs:
 //   p = 2^(x - lse), dl = p (dp - dsum); ds = dl times the cap's slope 1 - tanh^2
 template <class T>
-__device__ __forceinline__ void pair_grad(const AttnArgs& A, float sc, float capl, f4 sraw, f4 dp, f4 r, float slope,
-                                          f4 lse, f4 dsum, uint64_t on, int k, f4& p, f4& dl, f4& ds) {
+__device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4 dp, f4 r, float slope, f4 lse, f4 dsum,
+                                          bool all, uint64_t on, int k, f4& p, f4& dl, f4& ds) {
+  f4 f;
+  if (Z.cap) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      sraw[q] = cap_of<T>(sraw[q], Z.sc);
+      // 1 - tanh^2, with u = (1 - tanh) / 2: 4 u (1 - u)
+      f[q] = sizeof(T) == 2 ? 4.0f * fmaf(-sraw[q], sraw[q], sraw[q]) : fmaf(-sraw[q], sraw[q], 1.0f);
+    }
+  }
+  const float kk = Z.cap ? Z.k : Z.sc;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    float x, f = 1.0f;
-    if (A.cap > 0) {
-      const float th = tanh_of<T>(sraw[q] * sc);
-      x = capl * th;
-      f = fmaf(-th, th, 1.0f);
-    } else {
-      x = sraw[q] * sc;
-    }
-    if (A.pos) x = fmaf(-slope, r[q], x);
-    const bool o = (on >> (k + q)) & 1;
-    p[q] = o ? ex2(x - lse[q]) : 0.f;
-    dl[q] = o ? p[q] * (dp[q] - dsum[q]) : 0.f;
-    ds[q] = dl[q] * f;
+    const float x = fmaf(kk, sraw[q], dist ? fmaf(-slope, r[q], -lse[q]) : -lse[q]);
+    p[q] = ex2(x);
+    dl[q] = p[q] * (dp[q] - dsum[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) ds[q] = Z.cap ? dl[q] * f[q] : dl[q];
+  if (!all) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (!((on >> (k + q)) & 1)) p[q] = dl[q] = ds[q] = 0.f;
   }
 }
 
@@ -398,7 +500,7 @@ __global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
   __shared__ __align__(16) char s_w[KW][WB];
   __shared__ float s_p[KW][3][16];
   __shared__ float s_s[KW][H];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = KW > 1 ? uniform(threadIdx.x >> 6) : 0, i = lane & 15, g = lane >> 4;
   int row0, s, e;
   if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) {
     if (A.dslope_part && threadIdx.x < H) A.dslope_part[(int64_t)blockIdx.x * H + threadIdx.x] = 0.f;
@@ -406,10 +508,9 @@ __global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
   }
   const int row = row0 + i;
   const bool fix = A.to_fix > 0;
-  const uint64_t own_on = row0 + 16 <= e ? 0xffffull : (1ull << (e - row0)) - 1;
   typename M::F qf[1][NC], of[1][NC];
-  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, own_on, i, g);
-  load_frags<T, C, 1>(of, (const T*)A.dout, A.lddo, row0, own_on, i, g);
+  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
+  load_frags<T, C, 1>(of, (const T*)A.dout, A.lddo, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, row < e);
   float slope[H], lse[H], dsum[H], dsl[H];
 #pragma unroll
@@ -445,14 +546,15 @@ __global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
   float px = 0.f, py = 0.f, pz = 0.f;
   T* ks = (T*)s_w[wave];
   u4* ps = (u4*)(s_w[wave] + CK * RS * sizeof(T));
-  const float sc = A.cap > 0 ? A.scale / A.cap : A.scale * kLog2e, capl = A.cap * kLog2e;
+  const Score Z = score_of<T>(A);
 
   for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
     const uint64_t on = live<CK>(A, k0, e, lane, true);
     WaveTile<T, C, RS> tk;
-    tk.fetch((const T*)A.k, A.ldk, k0, on, lane);
+    tk.fetch((const T*)A.k, A.ldk, k0, e - k0, lane);
     typename M::F vf[NT][NC];
-    load_frags<T, C, NT>(vf, (const T*)A.v, A.ldv, k0, on, i, g);
+    load_frags<T, C, NT>(vf, (const T*)A.v, A.ldv, k0, e - k0, i, g);
+    if (on != all_live<CK>()) tk.clear(on, lane);
     if (A.pos && lane < CK) {
       const P3 p = load_pos(A, k0 + lane, (on >> lane) & 1);
       ps[lane] = u4{p.x, p.y, p.z, 0u};
@@ -484,7 +586,8 @@ __global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
         const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
         f4 p, dl;
         const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
-        pair_grad<T>(A, sc, capl, x, dp, r[t], slope[h], L, S, on, 16 * t + 4 * g, p, dl, ds[t]);
+        pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, on == all_live<CK>(), on, 16 * t + 4 * g, p, dl,
+                     ds[t]);
         if (A.pos) {
           const float sl = A.slope[h];
 #pragma unroll
@@ -574,7 +677,7 @@ __global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
   constexpr int WB = KW > 1 && SLAB > TILE ? SLAB : TILE;
   __shared__ __align__(16) char s_w[KW][WB];
   __shared__ float s_p[KW][3][16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = KW > 1 ? uniform(threadIdx.x >> 6) : 0, i = lane & 15, g = lane >> 4;
   int row0, s, e;
   if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
   const int row = row0 + i;
@@ -582,8 +685,8 @@ __global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
   const uint64_t own_on = live<16>(A, row0, e, lane, true);
   const bool own_live = (own_on >> i) & 1;
   typename M::F kf[1][NC], vf[1][NC];
-  load_frags<T, C, 1>(kf, (const T*)A.k, A.ldk, row0, own_on, i, g);
-  load_frags<T, C, 1>(vf, (const T*)A.v, A.ldv, row0, own_on, i, g);
+  load_frags<T, C, 1>(kf, (const T*)A.k, A.ldk, row0, e - row0, i, g);
+  load_frags<T, C, 1>(vf, (const T*)A.v, A.ldv, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, own_live);
   float slope[H];
 #pragma unroll
@@ -595,14 +698,18 @@ __global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
   T *qs = (T*)s_w[wave], *os = (T*)(s_w[wave] + TB);
   u4* ps = (u4*)(s_w[wave] + 2 * TB);
   float *ls = (float*)(s_w[wave] + 2 * TB + CK * 16), *ss = ls + H * CK;
-  const float sc = A.cap > 0 ? A.scale / A.cap : A.scale * kLog2e, capl = A.cap * kLog2e;
+  const Score Z = score_of<T>(A);
 
   if (own_on != 0) {
     for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
       const uint64_t on = live<CK>(A, k0, e, lane, false);
       WaveTile<T, C, RS> tq, to;
-      tq.fetch((const T*)A.q, A.ldq, k0, on, lane);
-      to.fetch((const T*)A.dout, A.lddo, k0, on, lane);
+      tq.fetch((const T*)A.q, A.ldq, k0, e - k0, lane);
+      to.fetch((const T*)A.dout, A.lddo, k0, e - k0, lane);
+      if (on != all_live<CK>()) {
+        tq.clear(on, lane);
+        to.clear(on, lane);
+      }
       if (lane < CK) {
         const bool l = (on >> lane) & 1;
         if (A.pos) {
@@ -632,6 +739,7 @@ __global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
         }
       }
       const uint64_t own_bits = own_live ? ~0ull : 0ull;
+      const bool all_own = own_on == 0xffffull;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         f4 p[NT], ds[NT];
@@ -647,7 +755,8 @@ __global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
           const f4 x = head_mma<T, DH, NC>(z, qf, kf[0], h, g), dp = head_mma<T, DH, NC>(z, of, vf[0], h, g);
           const f4 L = *(const f4*)(ls + h * CK + 16 * t + 4 * g), S = *(const f4*)(ss + h * CK + 16 * t + 4 * g);
           f4 dl;
-          pair_grad<T>(A, sc, capl, x, dp, r[t], slope[h], L, S, own_bits, 16 * t + 4 * g, p[t], dl, ds[t]);
+          pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, all_own, own_bits, 16 * t + 4 * g, p[t], dl,
+                       ds[t]);
           if (A.pos) {
             const float sl = A.slope[h];
 #pragma unroll
@@ -729,12 +838,16 @@ template <class T, int C, int DH>
 int launch_attn_c(const AttnArgs& A, bool split, int what, hipStream_t st) {
   const unsigned blocks = (unsigned)(A.n / 16 + A.n_struct);
   constexpr int KW = 4;
+  constexpr bool SAVES = sizeof(T) == 2;  // float32 has no second form
+  auto go = [&](void (*save)(AttnArgs), void (*plain)(AttnArgs), int threads) {
+    (A.lse ? save : plain)<<<blocks, threads, 0, st>>>(A);
+  };
   switch (what) {
     case 0:
       if (split)
-        k_attn_fwd<T, C, DH, KW><<<blocks, 64 * KW, 0, st>>>(A);
+        go(k_attn_fwd<T, C, DH, KW, SAVES>, k_attn_fwd<T, C, DH, KW, false>, 64 * KW);
       else
-        k_attn_fwd<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
+        go(k_attn_fwd<T, C, DH, 1, SAVES>, k_attn_fwd<T, C, DH, 1, false>, 64);
       break;
     case 1:
       if (split)
