@@ -72,20 +72,35 @@ __device__ __forceinline__ F ld16(const T* p, bool on) {
   return on ? *(const F*)p : zero16<F>();
 }
 
-// Transposed operand in tile order from an LDS matrix m[k][RS]: index = column, contracted =
-// rows k0 + 16 t + 4 g + r.  bf16: each group of 16 lanes reads four rows of 16 columns, lane
-// 4 r + s the four columns of chunk s of row r, and receives column i of the four rows
-// (ds_read_b64_tr_b16); cstep is the distance of the chunks (4: sixteen adjacent columns).
+// Order of the 16 rows of a tile that is read from LDS both by rows and transposed: index r of
+// the tile is LDS (or key) row pi(r).  bf16 transposed reads take four rows at once for each
+// group of 16 lanes; with a row stride of 4 banks (mod 32) those rows must be two apart to fall
+// on different banks, and any eight consecutive indices still cover eight adjacent rows, which
+// is what 16-byte reads by rows want.  float32 reads single words transposed: plain order.
+template <class T>
+__host__ __device__ constexpr int pi(int r) {
+  return sizeof(T) == 2 ? 8 * (r >> 3) + 2 * (r & 3) + ((r >> 2) & 1) : r;
+}
+template <class T>
+__host__ __device__ constexpr int pi_inv(int p) {
+  return sizeof(T) == 2 ? 8 * (p >> 3) + 4 * (p & 1) + ((p >> 1) & 3) : p;
+}
+static_assert(pi<uint16_t>(pi_inv<uint16_t>(7)) == 7 && pi_inv<uint16_t>(pi<uint16_t>(9)) == 9, "inverse");
+
+// Four rows row, row + 2, row + 4, row + 6 of sixteen adjacent columns, transposed: lane 4 r + s of
+// a 16-lane group reads columns 4 s .. 4 s + 3 of the r-th row, and lane i receives column i of the
+// four rows (ds_read_b64_tr_b16)
 template <int RS>
-__device__ __forceinline__ s4 ldt4(const uint16_t* m, int row, int col, int cstep, int lane) {
-  const uint16_t* p = m + (row + ((lane & 15) >> 2)) * RS + col + cstep * (lane & 3);
+__device__ __forceinline__ s4 ldt4(const uint16_t* m, int row, int col, int lane) {
+  const uint16_t* p = m + (row + 2 * ((lane & 15) >> 2)) * RS + col + 4 * (lane & 3);
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p);
 }
-// rows k0 + 16 t + 4 g + r, columns col + i
+// Transposed operand in tile order from an LDS matrix m[k][RS]: index = column col + i, contracted
+// = rows k0 + 16 t + pi(4 g + r)
 template <int RS>
 __device__ __forceinline__ s8 ldt(const uint16_t* m, int k0, int col, int lane) {
-  const int g = lane >> 4;
-  const s4 a = ldt4<RS>(m, k0 + 4 * g, col, 4, lane), b = ldt4<RS>(m, k0 + 16 + 4 * g, col, 4, lane);
+  const int r = k0 + pi<uint16_t>(4 * (lane >> 4));
+  const s4 a = ldt4<RS>(m, r, col, lane), b = ldt4<RS>(m, r + 16, col, lane);
   return s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 template <int RS>
@@ -93,11 +108,12 @@ __device__ __forceinline__ f4 ldt(const float* m, int k0, int col, int lane) {
   const float* p = m + (k0 + 4 * (lane >> 4)) * RS + col + (lane & 15);
   return f4{p[0], p[RS], p[2 * RS], p[3 * RS]};
 }
-// the same with rows in natural order, k0 + EV g + j
+// The same with the contracted index in natural order, k0 + EV g + j, of a matrix whose rows
+// were stored in the order pi within each 16
 template <int RS>
 __device__ __forceinline__ s8 ldtn(const uint16_t* m, int k0, int col, int lane) {
-  const int g = lane >> 4;
-  const s4 a = ldt4<RS>(m, k0 + 8 * g, col, 4, lane), b = ldt4<RS>(m, k0 + 8 * g + 4, col, 4, lane);
+  const int g = lane >> 4, r = k0 + 16 * (g >> 1) + 8 * (g & 1);
+  const s4 a = ldt4<RS>(m, r, col, lane), b = ldt4<RS>(m, r + 1, col, lane);
   return s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 template <int RS>
@@ -114,31 +130,15 @@ __device__ __forceinline__ int nat_row(int t, int i) {
   else
     return i;
 }
-
-// Transposed operands whose index i of tile t is column nat_row(t, i) of the CK-column group
-// cg, so that the NT result tiles of a lane hold EV consecutive columns; rows in tile order
-// (ldt_nat) or natural order (ldtn_nat)
-template <int RS>
-__device__ __forceinline__ s8 ldt_nat(const uint16_t* m, int k0, int cg, int t, int lane) {
-  const int g = lane >> 4;
-  const s4 a = ldt4<RS>(m, k0 + 4 * g, 32 * cg + 4 * t, 8, lane);
-  const s4 b = ldt4<RS>(m, k0 + 16 + 4 * g, 32 * cg + 4 * t, 8, lane);
-  return s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-}
-template <int RS>
-__device__ __forceinline__ f4 ldt_nat(const float* m, int k0, int cg, int, int lane) {
-  return ldt<RS>(m, k0, 16 * cg, lane);
-}
-template <int RS>
-__device__ __forceinline__ s8 ldtn_nat(const uint16_t* m, int k0, int cg, int t, int lane) {
-  const int g = lane >> 4;
-  const s4 a = ldt4<RS>(m, k0 + 8 * g, 32 * cg + 4 * t, 8, lane);
-  const s4 b = ldt4<RS>(m, k0 + 8 * g + 4, 32 * cg + 4 * t, 8, lane);
-  return s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-}
-template <int RS>
-__device__ __forceinline__ f4 ldtn_nat(const float* m, int k0, int cg, int, int lane) {
-  return ldt<RS>(m, k0, 16 * cg, lane);
+// where such a group's row x = nat_row(t, i) is stored to be read as 16 t + pi(i) (or 16 t + i)
+template <class T>
+__device__ __forceinline__ int nat_slot(int x, bool order_pi) {
+  if constexpr (sizeof(T) == 2) {
+    const int t = (x >> 2) & 1, i = 4 * (x >> 3) + (x & 3);
+    return 16 * t + (order_pi ? pi<T>(i) : i);
+  } else {
+    return x;
+  }
 }
 
 // A [ROWS][C] tile from global rows (stride ld) to LDS rows (stride RS), by NTH threads in
@@ -156,10 +156,15 @@ struct Tile {
     }
   }
   __device__ __forceinline__ void put(T* dst, int tid) const {
+    put(dst, tid, [](int r) { return r; });
+  }
+  // row r stored as row slot(r)
+  template <class SLOT>
+  __device__ __forceinline__ void put(T* dst, int tid, SLOT slot) const {
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
       const int x = tid + k * NTH, r = x / VPR, c = (x % VPR) * EV;
-      if (TOT % NTH == 0 || x < TOT) *(u4*)(dst + r * RS + c) = v[k];
+      if (TOT % NTH == 0 || x < TOT) *(u4*)(dst + slot(r) * RS + c) = v[k];
     }
   }
 };
@@ -173,6 +178,26 @@ __device__ __forceinline__ void st_row(T* p, const f4* t) {
 // four consecutive elements
 __device__ __forceinline__ void st4(float* p, f4 v) { *(f4*)p = v; }
 __device__ __forceinline__ void st4(uint16_t* p, f4 v) { *(u2*)p = u2{pk2bf(v.x, v.y), pk2bf(v.z, v.w)}; }
+
+// Sum over the four waves of a block of their [16 atoms][C] results, then rows out
+template <class T, int C, class ROW>
+__device__ __forceinline__ void join_waves(float* slab, int64_t a0, int64_t n, ROW row) {
+  using M = MF<T>;
+  constexpr int EV = M::EV, NT = M::NT, OS = C + 4;
+  __syncthreads();
+  for (int x = threadIdx.x; x < 16 * (C / EV); x += 256) {
+    const int r = x / (C / EV), c = (x % (C / EV)) * EV;
+    if (a0 + r >= n) break;
+    f4 o[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      o[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) o[t] += *(const f4*)(slab + (16 * w + r) * OS + c + 4 * t);
+    }
+    row(a0 + r, c, o);
+  }
+}
 
 // orders the LDS accesses of one wave (its lanes exchange data through LDS it alone uses)
 __device__ __forceinline__ void wave_sync() {

@@ -29,8 +29,14 @@ inline int check_width(const char* who, int32_t channels, int32_t feat_dtype) {
                        " must be 16-byte aligned, with a row stride of at least their width and a multiple of 16 bytes"); \
   } while (0)
 
-// out[j] = sum over s of part[s][j], j < N, in a fixed order; part rows are ldp floats apart
-int reduce_rows(const float* part, int64_t S, int64_t N, int64_t ldp, void* out, bool bf16, hipStream_t st);
+// out[j] = sum over s < S of part[s * ldp + off + j], j < N, added in a fixed order; up to three
+// such segments of one set of partials in one launch.  S = 0 writes zeros.
+struct Segment {
+  int64_t off, N;
+  void* out;  // null: no such segment
+  bool bf16;
+};
+int reduce_rows(const float* part, int64_t S, int64_t ldp, const Segment* seg, int nseg, hipStream_t st);
 
 }  // namespace ops
 }  // namespace mdmp

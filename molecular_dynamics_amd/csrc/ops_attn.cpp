@@ -114,8 +114,10 @@ extern "C" int mp_structure_attention_bwd(const mp_attention_args* a, const void
   MP_TRY(ops::attn_args("mp_structure_attention_bwd", a, A));
   if ((dpos || dslope) && !a->pos) return arg_error("mp_structure_attention_bwd: dpos and dslope need pos and slope");
   const int C = a->channels, H = a->heads, dt = a->feat_dtype;
-  if (a->n == 0 || a->n_struct == 0)  // no pair: the sum over nothing
-    return dslope ? ops::reduce_rows(nullptr, 0, H, H, dslope, false, st) : MP_OK;
+  if (a->n == 0 || a->n_struct == 0) {  // no pair: the sum over nothing
+    const ops::Segment none{0, H, dslope, false};
+    return ops::reduce_rows(nullptr, 0, H, &none, 1, st);
+  }
   if (!out || !saved || !dout || !dq || !dk || !dv)
     return arg_error("mp_structure_attention_bwd: null out, saved, dout, dq, dk or dv");
   if (lddo > ops::kMaxLd) return arg_error("mp_structure_attention_bwd: row stride above 2^24");
@@ -140,6 +142,6 @@ extern "C" int mp_structure_attention_bwd(const mp_attention_args* a, const void
   ProfScope p("structure_attention_bwd", st);
   MP_TRY(ops::launch(a, A, 1, st));
   MP_TRY(ops::launch(a, A, 2, st));
-  if (dslope) MP_TRY(ops::reduce_rows(part, slots, H, H, dslope, false, st));
-  return MP_OK;
+  const ops::Segment seg{0, H, dslope, false};
+  return ops::reduce_rows(part, slots, H, &seg, 1, st);
 }

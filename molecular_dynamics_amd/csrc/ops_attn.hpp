@@ -153,15 +153,15 @@ struct WaveTile {
     for (int j = 0; j < IT; ++j) *(u4*)(dst + (lane / VPR + j * RJ) * RS + (lane % VPR) * EV) = v[j];
   }
 };
-// chunks c0 .. c1 - 1 of the operands of NTL tiles
-template <class T, int C, int NTL>
+// chunks c0 .. c1 - 1 of the operands of NTL tiles; ORDER: rows in the order pi
+template <class T, int C, int NTL, bool ORDER>
 __device__ __forceinline__ void load_frags(typename MF<T>::F (&f)[NTL][C / MF<T>::CK], const T* src, int64_t ld,
                                            int64_t k0, int rows, int i, int g, int c0 = 0, int c1 = C / MF<T>::CK) {
   using M = MF<T>;
   const T* p = src + k0 * ld;
 #pragma unroll
   for (int t = 0; t < NTL; ++t) {
-    uint32_t r = 16 * t + i;
+    uint32_t r = 16 * t + (ORDER ? pi<T>(i) : i);
     if (rows < 16 * NTL) r = min(r, (uint32_t)rows - 1);
     const uint32_t off = r * (uint32_t)ld + M::EV * g;
 #pragma unroll
@@ -255,8 +255,9 @@ void k_attn_fwd(AttnArgs A) {
   if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
   const int row = row0 + i;
   const bool fix = A.to_fix > 0, dist = A.pos != nullptr;
+  const int slot = lane / 16 * 16 + pi_inv<T>(lane % 16);  // where index `lane` of a step is kept
   typename M::F qf[1][NC];
-  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
+  load_frags<T, C, 1, false>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, row < e);
   // thr: a score above it (in the reference m) raises the reference; -inf until there is one
   float m[H], thr[H];
@@ -288,7 +289,7 @@ void k_attn_fwd(AttnArgs A) {
   };
   if (s + CK * wave < e) {
     fetch_v(s + CK * wave, on);
-    load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, s + CK * wave, e - s - CK * wave, i, g);
+    load_frags<T, C, NT, true>(kf, (const T*)A.k, A.ldk, s + CK * wave, e - s - CK * wave, i, g);
   }
 
   for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
@@ -297,17 +298,16 @@ void k_attn_fwd(AttnArgs A) {
     const uint64_t on_n = live<CK>(A, kn, e, lane, true);
     if (part) tv.clear(on, lane);
     tv.put(vs, lane);
-    if (dist && lane < CK) ps[lane] = u4{kp.x, kp.y, kp.z, 0u};
+    if (dist && lane < CK) ps[slot] = u4{kp.x, kp.y, kp.z, 0u};
     wave_sync();
     if (kn < e) fetch_v(kn, on_n);
-    const uint32_t bits = (uint32_t)on >> (4 * g);
     bool lv[NT][4];
     f4 r[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       r[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) lv[t][q] = (bits >> (16 * t + q)) & 1;
+      for (int q = 0; q < 4; ++q) lv[t][q] = (on >> (16 * t + pi<T>(4 * g + q))) & 1;
     }
     if (dist) {
 #pragma unroll
@@ -325,7 +325,7 @@ void k_attn_fwd(AttnArgs A) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
       if (kn < e)
-        load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, kn, e - kn, i, g, chunk_first<T, DH>(h), chunk_end<T, DH>(h));
+        load_frags<T, C, NT, true>(kf, (const T*)A.k, A.ldk, kn, e - kn, i, g, chunk_first<T, DH>(h), chunk_end<T, DH>(h));
       const float sl = dist ? A.slope[h] * (kLog2e * A.unit) : 0.f;
       if (Z.cap) {
 #pragma unroll
@@ -460,7 +460,7 @@ void k_attn_fwd(AttnArgs A) {
 //   p = 2^(x - lse), dl = p (dp - dsum); ds = dl times the cap's slope 1 - tanh^2
 template <class T>
 __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4 dp, f4 r, float slope, f4 lse, f4 dsum,
-                                          bool all, uint64_t on, int k, f4& p, f4& dl, f4& ds) {
+                                          bool all, uint64_t on, f4& p, f4& dl, f4& ds) {
   f4 f;
   if (Z.cap) {
 #pragma unroll
@@ -482,7 +482,7 @@ __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4
   if (!all) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (!((on >> (k + q)) & 1)) p[q] = dl[q] = ds[q] = 0.f;
+      if (!((on >> (pi<T>(4 + q) - pi<T>(4))) & 1)) p[q] = dl[q] = ds[q] = 0.f;
   }
 }
 
@@ -491,7 +491,7 @@ __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4
 // side of the position gradient, and the block's partial of dslope.  out enters unrounded (o32)
 // so that dsum, and with it the float32 gradients, do not carry bf16's rounding.
 template <class T, int C, int DH, int KW>
-__global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
+__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 128 ? 2 : 3))) void k_attn_row(AttnArgs A) {
   using M = MF<T>;
   using D = AttnDims<T, C>;
   constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
@@ -508,9 +508,10 @@ __global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
   }
   const int row = row0 + i;
   const bool fix = A.to_fix > 0;
+  const int slot = lane / 16 * 16 + pi_inv<T>(lane % 16);  // where index `lane` of a step is kept
   typename M::F qf[1][NC], of[1][NC];
-  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
-  load_frags<T, C, 1>(of, (const T*)A.dout, A.lddo, row0, e - row0, i, g);
+  load_frags<T, C, 1, false>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
+  load_frags<T, C, 1, false>(of, (const T*)A.dout, A.lddo, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, row < e);
   float slope[H], lse[H], dsum[H], dsl[H];
 #pragma unroll
@@ -553,11 +554,11 @@ __global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
     WaveTile<T, C, RS> tk;
     tk.fetch((const T*)A.k, A.ldk, k0, e - k0, lane);
     typename M::F vf[NT][NC];
-    load_frags<T, C, NT>(vf, (const T*)A.v, A.ldv, k0, e - k0, i, g);
+    load_frags<T, C, NT, true>(vf, (const T*)A.v, A.ldv, k0, e - k0, i, g);
     if (on != all_live<CK>()) tk.clear(on, lane);
     if (A.pos && lane < CK) {
       const P3 p = load_pos(A, k0 + lane, (on >> lane) & 1);
-      ps[lane] = u4{p.x, p.y, p.z, 0u};
+      ps[slot] = u4{p.x, p.y, p.z, 0u};
     }
     tk.put(ks, lane);
     wave_sync();
@@ -581,13 +582,12 @@ __global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
       for (int t = 0; t < NT; ++t) {
         typename M::F kf[NC];
 #pragma unroll
-        for (int ch = 0; ch < NC; ++ch) kf[ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
+        for (int ch = 0; ch < NC; ++ch) kf[ch] = *(const typename M::F*)(ks + (16 * t + pi<T>(i)) * RS + ch * CK + EV * g);
         const f4 z = f4{0.f, 0.f, 0.f, 0.f};
         const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
         f4 p, dl;
         const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
-        pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, on == all_live<CK>(), on, 16 * t + 4 * g, p, dl,
-                     ds[t]);
+        pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, on == all_live<CK>(), on >> (16 * t + pi<T>(4 * g)), p, dl, ds[t]);
         if (A.pos) {
           const float sl = A.slope[h];
 #pragma unroll
@@ -668,7 +668,7 @@ __global__ __launch_bounds__(64 * KW) void k_attn_row(AttnArgs A) {
 // For 16 keys: dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij dout_i, and the keys' side of the
 // position gradient, added to what the row pass wrote.
 template <class T, int C, int DH, int KW>
-__global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
+__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 128 ? 2 : 3))) void k_attn_col(AttnArgs A) {
   using M = MF<T>;
   using D = AttnDims<T, C>;
   constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
@@ -682,11 +682,12 @@ __global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
   if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
   const int row = row0 + i;
   const bool fix = A.to_fix > 0;
+  const int slot = lane / 16 * 16 + pi_inv<T>(lane % 16);  // where index `lane` of a step is kept
   const uint64_t own_on = live<16>(A, row0, e, lane, true);
   const bool own_live = (own_on >> i) & 1;
   typename M::F kf[1][NC], vf[1][NC];
-  load_frags<T, C, 1>(kf, (const T*)A.k, A.ldk, row0, e - row0, i, g);
-  load_frags<T, C, 1>(vf, (const T*)A.v, A.ldv, row0, e - row0, i, g);
+  load_frags<T, C, 1, false>(kf, (const T*)A.k, A.ldk, row0, e - row0, i, g);
+  load_frags<T, C, 1, false>(vf, (const T*)A.v, A.ldv, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, own_live);
   float slope[H];
 #pragma unroll
@@ -714,12 +715,12 @@ __global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
         const bool l = (on >> lane) & 1;
         if (A.pos) {
           const P3 p = load_pos(A, k0 + lane, l);
-          ps[lane] = u4{p.x, p.y, p.z, 0u};
+          ps[slot] = u4{p.x, p.y, p.z, 0u};
         }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          ls[h * CK + lane] = l ? A.lse[(int64_t)(k0 + lane) * H + h] : INFINITY;
-          ss[h * CK + lane] = l ? A.dsum[(int64_t)(k0 + lane) * H + h] : 0.f;
+          ls[h * CK + slot] = l ? A.lse[(int64_t)(k0 + lane) * H + h] : INFINITY;
+          ss[h * CK + slot] = l ? A.dsum[(int64_t)(k0 + lane) * H + h] : 0.f;
         }
       }
       tq.put(qs, lane);
@@ -748,15 +749,14 @@ __global__ __launch_bounds__(64 * KW) void k_attn_col(AttnArgs A) {
           typename M::F qf[NC], of[NC];
 #pragma unroll
           for (int ch = 0; ch < NC; ++ch) {
-            qf[ch] = *(const typename M::F*)(qs + (16 * t + i) * RS + ch * CK + EV * g);
-            of[ch] = *(const typename M::F*)(os + (16 * t + i) * RS + ch * CK + EV * g);
+            qf[ch] = *(const typename M::F*)(qs + (16 * t + pi<T>(i)) * RS + ch * CK + EV * g);
+            of[ch] = *(const typename M::F*)(os + (16 * t + pi<T>(i)) * RS + ch * CK + EV * g);
           }
           const f4 z = f4{0.f, 0.f, 0.f, 0.f};
           const f4 x = head_mma<T, DH, NC>(z, qf, kf[0], h, g), dp = head_mma<T, DH, NC>(z, of, vf[0], h, g);
           const f4 L = *(const f4*)(ls + h * CK + 16 * t + 4 * g), S = *(const f4*)(ss + h * CK + 16 * t + 4 * g);
           f4 dl;
-          pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, all_own, own_bits, 16 * t + 4 * g, p[t], dl,
-                       ds[t]);
+          pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, all_own, own_bits, p[t], dl, ds[t]);
           if (A.pos) {
             const float sl = A.slope[h];
 #pragma unroll

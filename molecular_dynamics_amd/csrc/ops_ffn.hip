@@ -17,24 +17,47 @@ struct FfnArgs {
 
 constexpr int pad_of(int esize) { return 16 / esize; }
 
-// One chunk of CK hidden units of the three matrices, in LDS: rows of Wg and Wu (CK x C)
-// and columns of Wd (C x CK)
-template <class T, int C>
+// One chunk of CK hidden units of the three matrices, in LDS: rows of Wg and Wu (CK x C) and
+// columns of Wd (C x CK), staged by NTH threads.  Rows are stored where the reads of 16
+// consecutive indices fall on different banks:
+//   Wg, Wu   hidden unit nat_row(t, i) in row 16 t + i (forward: read by rows only), or in row
+//            16 t + pi(i) (backward: also read transposed)
+//   Wd       forward: channel 16 NT p + nat_row(t, i) in row 16 (NT p + t) + i; backward (read
+//            transposed only): rows in the order pi, hidden unit nat_row(t, i) in column 16 t + i
+template <class T, int C, int NTH, bool BWD>
 struct Chunk {
   using M = MF<T>;
   static constexpr int CK = M::CK, RS = C + pad_of(sizeof(T)), RD = CK + pad_of(sizeof(T));
   static constexpr int SIZE = 2 * CK * RS + C * RD;
-  Tile<T, CK, C, RS, 256> g, u;
-  Tile<T, C, CK, RD, 256> d;
+  Tile<T, CK, C, RS, NTH> g, u;
+  Tile<T, C, CK, RD, NTH> d;
   __device__ __forceinline__ void fetch(const FfnArgs& A, int h0, int tid) {
     g.fetch((const T*)A.wg + (int64_t)h0 * C, C, CK, tid);
     u.fetch((const T*)A.wu + (int64_t)h0 * C, C, CK, tid);
     d.fetch((const T*)A.wd + h0, A.hidden, C, tid);
   }
   __device__ __forceinline__ void put(T* s, int tid) const {
-    g.put(s, tid);
-    u.put(s + CK * RS, tid);
-    d.put(s + 2 * CK * RS, tid);
+    auto slot = [](int r) { return nat_slot<T>(r, BWD); };
+    g.put(s, tid, slot);
+    u.put(s + CK * RS, tid, slot);
+    T* sd = s + 2 * CK * RS;
+    if constexpr (!BWD) {
+      d.put(sd, tid, [](int r) { return r / CK * CK + nat_slot<T>(r % CK, false); });
+    } else {
+      using TD = Tile<T, C, CK, RD, NTH>;
+#pragma unroll
+      for (int k = 0; k < TD::IT; ++k) {
+        const int x = tid + k * NTH, r = x / TD::VPR, c = (x % TD::VPR) * M::EV;
+        if (TD::TOT % NTH != 0 && x >= TD::TOT) break;
+        T* q = sd + (r / 16 * 16 + pi<T>(r % 16)) * RD;
+        if constexpr (sizeof(T) == 2) {  // units c .. c + 3 and c + 4 .. c + 7: tiles 0 and 1
+          *(u2*)(q + c / 2) = u2{d.v[k][0], d.v[k][1]};
+          *(u2*)(q + 16 + c / 2) = u2{d.v[k][2], d.v[k][3]};
+        } else {
+          *(u4*)(q + c) = d.v[k];
+        }
+      }
+    }
   }
 };
 
@@ -56,17 +79,20 @@ __device__ __forceinline__ void load_rows(typename MF<T>::F (&f)[AT][C / MF<T>::
 // ends with EV consecutive hidden units of its atom, which after act(.) * (.) are the
 // operand of D[c][a] += Wd h as they stand.  Hidden units live in registers only.  The
 // weights of a chunk are shared by the block's four waves through LDS (two buffers, the next
-// chunk's loads in flight during the products).  Bound: the matrix products and, beside
-// them, the sigmoid of every hidden unit (exp and reciprocal at a quarter of the VALU rate).
-template <class T, int C, int AT>
-__global__ __launch_bounds__(256) void k_ffn(FfnArgs A) {
+// chunk's loads in flight during the products).  SPLIT (few rows): the four waves take the same
+// 16 atoms and every fourth chunk each, weights straight from L2, and their sums are joined.
+// Bound: the matrix products and, beside them, the sigmoid of every hidden unit (exp and
+// reciprocal at a quarter of the VALU rate).
+template <class T, int C, int AT, bool SPLIT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn(FfnArgs A) {
   using M = MF<T>;
-  using CH = Chunk<T, C>;
-  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = CH::RS, RD = CH::RD;
-  extern __shared__ __align__(16) char s_raw[];
+  using CH = Chunk<T, C, 256, false>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = SPLIT ? C : CH::RS, OS = C + 4;
+  constexpr int LDS = SPLIT ? 64 * OS * 4 : 2 * CH::SIZE * (int)sizeof(T);
+  __shared__ __align__(16) char s_raw[LDS];
   T* s = (T*)s_raw;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int64_t a0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
+  const int64_t a0 = SPLIT ? (int64_t)blockIdx.x * 16 : ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
   typename M::F xf[AT][NC];
   load_rows<T, C, AT>(xf, A.x, A.ldx, a0, A.n, i, g);
   f4 acc[AT][NC][NT];
@@ -77,19 +103,29 @@ __global__ __launch_bounds__(256) void k_ffn(FfnArgs A) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[at][p][t] = f4{0.f, 0.f, 0.f, 0.f};
   CH ck;
-  ck.fetch(A, 0, threadIdx.x);
-  ck.put(s, threadIdx.x);
-  __syncthreads();
+  if constexpr (!SPLIT) {
+    ck.fetch(A, 0, threadIdx.x);
+    ck.put(s, threadIdx.x);
+    __syncthreads();
+  }
   int b = 0;
-  for (int h0 = 0; h0 < A.hidden; h0 += CK, b ^= 1) {
-    const T *wg = s + b * CH::SIZE, *wu = wg + CK * RS, *wd = wu + CK * RS;
-    if (h0 + CK < A.hidden) ck.fetch(A, h0 + CK, threadIdx.x);
+  for (int h0 = SPLIT ? CK * wave : 0; h0 < A.hidden; h0 += SPLIT ? 4 * CK : CK, b ^= 1) {
+    const T *wg, *wu, *wd;
+    int ldd;  // row stride of Wd
+    if constexpr (SPLIT) {
+      wg = (const T*)A.wg + (int64_t)h0 * C, wu = (const T*)A.wu + (int64_t)h0 * C, wd = (const T*)A.wd + h0;
+      ldd = A.hidden;
+    } else {
+      wg = s + b * CH::SIZE, wu = wg + CK * RS, wd = wu + CK * RS;
+      ldd = CH::RD;
+      ck.fetch(A, min(h0 + CK, A.hidden - CK), threadIdx.x);
+    }
     f4 zg[AT][NT], zu[AT][NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int at = 0; at < AT; ++at) zg[at][t] = zu[at][t] = f4{0.f, 0.f, 0.f, 0.f};
-      const int row = nat_row<T>(t, i) * RS + EV * g;
+      const int row = (SPLIT ? nat_row<T>(t, i) : 16 * t + i) * RS + EV * g;
 #pragma unroll
       for (int ch = 0; ch < NC; ++ch) {
         const typename M::F fg = *(const typename M::F*)(wg + row + ch * CK);
@@ -114,27 +150,39 @@ __global__ __launch_bounds__(256) void k_ffn(FfnArgs A) {
     for (int p = 0; p < NC; ++p)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const typename M::F f = *(const typename M::F*)(wd + (p * CK + nat_row<T>(t, i)) * RD + EV * g);
+        const int row = p * CK + (SPLIT ? nat_row<T>(t, i) : 16 * t + i);
+        const typename M::F f = *(const typename M::F*)(wd + (int64_t)row * ldd + EV * g);
 #pragma unroll
         for (int at = 0; at < AT; ++at) acc[at][p][t] = M::mma(acc[at][p][t], f, h[at]);
       }
-    if (h0 + CK < A.hidden) ck.put(s + (b ^ 1) * CH::SIZE, threadIdx.x);
-    __syncthreads();
+    if constexpr (!SPLIT) {
+      ck.put(s + (b ^ 1) * CH::SIZE, threadIdx.x);
+      __syncthreads();
+    }
   }
+  auto out = [&](int64_t a, int c, f4* o) {
+    if (A.res) {
+      f4 q[NT];
+      M::unpack(*(const typename M::F*)((const T*)A.res + a * A.ldr + c), q);
 #pragma unroll
-  for (int at = 0; at < AT; ++at) {
-    const int64_t a = a0 + 16 * at + i;
-    if (a >= A.n) continue;
+      for (int t = 0; t < NT; ++t) o[t] += q[t];
+    }
+    st_row<T>((T*)A.y + a * A.ldy + c, o);
+  };
+  if constexpr (SPLIT) {
+    float* slab = (float*)s_raw + (16 * wave + i) * OS;
 #pragma unroll
-    for (int p = 0; p < NC; ++p) {
-      const int c = p * CK + EV * g;
-      if (A.res) {
-        f4 q[NT];
-        M::unpack(*(const typename M::F*)((const T*)A.res + a * A.ldr + c), q);
+    for (int p = 0; p < NC; ++p)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[at][p][t] += q[t];
-      }
-      st_row<T>((T*)A.y + a * A.ldy + c, acc[at][p]);
+      for (int t = 0; t < NT; ++t) *(f4*)(slab + p * CK + EV * g + 4 * t) = acc[0][p][t];
+    join_waves<T, C>((float*)s_raw, a0, A.n, out);
+  } else {
+#pragma unroll
+    for (int at = 0; at < AT; ++at) {
+      const int64_t a = a0 + 16 * at + i;
+      if (a >= A.n) continue;
+#pragma unroll
+      for (int p = 0; p < NC; ++p) out(a, p * CK + EV * g, acc[at][p]);
     }
   }
 }
@@ -151,45 +199,54 @@ __device__ __forceinline__ void hidden_grad(float zg, float zu, float dh, ActAB 
 
 // dx: the forward's first two products, dh = Wd^T dy (Wd read transposed from the same LDS
 // chunk), the hidden gradients in registers, and D[c][a] += Wg^T dzg + Wu^T dzu (the same
-// rows of Wg and Wu, read transposed).
-template <class T, int C, int AT>
-__global__ __launch_bounds__(256) void k_ffn_dx(FfnArgs A) {
+// rows of Wg and Wu, read transposed).  SPLIT as in the forward, each wave with a chunk of its
+// own in LDS.
+template <class T, int C, int AT, bool SPLIT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(SPLIT ? 1 : 2, 2))) void k_ffn_dx(FfnArgs A) {
   using M = MF<T>;
-  using CH = Chunk<T, C>;
-  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = CH::RS, RD = CH::RD;
-  extern __shared__ __align__(16) char s_raw[];
+  using CH = Chunk<T, C, SPLIT ? 64 : 256, true>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = CH::RS, RD = CH::RD, OS = C + 4;
+  constexpr int SLAB = SPLIT ? 64 * OS * 4 : 0, CHUNKS = (SPLIT ? 4 : 2) * CH::SIZE * (int)sizeof(T);
+  __shared__ __align__(16) char s_raw[SLAB > CHUNKS ? SLAB : CHUNKS];
   T* s = (T*)s_raw;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int64_t a0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
+  const int64_t a0 = SPLIT ? (int64_t)blockIdx.x * 16 : ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
   typename M::F xf[AT][NC], df[AT][NC];
   load_rows<T, C, AT>(xf, A.x, A.ldx, a0, A.n, i, g);
   load_rows<T, C, AT>(df, A.dy, A.ldy, a0, A.n, i, g);
-  f4 acc[AT][NC][NT];
+  f4 acc[AT][C / 16];
 #pragma unroll
   for (int at = 0; at < AT; ++at)
 #pragma unroll
-    for (int p = 0; p < NC; ++p)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[at][p][t] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int ct = 0; ct < C / 16; ++ct) acc[at][ct] = f4{0.f, 0.f, 0.f, 0.f};
   CH ck;
-  ck.fetch(A, 0, threadIdx.x);
-  ck.put(s, threadIdx.x);
-  __syncthreads();
+  if constexpr (!SPLIT) {
+    ck.fetch(A, 0, threadIdx.x);
+    ck.put(s, threadIdx.x);
+    __syncthreads();
+  }
   int b = 0;
-  for (int h0 = 0; h0 < A.hidden; h0 += CK, b ^= 1) {
-    const T *wg = s + b * CH::SIZE, *wu = wg + CK * RS, *wd = wu + CK * RS;
-    if (h0 + CK < A.hidden) ck.fetch(A, h0 + CK, threadIdx.x);
+  for (int h0 = SPLIT ? CK * wave : 0; h0 < A.hidden; h0 += SPLIT ? 4 * CK : CK, b ^= 1) {
+    T* buf = s + (SPLIT ? wave : b) * CH::SIZE;
+    if constexpr (SPLIT) {
+      ck.fetch(A, h0, lane);
+      ck.put(buf, lane);
+      wave_sync();
+    } else {
+      ck.fetch(A, min(h0 + CK, A.hidden - CK), threadIdx.x);
+    }
+    const T *wg = buf, *wu = wg + CK * RS, *wd = wu + CK * RS;
     f4 zg[AT][NT], zu[AT][NT], dh[AT][NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int at = 0; at < AT; ++at) zg[at][t] = zu[at][t] = dh[at][t] = f4{0.f, 0.f, 0.f, 0.f};
-      const int row = nat_row<T>(t, i) * RS + EV * g;
+      const int row = (16 * t + pi<T>(i)) * RS + EV * g;
 #pragma unroll
       for (int ch = 0; ch < NC; ++ch) {
         const typename M::F fg = *(const typename M::F*)(wg + row + ch * CK);
         const typename M::F fu = *(const typename M::F*)(wu + row + ch * CK);
-        const typename M::F fd = ldtn_nat<RD>(wd, ch * CK, 0, t, lane);
+        const typename M::F fd = ldtn<RD>(wd, ch * CK, 16 * t, lane);
 #pragma unroll
         for (int at = 0; at < AT; ++at) {
           zg[at][t] = M::mma(zg[at][t], fg, xf[at][ch]);
@@ -213,24 +270,35 @@ __global__ __launch_bounds__(256) void k_ffn_dx(FfnArgs A) {
       dg[at] = M::pack(zg[at]);
       du[at] = M::pack(zu[at]);
     }
+    // hidden unit EV g + j of the operands is row 16 t + pi(4 g + r): tile order
 #pragma unroll
-    for (int p = 0; p < NC; ++p)
+    for (int ct = 0; ct < C / 16; ++ct) {
+      const typename M::F fg = ldt<RS>(wg, 0, 16 * ct, lane), fu = ldt<RS>(wu, 0, 16 * ct, lane);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const typename M::F fg = ldtn_nat<RS>(wg, 0, p, t, lane), fu = ldtn_nat<RS>(wu, 0, p, t, lane);
-#pragma unroll
-        for (int at = 0; at < AT; ++at)
-          acc[at][p][t] = M::mma(M::mma(acc[at][p][t], fg, dg[at]), fu, du[at]);
-      }
-    if (h0 + CK < A.hidden) ck.put(s + (b ^ 1) * CH::SIZE, threadIdx.x);
-    __syncthreads();
+      for (int at = 0; at < AT; ++at) acc[at][ct] = M::mma(M::mma(acc[at][ct], fg, dg[at]), fu, du[at]);
+    }
+    if constexpr (SPLIT) {
+      wave_sync();
+    } else {
+      ck.put(s + (b ^ 1) * CH::SIZE, threadIdx.x);
+      __syncthreads();
+    }
   }
+  if constexpr (SPLIT) {
+    __syncthreads();  // the slabs lie over the chunks
+    float* slab = (float*)s_raw + (16 * wave + i) * OS;
 #pragma unroll
-  for (int at = 0; at < AT; ++at) {
-    const int64_t a = a0 + 16 * at + i;
-    if (a >= A.n) continue;
+    for (int ct = 0; ct < C / 16; ++ct) *(f4*)(slab + 16 * ct + 4 * g) = acc[0][ct];
+    join_waves<T, C>((float*)s_raw, a0, A.n,
+                     [&](int64_t a, int c, f4* o) { st_row<T>((T*)A.dx + a * A.lddx + c, o); });
+  } else {
 #pragma unroll
-    for (int p = 0; p < NC; ++p) st_row<T>((T*)A.dx + a * A.lddx + p * CK + EV * g, acc[at][p]);
+    for (int at = 0; at < AT; ++at) {
+      const int64_t a = a0 + 16 * at + i;
+      if (a >= A.n) continue;
+#pragma unroll
+      for (int ct = 0; ct < C / 16; ++ct) st4((T*)A.dx + a * A.lddx + 16 * ct + 4 * g, acc[at][ct]);
+    }
   }
 }
 
@@ -240,7 +308,7 @@ __global__ __launch_bounds__(256) void k_ffn_dx(FfnArgs A) {
 //   dWg[hid][c] += dzg^T x,  dWu[hid][c] += dzu^T x,  dWd[c][hid] += dy^T h,
 // x and dy read transposed from LDS.
 template <class T, int C>
-__global__ __launch_bounds__(256) void k_ffn_dw(FfnArgs A) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn_dw(FfnArgs A) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + pad_of(sizeof(T));
   __shared__ __align__(16) T s_x[2][CK * RS];
@@ -287,7 +355,7 @@ __global__ __launch_bounds__(256) void k_ffn_dw(FfnArgs A) {
       for (int t = 0; t < NT; ++t) {
         f4 dh = f4{0.f, 0.f, 0.f, 0.f};
         zg[t] = zu[t] = dh;
-        const int row = (16 * t + i) * RS + EV * g;
+        const int row = (16 * t + pi<T>(i)) * RS + EV * g;
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
           const typename M::F fx = *(const typename M::F*)(xs + row + ch * CK);
@@ -344,25 +412,24 @@ int64_t ffn_splits(int64_t n, int hidden) {
 template <class T, int C>
 int launch_ffn_c(FfnArgs A, int what, hipStream_t st) {
   constexpr int AT = sizeof(T) == 2 ? 2 : 1;
-  constexpr size_t lds = 2 * Chunk<T, C>::SIZE * sizeof(T);
-  static_assert(lds <= 65536, "two weight chunks in LDS");
   if (what == 2) {
     const int64_t S = ffn_splits(A.n, A.hidden);
     A.rows_per_split = cdiv(cdiv(A.n, S), MF<T>::CK) * MF<T>::CK;
     k_ffn_dw<T, C><<<dim3((unsigned)cdiv(A.hidden, 64), (unsigned)S), 256, 0, st>>>(A);
   } else {
+    // few rows: the hidden units are split over the waves of a block
     const bool few = cdiv(A.n, 64 * AT) < 256;
-    const unsigned blocks = (unsigned)cdiv(A.n, few ? 64 : 64 * AT);
+    const unsigned blocks = (unsigned)cdiv(A.n, few ? 16 : 64 * AT);
     if (what == 0) {
       if (few)
-        k_ffn<T, C, 1><<<blocks, 256, lds, st>>>(A);
+        k_ffn<T, C, 1, true><<<blocks, 256, 0, st>>>(A);
       else
-        k_ffn<T, C, AT><<<blocks, 256, lds, st>>>(A);
+        k_ffn<T, C, AT, false><<<blocks, 256, 0, st>>>(A);
     } else {
       if (few)
-        k_ffn_dx<T, C, 1><<<blocks, 256, lds, st>>>(A);
+        k_ffn_dx<T, C, 1, true><<<blocks, 256, 0, st>>>(A);
       else
-        k_ffn_dx<T, C, AT><<<blocks, 256, lds, st>>>(A);
+        k_ffn_dx<T, C, AT, false><<<blocks, 256, 0, st>>>(A);
     }
   }
   MP_CHECK_LAUNCH();
@@ -460,7 +527,6 @@ extern "C" int mp_gated_ffn_bwd(int32_t n, int32_t channels, int32_t hidden, int
   if (!grads) return MP_OK;
   if (n > 0) MP_TRY(ops::launch_ffn(A, channels, dt == 1, 2, st));
   const int64_t S = n > 0 ? ops::ffn_splits(n, hidden) : 0, N = (int64_t)channels * hidden;
-  void* out[3] = {dwg, dwu, dwd};
-  for (int k = 0; k < 3; ++k) MP_TRY(ops::reduce_rows(A.part + k * N, S, N, 3 * N, out[k], dt == 1, st));
-  return MP_OK;
+  const ops::Segment seg[3] = {{0, N, dwg, dt == 1}, {N, N, dwu, dt == 1}, {2 * N, N, dwd, dt == 1}};
+  return ops::reduce_rows(A.part, S, 3 * N, seg, 3, st);
 }

@@ -13,7 +13,7 @@ struct LinArgs {
   const void *x, *w, *res, *dy;
   const float* bias;
   void *y, *dx;
-  float *part, *part_b;  // [splits][out][C], [splits][out]
+  float* part;           // [splits][out C + out]: dW, then dbias
   int64_t rows_per_split;
 };
 
@@ -96,87 +96,88 @@ __global__ __launch_bounds__(256) void k_linear(LinArgs A) {
 // dx: D[c][a] = sum_o W[o][c] dz[a][o], dz = dy act'(z), z formed again by the forward's
 // product.  Both operands of dz sit as EV consecutive outputs per lane (natural order), so
 // dz goes from result to operand in registers.  W passes through LDS CK rows at a time,
-// read there by rows (z) and transposed (dx).  Bound: HBM (dy rows) without an activation.
-template <class T, int C, int AT>
-__global__ __launch_bounds__(256) void k_linear_dx(LinArgs A) {
+// output nat_row(t, i) in row 16 t + pi(i), read there by rows (z) and transposed (dx).
+// SPLIT (few rows): the four waves take the same 16 atoms and every fourth group of outputs,
+// each with rows of its own in LDS, and their sums are joined.
+// Bound: HBM (dy rows) without an activation.
+template <class T, int C, bool SPLIT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_linear_dx(LinArgs A) {
   using M = MF<T>;
-  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK, RS = C + PADE(sizeof(T)), NG = C / M::CK;
-  __shared__ __align__(16) T s_w[2][OG * RS];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int64_t a0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
-  typename M::F xf[AT][NC];
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK, RS = C + PADE(sizeof(T)), OS = C + 4;
+  constexpr int ROWS = (SPLIT ? 4 : 2) * OG * RS * (int)sizeof(T), SLAB = SPLIT ? 64 * OS * 4 : 0;
+  __shared__ __align__(16) char s_raw[ROWS > SLAB ? ROWS : SLAB];
+  T* s = (T*)s_raw;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
+  const int64_t a0 = SPLIT ? (int64_t)blockIdx.x * 16 : ((int64_t)blockIdx.x * 4 + wave) * 16;
+  const int64_t a = a0 + i;
+  typename M::F xf[NC];
   if (A.act) {
+    const T* p = (const T*)A.x + a * A.ldx + EV * g;
 #pragma unroll
-    for (int at = 0; at < AT; ++at) {
-      const int64_t a = a0 + 16 * at + i;
-      const T* p = (const T*)A.x + a * A.ldx + EV * g;
-#pragma unroll
-      for (int ch = 0; ch < NC; ++ch) xf[at][ch] = ld16<typename M::F>(p + ch * M::CK, a < A.n);
-    }
+    for (int ch = 0; ch < NC; ++ch) xf[ch] = ld16<typename M::F>(p + ch * M::CK, a < A.n);
   }
-  f4 dx[AT][NG][NT];
+  f4 dx[C / 16];
 #pragma unroll
-  for (int at = 0; at < AT; ++at)
-#pragma unroll
-    for (int p = 0; p < NG; ++p)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) dx[at][p][t] = f4{0.f, 0.f, 0.f, 0.f};
-  const int ngr = (A.out + OG - 1) / OG;
-  Tile<T, OG, C, RS, 256> tw;
-  tw.fetch((const T*)A.w, C, A.out, threadIdx.x);
-  tw.put(s_w[0], threadIdx.x);
-  __syncthreads();
-  for (int og = 0; og < ngr; ++og) {
+  for (int ct = 0; ct < C / 16; ++ct) dx[ct] = f4{0.f, 0.f, 0.f, 0.f};
+  const int ngr = (A.out + OG - 1) / OG, tid = SPLIT ? lane : (int)threadIdx.x, step = SPLIT ? 4 : 1;
+  auto slot = [](int r) { return nat_slot<T>(r, true); };
+  Tile<T, OG, C, RS, SPLIT ? 64 : 256> tw;
+  typename M::F dz, dzn;
+  auto fetch = [&](int og) {
     const int o0 = og * OG, oe = o0 + EV * g;
-    const T* w = s_w[og & 1];
-    if (og + 1 < ngr) tw.fetch((const T*)A.w + (int64_t)(o0 + OG) * C, C, A.out - o0 - OG, threadIdx.x);
-    typename M::F dz[AT];
-#pragma unroll
-    for (int at = 0; at < AT; ++at) {
-      const int64_t a = a0 + 16 * at + i;
-      dz[at] = ld16<typename M::F>((const T*)A.dy + a * A.ldy + oe, a < A.n && oe < A.out);
-    }
+    tw.fetch((const T*)A.w + (int64_t)o0 * C, C, A.out - o0, tid);
+    dzn = ld16<typename M::F>((const T*)A.dy + a * A.ldy + oe, a < A.n && oe < A.out);
+  };
+  const int og0 = SPLIT ? wave : 0;
+  if (og0 < ngr) fetch(og0);
+  int b = 0;
+  for (int og = og0; og < ngr; og += step, b ^= 1) {
+    const int oe = og * OG + EV * g;
+    T* w = s + (SPLIT ? wave : b) * OG * RS;
+    tw.put(w, tid, slot);
+    dz = dzn;
+    // two buffers: a wave that is a step ahead writes the one that the others have left
+    if constexpr (SPLIT)
+      wave_sync();
+    else
+      __syncthreads();
+    if (og + step < ngr) fetch(og + step);
     if (A.act) {
-#pragma unroll
-      for (int at = 0; at < AT; ++at) {
-        f4 z[NT], d[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          z[t] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int ch = 0; ch < NC; ++ch)
-            z[t] = M::mma(z[t], *(const typename M::F*)(w + nat_row<T>(t, i) * RS + ch * M::CK + EV * g), xf[at][ch]);
-        }
-        M::unpack(dz[at], d);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float b = A.bias && oe < A.out ? A.bias[oe + 4 * t + r] : 0.f;
-            float v, e;
-            act_both(z[t][r] + b, A.ab, v, e);
-            d[t][r] *= e;
-          }
-        dz[at] = M::pack(d);
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < NG; ++p)
+      f4 z[NT], d[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const typename M::F wt = ldtn_nat<RS>(w, 0, p, t, lane);
+        z[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int at = 0; at < AT; ++at) dx[at][p][t] = M::mma(dx[at][p][t], wt, dz[at]);
+        for (int ch = 0; ch < NC; ++ch)
+          z[t] = M::mma(z[t], *(const typename M::F*)(w + (16 * t + pi<T>(i)) * RS + ch * M::CK + EV * g), xf[ch]);
       }
-    if (og + 1 < ngr) tw.put(s_w[(og + 1) & 1], threadIdx.x);
-    __syncthreads();
+      M::unpack(dz, d);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float bias = A.bias && oe < A.out ? A.bias[oe + 4 * t + r] : 0.f;
+          float v, e;
+          act_both(z[t][r] + bias, A.ab, v, e);
+          d[t][r] *= e;
+        }
+      dz = M::pack(d);
+    }
+#pragma unroll
+    for (int ct = 0; ct < C / 16; ++ct) dx[ct] = M::mma(dx[ct], ldt<RS>(w, 0, 16 * ct, lane), dz);
+    if constexpr (SPLIT) wave_sync();
   }
+  if constexpr (SPLIT) {
+    __syncthreads();  // the slabs lie over the rows of W
+    float* slab = (float*)s_raw + (16 * wave + i) * OS;
 #pragma unroll
-  for (int at = 0; at < AT; ++at) {
-    const int64_t a = a0 + 16 * at + i;
-    if (a >= A.n) continue;
+    for (int ct = 0; ct < C / 16; ++ct) *(f4*)(slab + 16 * ct + 4 * g) = dx[ct];
+    join_waves<T, C>((float*)s_raw, a0, A.n,
+                     [&](int64_t r, int c, f4* o) { st_row<T>((T*)A.dx + r * A.lddx + c, o); });
+  } else {
+    if (a >= A.n) return;
 #pragma unroll
-    for (int p = 0; p < NG; ++p) st_row<T>((T*)A.dx + a * A.lddx + p * M::CK + EV * g, dx[at][p]);
+    for (int ct = 0; ct < C / 16; ++ct) st4((T*)A.dx + a * A.lddx + 16 * ct + 4 * g, dx[ct]);
   }
 }
 
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(256) void k_linear_dx(LinArgs A) {
 // and x are read transposed.  Each split writes its own partial, added up in split order.
 // Bound: HBM (x and dy rows).
 template <class T, int C>
-__global__ __launch_bounds__(256) void k_linear_dw(LinArgs A) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k_linear_dw(LinArgs A) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + PADE(sizeof(T));
   constexpr int OB = 64, RO = OB + PADE(sizeof(T));
@@ -246,7 +247,7 @@ __global__ __launch_bounds__(256) void k_linear_dw(LinArgs A) {
           f4 z = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int ch = 0; ch < NC; ++ch)
-            z = M::mma(z, *(const typename M::F*)(xs + (16 * t + i) * RS + ch * CK + EV * g), wf[ch]);
+            z = M::mma(z, *(const typename M::F*)(xs + (16 * t + pi<T>(i)) * RS + ch * CK + EV * g), wf[ch]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float v, e;
@@ -265,20 +266,21 @@ __global__ __launch_bounds__(256) void k_linear_dw(LinArgs A) {
     __syncthreads();
   }
   if (!on) return;
-  float* p = A.part + ((int64_t)blockIdx.y * A.out + ob + 16 * wave) * C;
+  float* ps = A.part + (int64_t)blockIdx.y * A.out * (C + 1);
+  float* p = ps + (int64_t)(ob + 16 * wave) * C;
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct)
 #pragma unroll
     for (int q = 0; q < 4; ++q) p[(4 * g + q) * C + 16 * ct + i] = acc[ct][q];
   db = gsum(db);
-  if (g == 0) A.part_b[(int64_t)blockIdx.y * A.out + o] = db;
+  if (g == 0) ps[(int64_t)A.out * C + o] = db;
 }
 
-// Splits of the rows for dW: about 512 blocks in all, each with at least 128 rows (a split
+// Splits of the rows for dW: about 512 blocks in all, each with at least 32 rows (a split
 // costs a partial matrix written and read once)
 int64_t dw_splits(int64_t n, int out) {
   const int64_t nb = cdiv(out, 64);
-  return std::max<int64_t>(1, std::min<int64_t>(512 / nb, cdiv(n, 128)));
+  return std::max<int64_t>(1, std::min<int64_t>(512 / nb, cdiv(n, 32)));
 }
 
 template <class T>
@@ -300,7 +302,10 @@ int launch_linear(const LinArgs& A0, int C, int what, hipStream_t st) {
       else                                                                                  \
         k_linear<T, CC, AT><<<dim3((unsigned)bx, by), 256, 0, st>>>(A);                     \
     } else if (what == 1) {                                                                 \
-      k_linear_dx<T, CC, 1><<<(unsigned)cdiv(A.n, 64), 256, 0, st>>>(A);                    \
+      if (cdiv(A.n, 64) < 512)                                                              \
+        k_linear_dx<T, CC, true><<<(unsigned)cdiv(A.n, 16), 256, 0, st>>>(A);               \
+      else                                                                                  \
+        k_linear_dx<T, CC, false><<<(unsigned)cdiv(A.n, 64), 256, 0, st>>>(A);              \
     } else {                                                                                \
       k_linear_dw<T, CC><<<dim3((unsigned)cdiv(A.out, 64), (unsigned)S), 256, 0, st>>>(A);  \
     }                                                                                       \
@@ -362,10 +367,7 @@ extern "C" int mp_linear_bwd_ws(int32_t n, int32_t in, int32_t out, int32_t dt, 
   MP_TRY(ops::check_linear("mp_linear_bwd_ws", n, in, out, dt, 0));
   if (!bytes) return arg_error("mp_linear_bwd_ws: null bytes");
   const int64_t S = ops::dw_splits(n, out);
-  Arena a(nullptr, 0, true);
-  a.take<float>(S * out * in);
-  a.take<float>(S * out);
-  *bytes = a.off;
+  *bytes = align_up(sizeof(float) * (size_t)(S * out * (in + 1)));
   return MP_OK;
 }
 
@@ -385,11 +387,11 @@ extern "C" int mp_linear_bwd(int32_t n, int32_t in, int32_t out, int32_t dt, int
   int64_t S = 0;
   if (dw || dbias) {
     if (!ws || ((uintptr_t)ws & 15)) return arg_error("mp_linear_bwd: workspace null or not 16-byte aligned");
-    Arena a(ws, ws_bytes);
+    size_t need = 0;
+    MP_TRY(mp_linear_bwd_ws(n, in, out, dt, &need));
+    if (ws_bytes < need) return arg_error("mp_linear_bwd: workspace too small");
     S = ops::dw_splits(n, out);
-    A.part = a.take<float>(S * out * in);
-    A.part_b = a.take<float>(S * out);
-    if (!a.ok()) return arg_error("mp_linear_bwd: workspace too small");
+    A.part = (float*)ws;
   }
   ProfScope p("linear_bwd", st);
   auto go = [&](int what) {
@@ -399,7 +401,7 @@ extern "C" int mp_linear_bwd(int32_t n, int32_t in, int32_t out, int32_t dt, int
   if (!A.part) return MP_OK;
   if (n > 0) MP_TRY(go(2));
   if (n == 0) S = 0;  // no rows: sums over nothing, zeros
-  if (dw) MP_TRY(ops::reduce_rows(A.part, S, (int64_t)out * in, (int64_t)out * in, dw, dt == 1, st));
-  if (dbias) MP_TRY(ops::reduce_rows(A.part_b, S, out, out, dbias, false, st));
-  return MP_OK;
+  const int64_t N = (int64_t)out * in;
+  const ops::Segment seg[2] = {{0, N, dw, dt == 1}, {N, out, dbias, false}};
+  return ops::reduce_rows(A.part, S, N + out, seg, 2, st);
 }

@@ -225,39 +225,56 @@ int norm_blocks(int64_t n, int C, bool bf16, int most = 1024) {
   return (int)std::min<int64_t>(cdiv(n, rpb), most);
 }
 
-// out[j] = sum_s part[s][j]: a block takes 32 columns, its 8 thread rows every eighth partial
-// row, joined in a fixed order
-template <class TO>
-__global__ __launch_bounds__(256) void k_reduce_rows(const float* __restrict__ part, int64_t S, int64_t N, int64_t ldp,
-                                                     TO* __restrict__ out) {
-  __shared__ float sh[8][32];
-  const int64_t j = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-  const int r = threadIdx.x >> 5;
+struct Segments {
+  Segment s[3];
+};
+// A block of 1024 threads takes NCOL columns, its thread rows every (1024 / NCOL)-th partial row,
+// joined pairwise.  Few columns (the distance slopes) take 8: with 32, three quarters of the
+// threads would idle over thousands of partial rows (9,300 rows of 4: 48 us against 6).
+template <int NCOL>
+__global__ __launch_bounds__(1024) void k_reduce_rows(const float* __restrict__ part, int64_t S, int64_t ldp, Segments G) {
+  constexpr int NR = 1024 / NCOL;
+  __shared__ float sh[NR][NCOL];
+  const Segment sg = G.s[blockIdx.y];
+  const int c = threadIdx.x % NCOL, r = threadIdx.x / NCOL;
+  const int64_t j = (int64_t)blockIdx.x * NCOL + c;
+  if ((int64_t)blockIdx.x * NCOL >= sg.N) return;
   float s = 0.f;
-  if (j < N) {
+  if (j < sg.N) {
 #pragma unroll 8
-    for (int64_t k = r; k < S; k += 8) s += part[k * ldp + j];
+    for (int64_t k = r; k < S; k += NR) s += part[k * ldp + sg.off + j];
   }
-  sh[r][threadIdx.x & 31] = s;
+  sh[r][c] = s;
   __syncthreads();
-  if (r == 0 && j < N) {
 #pragma unroll
-    for (int q = 1; q < 8; ++q) s += sh[q][threadIdx.x];
-    if constexpr (sizeof(TO) == 2)
-      out[j] = f2bf(s);
+  for (int o = NR / 2; o > 0; o >>= 1) {
+    if (r < o) sh[r][c] += sh[r + o][c];
+    __syncthreads();
+  }
+  if (r == 0 && j < sg.N) {
+    if (sg.bf16)
+      ((uint16_t*)sg.out)[j] = f2bf(sh[0][c]);
     else
-      out[j] = s;
+      ((float*)sg.out)[j] = sh[0][c];
   }
 }
 
 }  // namespace
 
-int reduce_rows(const float* part, int64_t S, int64_t N, int64_t ldp, void* out, bool bf16, hipStream_t st) {
-  const int blocks = (int)cdiv(N, 32);
-  if (bf16)
-    k_reduce_rows<uint16_t><<<blocks, 256, 0, st>>>(part, S, N, ldp, (uint16_t*)out);
+int reduce_rows(const float* part, int64_t S, int64_t ldp, const Segment* seg, int nseg, hipStream_t st) {
+  Segments G{};
+  int k = 0;
+  int64_t most = 0;
+  for (int q = 0; q < nseg; ++q)
+    if (seg[q].out) {
+      most = std::max(most, seg[q].N);
+      G.s[k++] = seg[q];
+    }
+  if (k == 0) return MP_OK;
+  if (most <= 8)
+    k_reduce_rows<8><<<dim3(1, k), 1024, 0, st>>>(part, S, ldp, G);
   else
-    k_reduce_rows<float><<<blocks, 256, 0, st>>>(part, S, N, ldp, (float*)out);
+    k_reduce_rows<32><<<dim3((unsigned)cdiv(most, 32), k), 1024, 0, st>>>(part, S, ldp, G);
   MP_CHECK_LAUNCH();
   return MP_OK;
 }
@@ -350,8 +367,6 @@ extern "C" int mp_norm_block_bwd(const mp_norm_args* a, const void* dy, int64_t 
                    : ops::launch_norm<float>(A, C, true, blocks, st));
   }
   // no rows: sums over nothing, zeros
-  float* out[3] = {dscale, dw_post, dw_pre};
-  for (int k = 0; k < 3; ++k)
-    if (out[k]) MP_TRY(ops::reduce_rows(A.part + k * C, blocks, C, 3 * C, out[k], false, st));
-  return MP_OK;
+  const ops::Segment seg[3] = {{0, C, dscale, false}, {C, C, dw_post, false}, {2 * C, C, dw_pre, false}};
+  return ops::reduce_rows(A.part, blocks, 3 * C, seg, 3, st);
 }
