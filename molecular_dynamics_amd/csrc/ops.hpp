@@ -72,53 +72,30 @@ __device__ __forceinline__ F ld16(const T* p, bool on) {
   return on ? *(const F*)p : zero16<F>();
 }
 
-// Order of the 16 rows of a tile that is read from LDS both by rows and transposed: index r of
-// the tile is LDS (or key) row pi(r).  bf16 transposed reads take four rows at once for each
-// group of 16 lanes; with a row stride of 4 banks (mod 32) those rows must be two apart to fall
-// on different banks, and any eight consecutive indices still cover eight adjacent rows, which
-// is what 16-byte reads by rows want.  float32 reads single words transposed: plain order.
+// Padding of a row of a matrix in LDS, in elements.  bf16: 32 bytes, so that rows of C or of 32
+// elements are 32 bytes off a multiple of 64 and both 16-byte reads of 16 consecutive rows and
+// transposed reads of rows 4 g + r meet no bank twice (measured: 16 bytes of padding cost a
+// conflict in every read); float32: 16 bytes, its transposed reads take single words.
 template <class T>
-__host__ __device__ constexpr int pi(int r) {
-  return sizeof(T) == 2 ? 8 * (r >> 3) + 2 * (r & 3) + ((r >> 2) & 1) : r;
+constexpr int lds_pad() {
+  return sizeof(T) == 2 ? 16 : 4;
 }
-template <class T>
-__host__ __device__ constexpr int pi_inv(int p) {
-  return sizeof(T) == 2 ? 8 * (p >> 3) + 4 * (p & 1) + ((p >> 1) & 3) : p;
-}
-static_assert(pi<uint16_t>(pi_inv<uint16_t>(7)) == 7 && pi_inv<uint16_t>(pi<uint16_t>(9)) == 9, "inverse");
 
-// Four rows row, row + 2, row + 4, row + 6 of sixteen adjacent columns, transposed: lane 4 r + s of
-// a 16-lane group reads columns 4 s .. 4 s + 3 of the r-th row, and lane i receives column i of the
-// four rows (ds_read_b64_tr_b16)
-template <int RS>
-__device__ __forceinline__ s4 ldt4(const uint16_t* m, int row, int col, int lane) {
-  const uint16_t* p = m + (row + 2 * ((lane & 15) >> 2)) * RS + col + 4 * (lane & 3);
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p);
-}
 // Transposed operand in tile order from an LDS matrix m[k][RS]: index = column col + i, contracted
-// = rows k0 + 16 t + pi(4 g + r)
+// = rows k0 + 16 t + 4 g + r.  bf16: each group of 16 lanes reads four rows of 16 columns, lane
+// 4 r + s the columns 4 s .. 4 s + 3 of row r, and lane i receives column i of the four rows
+// (ds_read_b64_tr_b16).
 template <int RS>
 __device__ __forceinline__ s8 ldt(const uint16_t* m, int k0, int col, int lane) {
-  const int r = k0 + pi<uint16_t>(4 * (lane >> 4));
-  const s4 a = ldt4<RS>(m, r, col, lane), b = ldt4<RS>(m, r + 16, col, lane);
+  const uint16_t* p = m + (k0 + 4 * (lane >> 4) + ((lane & 15) >> 2)) * RS + col + 4 * (lane & 3);
+  const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p);
+  const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(p + 16 * RS));
   return s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 template <int RS>
 __device__ __forceinline__ f4 ldt(const float* m, int k0, int col, int lane) {
   const float* p = m + (k0 + 4 * (lane >> 4)) * RS + col + (lane & 15);
   return f4{p[0], p[RS], p[2 * RS], p[3 * RS]};
-}
-// The same with the contracted index in natural order, k0 + EV g + j, of a matrix whose rows
-// were stored in the order pi within each 16
-template <int RS>
-__device__ __forceinline__ s8 ldtn(const uint16_t* m, int k0, int col, int lane) {
-  const int g = lane >> 4, r = k0 + 16 * (g >> 1) + 8 * (g & 1);
-  const s4 a = ldt4<RS>(m, r, col, lane), b = ldt4<RS>(m, r + 1, col, lane);
-  return s8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-}
-template <int RS>
-__device__ __forceinline__ f4 ldtn(const float* m, int k0, int col, int lane) {
-  return ldt<RS>(m, k0, col, lane);
 }
 
 // Row of a CK-row group that index i of result tile t stands for, such that the NT result
@@ -130,15 +107,14 @@ __device__ __forceinline__ int nat_row(int t, int i) {
   else
     return i;
 }
-// where such a group's row x = nat_row(t, i) is stored to be read as 16 t + pi(i) (or 16 t + i)
+// Row 16 t + i in which row x = nat_row(t, i) of a group is stored: a group stored so is read by
+// rows in the order nat_row, and transposed (ldt) with the contracted rows in natural order
 template <class T>
-__device__ __forceinline__ int nat_slot(int x, bool order_pi) {
-  if constexpr (sizeof(T) == 2) {
-    const int t = (x >> 2) & 1, i = 4 * (x >> 3) + (x & 3);
-    return 16 * t + (order_pi ? pi<T>(i) : i);
-  } else {
+__device__ __forceinline__ int nat_slot(int x) {
+  if constexpr (sizeof(T) == 2)
+    return x / 32 * 32 + 16 * ((x >> 2) & 1) + 4 * ((x >> 3) & 3) + (x & 3);
+  else
     return x;
-  }
 }
 
 // A [ROWS][C] tile from global rows (stride ld) to LDS rows (stride RS), by NTH threads in

@@ -153,15 +153,15 @@ struct WaveTile {
     for (int j = 0; j < IT; ++j) *(u4*)(dst + (lane / VPR + j * RJ) * RS + (lane % VPR) * EV) = v[j];
   }
 };
-// chunks c0 .. c1 - 1 of the operands of NTL tiles; ORDER: rows in the order pi
-template <class T, int C, int NTL, bool ORDER>
+// chunks c0 .. c1 - 1 of the operands of NTL tiles
+template <class T, int C, int NTL>
 __device__ __forceinline__ void load_frags(typename MF<T>::F (&f)[NTL][C / MF<T>::CK], const T* src, int64_t ld,
                                            int64_t k0, int rows, int i, int g, int c0 = 0, int c1 = C / MF<T>::CK) {
   using M = MF<T>;
   const T* p = src + k0 * ld;
 #pragma unroll
   for (int t = 0; t < NTL; ++t) {
-    uint32_t r = 16 * t + (ORDER ? pi<T>(i) : i);
+    uint32_t r = 16 * t + i;
     if (rows < 16 * NTL) r = min(r, (uint32_t)rows - 1);
     const uint32_t off = r * (uint32_t)ld + M::EV * g;
 #pragma unroll
@@ -200,7 +200,7 @@ __device__ __forceinline__ bool lane_in_head(int ch, int g, int h) {
 
 template <class T, int C>
 struct AttnDims {
-  static constexpr int CK = MF<T>::CK, RS = C + 16 / (int)sizeof(T), OS = C + 4;
+  static constexpr int CK = MF<T>::CK, RS = C + lds_pad<T>(), OS = C + 4;
 };
 
 // one head's channel chunk range: chunk ch belongs to the operands of head h alone (heads of a
@@ -255,9 +255,8 @@ void k_attn_fwd(AttnArgs A) {
   if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
   const int row = row0 + i;
   const bool fix = A.to_fix > 0, dist = A.pos != nullptr;
-  const int slot = lane / 16 * 16 + pi_inv<T>(lane % 16);  // where index `lane` of a step is kept
   typename M::F qf[1][NC];
-  load_frags<T, C, 1, false>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
+  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, row < e);
   // thr: a score above it (in the reference m) raises the reference; -inf until there is one
   float m[H], thr[H];
@@ -289,7 +288,7 @@ void k_attn_fwd(AttnArgs A) {
   };
   if (s + CK * wave < e) {
     fetch_v(s + CK * wave, on);
-    load_frags<T, C, NT, true>(kf, (const T*)A.k, A.ldk, s + CK * wave, e - s - CK * wave, i, g);
+    load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, s + CK * wave, e - s - CK * wave, i, g);
   }
 
   for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
@@ -298,7 +297,7 @@ void k_attn_fwd(AttnArgs A) {
     const uint64_t on_n = live<CK>(A, kn, e, lane, true);
     if (part) tv.clear(on, lane);
     tv.put(vs, lane);
-    if (dist && lane < CK) ps[slot] = u4{kp.x, kp.y, kp.z, 0u};
+    if (dist && lane < CK) ps[lane] = u4{kp.x, kp.y, kp.z, 0u};
     wave_sync();
     if (kn < e) fetch_v(kn, on_n);
     bool lv[NT][4];
@@ -307,7 +306,7 @@ void k_attn_fwd(AttnArgs A) {
     for (int t = 0; t < NT; ++t) {
       r[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) lv[t][q] = (on >> (16 * t + pi<T>(4 * g + q))) & 1;
+      for (int q = 0; q < 4; ++q) lv[t][q] = ((uint32_t)on >> (4 * g)) >> (16 * t + q) & 1;
     }
     if (dist) {
 #pragma unroll
@@ -325,7 +324,7 @@ void k_attn_fwd(AttnArgs A) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
       if (kn < e)
-        load_frags<T, C, NT, true>(kf, (const T*)A.k, A.ldk, kn, e - kn, i, g, chunk_first<T, DH>(h), chunk_end<T, DH>(h));
+        load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, kn, e - kn, i, g, chunk_first<T, DH>(h), chunk_end<T, DH>(h));
       const float sl = dist ? A.slope[h] * (kLog2e * A.unit) : 0.f;
       if (Z.cap) {
 #pragma unroll
@@ -460,7 +459,7 @@ void k_attn_fwd(AttnArgs A) {
 //   p = 2^(x - lse), dl = p (dp - dsum); ds = dl times the cap's slope 1 - tanh^2
 template <class T>
 __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4 dp, f4 r, float slope, f4 lse, f4 dsum,
-                                          bool all, uint64_t on, f4& p, f4& dl, f4& ds) {
+                                          bool all, uint32_t on, f4& p, f4& dl, f4& ds) {
   f4 f;
   if (Z.cap) {
 #pragma unroll
@@ -482,7 +481,7 @@ __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4
   if (!all) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (!((on >> (pi<T>(4 + q) - pi<T>(4))) & 1)) p[q] = dl[q] = ds[q] = 0.f;
+      if (!((on >> q) & 1)) p[q] = dl[q] = ds[q] = 0.f;
   }
 }
 
@@ -508,10 +507,9 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
   }
   const int row = row0 + i;
   const bool fix = A.to_fix > 0;
-  const int slot = lane / 16 * 16 + pi_inv<T>(lane % 16);  // where index `lane` of a step is kept
   typename M::F qf[1][NC], of[1][NC];
-  load_frags<T, C, 1, false>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
-  load_frags<T, C, 1, false>(of, (const T*)A.dout, A.lddo, row0, e - row0, i, g);
+  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
+  load_frags<T, C, 1>(of, (const T*)A.dout, A.lddo, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, row < e);
   float slope[H], lse[H], dsum[H], dsl[H];
 #pragma unroll
@@ -554,11 +552,11 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
     WaveTile<T, C, RS> tk;
     tk.fetch((const T*)A.k, A.ldk, k0, e - k0, lane);
     typename M::F vf[NT][NC];
-    load_frags<T, C, NT, true>(vf, (const T*)A.v, A.ldv, k0, e - k0, i, g);
+    load_frags<T, C, NT>(vf, (const T*)A.v, A.ldv, k0, e - k0, i, g);
     if (on != all_live<CK>()) tk.clear(on, lane);
     if (A.pos && lane < CK) {
       const P3 p = load_pos(A, k0 + lane, (on >> lane) & 1);
-      ps[slot] = u4{p.x, p.y, p.z, 0u};
+      ps[lane] = u4{p.x, p.y, p.z, 0u};
     }
     tk.put(ks, lane);
     wave_sync();
@@ -582,12 +580,12 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
       for (int t = 0; t < NT; ++t) {
         typename M::F kf[NC];
 #pragma unroll
-        for (int ch = 0; ch < NC; ++ch) kf[ch] = *(const typename M::F*)(ks + (16 * t + pi<T>(i)) * RS + ch * CK + EV * g);
+        for (int ch = 0; ch < NC; ++ch) kf[ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
         const f4 z = f4{0.f, 0.f, 0.f, 0.f};
         const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
         f4 p, dl;
         const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
-        pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, on == all_live<CK>(), on >> (16 * t + pi<T>(4 * g)), p, dl, ds[t]);
+        pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl, ds[t]);
         if (A.pos) {
           const float sl = A.slope[h];
 #pragma unroll
@@ -682,12 +680,11 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
   if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
   const int row = row0 + i;
   const bool fix = A.to_fix > 0;
-  const int slot = lane / 16 * 16 + pi_inv<T>(lane % 16);  // where index `lane` of a step is kept
   const uint64_t own_on = live<16>(A, row0, e, lane, true);
   const bool own_live = (own_on >> i) & 1;
   typename M::F kf[1][NC], vf[1][NC];
-  load_frags<T, C, 1, false>(kf, (const T*)A.k, A.ldk, row0, e - row0, i, g);
-  load_frags<T, C, 1, false>(vf, (const T*)A.v, A.ldv, row0, e - row0, i, g);
+  load_frags<T, C, 1>(kf, (const T*)A.k, A.ldk, row0, e - row0, i, g);
+  load_frags<T, C, 1>(vf, (const T*)A.v, A.ldv, row0, e - row0, i, g);
   const P3 own = load_pos(A, row, own_live);
   float slope[H];
 #pragma unroll
@@ -715,12 +712,12 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
         const bool l = (on >> lane) & 1;
         if (A.pos) {
           const P3 p = load_pos(A, k0 + lane, l);
-          ps[slot] = u4{p.x, p.y, p.z, 0u};
+          ps[lane] = u4{p.x, p.y, p.z, 0u};
         }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          ls[h * CK + slot] = l ? A.lse[(int64_t)(k0 + lane) * H + h] : INFINITY;
-          ss[h * CK + slot] = l ? A.dsum[(int64_t)(k0 + lane) * H + h] : 0.f;
+          ls[h * CK + lane] = l ? A.lse[(int64_t)(k0 + lane) * H + h] : INFINITY;
+          ss[h * CK + lane] = l ? A.dsum[(int64_t)(k0 + lane) * H + h] : 0.f;
         }
       }
       tq.put(qs, lane);
@@ -739,7 +736,7 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
           }
         }
       }
-      const uint64_t own_bits = own_live ? ~0ull : 0ull;
+      const uint32_t own_bits = own_live ? ~0u : 0u;
       const bool all_own = own_on == 0xffffull;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
@@ -749,8 +746,8 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
           typename M::F qf[NC], of[NC];
 #pragma unroll
           for (int ch = 0; ch < NC; ++ch) {
-            qf[ch] = *(const typename M::F*)(qs + (16 * t + pi<T>(i)) * RS + ch * CK + EV * g);
-            of[ch] = *(const typename M::F*)(os + (16 * t + pi<T>(i)) * RS + ch * CK + EV * g);
+            qf[ch] = *(const typename M::F*)(qs + (16 * t + i) * RS + ch * CK + EV * g);
+            of[ch] = *(const typename M::F*)(os + (16 * t + i) * RS + ch * CK + EV * g);
           }
           const f4 z = f4{0.f, 0.f, 0.f, 0.f};
           const f4 x = head_mma<T, DH, NC>(z, qf, kf[0], h, g), dp = head_mma<T, DH, NC>(z, of, vf[0], h, g);

@@ -15,19 +15,14 @@ struct FfnArgs {
   int64_t rows_per_split;
 };
 
-constexpr int pad_of(int esize) { return 16 / esize; }
-
 // One chunk of CK hidden units of the three matrices, in LDS: rows of Wg and Wu (CK x C) and
-// columns of Wd (C x CK), staged by NTH threads.  Rows are stored where the reads of 16
-// consecutive indices fall on different banks:
-//   Wg, Wu   hidden unit nat_row(t, i) in row 16 t + i (forward: read by rows only), or in row
-//            16 t + pi(i) (backward: also read transposed)
-//   Wd       forward: channel 16 NT p + nat_row(t, i) in row 16 (NT p + t) + i; backward (read
-//            transposed only): rows in the order pi, hidden unit nat_row(t, i) in column 16 t + i
+// columns of Wd (C x CK), staged by NTH threads.  Rows (hidden units of Wg and Wu, channels of Wd)
+// are stored in the order nat_slot.  The backward pass reads Wd transposed, its hidden units as
+// result rows: there hidden unit nat_row(t, i) is column 16 t + i.
 template <class T, int C, int NTH, bool BWD>
 struct Chunk {
   using M = MF<T>;
-  static constexpr int CK = M::CK, RS = C + pad_of(sizeof(T)), RD = CK + pad_of(sizeof(T));
+  static constexpr int CK = M::CK, RS = C + lds_pad<T>(), RD = CK + lds_pad<T>();
   static constexpr int SIZE = 2 * CK * RS + C * RD;
   Tile<T, CK, C, RS, NTH> g, u;
   Tile<T, C, CK, RD, NTH> d;
@@ -37,25 +32,21 @@ struct Chunk {
     d.fetch((const T*)A.wd + h0, A.hidden, C, tid);
   }
   __device__ __forceinline__ void put(T* s, int tid) const {
-    auto slot = [](int r) { return nat_slot<T>(r, BWD); };
+    auto slot = [](int r) { return nat_slot<T>(r); };
     g.put(s, tid, slot);
     u.put(s + CK * RS, tid, slot);
     T* sd = s + 2 * CK * RS;
-    if constexpr (!BWD) {
-      d.put(sd, tid, [](int r) { return r / CK * CK + nat_slot<T>(r % CK, false); });
+    if constexpr (!BWD || sizeof(T) == 4) {
+      d.put(sd, tid, slot);
     } else {
       using TD = Tile<T, C, CK, RD, NTH>;
 #pragma unroll
       for (int k = 0; k < TD::IT; ++k) {
         const int x = tid + k * NTH, r = x / TD::VPR, c = (x % TD::VPR) * M::EV;
         if (TD::TOT % NTH != 0 && x >= TD::TOT) break;
-        T* q = sd + (r / 16 * 16 + pi<T>(r % 16)) * RD;
-        if constexpr (sizeof(T) == 2) {  // units c .. c + 3 and c + 4 .. c + 7: tiles 0 and 1
-          *(u2*)(q + c / 2) = u2{d.v[k][0], d.v[k][1]};
-          *(u2*)(q + 16 + c / 2) = u2{d.v[k][2], d.v[k][3]};
-        } else {
-          *(u4*)(q + c) = d.v[k];
-        }
+        T* q = sd + nat_slot<T>(r) * RD + c / 2;  // units c .. c + 3 of tile 0, c + 4 .. c + 7 of tile 1
+        *(u2*)q = u2{d.v[k][0], d.v[k][1]};
+        *(u2*)(q + 16) = u2{d.v[k][2], d.v[k][3]};
       }
     }
   }
@@ -241,12 +232,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(SPLIT ? 1 :
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int at = 0; at < AT; ++at) zg[at][t] = zu[at][t] = dh[at][t] = f4{0.f, 0.f, 0.f, 0.f};
-      const int row = (16 * t + pi<T>(i)) * RS + EV * g;
+      const int row = (16 * t + i) * RS + EV * g;
 #pragma unroll
       for (int ch = 0; ch < NC; ++ch) {
         const typename M::F fg = *(const typename M::F*)(wg + row + ch * CK);
         const typename M::F fu = *(const typename M::F*)(wu + row + ch * CK);
-        const typename M::F fd = ldtn<RD>(wd, ch * CK, 16 * t, lane);
+        const typename M::F fd = ldt<RD>(wd, ch * CK, 16 * t, lane);
 #pragma unroll
         for (int at = 0; at < AT; ++at) {
           zg[at][t] = M::mma(zg[at][t], fg, xf[at][ch]);
@@ -270,7 +261,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(SPLIT ? 1 :
       dg[at] = M::pack(zg[at]);
       du[at] = M::pack(zu[at]);
     }
-    // hidden unit EV g + j of the operands is row 16 t + pi(4 g + r): tile order
+    // hidden unit EV g + j of the operands is LDS row 16 t + 4 g + r: tile order
 #pragma unroll
     for (int ct = 0; ct < C / 16; ++ct) {
       const typename M::F fg = ldt<RS>(wg, 0, 16 * ct, lane), fu = ldt<RS>(wu, 0, 16 * ct, lane);
@@ -310,7 +301,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(SPLIT ? 1 :
 template <class T, int C>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn_dw(FfnArgs A) {
   using M = MF<T>;
-  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + pad_of(sizeof(T));
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + lds_pad<T>();
   __shared__ __align__(16) T s_x[2][CK * RS];
   __shared__ __align__(16) T s_d[2][CK * RS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
@@ -355,7 +346,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       for (int t = 0; t < NT; ++t) {
         f4 dh = f4{0.f, 0.f, 0.f, 0.f};
         zg[t] = zu[t] = dh;
-        const int row = (16 * t + pi<T>(i)) * RS + EV * g;
+        const int row = (16 * t + i) * RS + EV * g;
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
           const typename M::F fx = *(const typename M::F*)(xs + row + ch * CK);

@@ -17,8 +17,6 @@ struct LinArgs {
   int64_t rows_per_split;
 };
 
-constexpr int PADE(int esize) { return 16 / esize; }
-
 // Forward: D[o][a] = sum_c W[o][c] x[a][c].  A wave keeps the rows of 16 AT atoms in registers
 // as one operand and walks the outputs CK at a time, the other operand read straight from W
 // (at most 256 KB, so L1/L2 hold it).  W's rows are taken in the order nat_row, which leaves
@@ -96,14 +94,14 @@ __global__ __launch_bounds__(256) void k_linear(LinArgs A) {
 // dx: D[c][a] = sum_o W[o][c] dz[a][o], dz = dy act'(z), z formed again by the forward's
 // product.  Both operands of dz sit as EV consecutive outputs per lane (natural order), so
 // dz goes from result to operand in registers.  W passes through LDS CK rows at a time,
-// output nat_row(t, i) in row 16 t + pi(i), read there by rows (z) and transposed (dx).
+// output nat_row(t, i) in row 16 t + i, read there by rows (z) and transposed (dx).
 // SPLIT (few rows): the four waves take the same 16 atoms and every fourth group of outputs,
 // each with rows of its own in LDS, and their sums are joined.
 // Bound: HBM (dy rows) without an activation.
 template <class T, int C, bool SPLIT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_linear_dx(LinArgs A) {
   using M = MF<T>;
-  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK, RS = C + PADE(sizeof(T)), OS = C + 4;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK, RS = C + lds_pad<T>(), OS = C + 4;
   constexpr int ROWS = (SPLIT ? 4 : 2) * OG * RS * (int)sizeof(T), SLAB = SPLIT ? 64 * OS * 4 : 0;
   __shared__ __align__(16) char s_raw[ROWS > SLAB ? ROWS : SLAB];
   T* s = (T*)s_raw;
@@ -120,7 +118,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) dx[ct] = f4{0.f, 0.f, 0.f, 0.f};
   const int ngr = (A.out + OG - 1) / OG, tid = SPLIT ? lane : (int)threadIdx.x, step = SPLIT ? 4 : 1;
-  auto slot = [](int r) { return nat_slot<T>(r, true); };
+  auto slot = [](int r) { return nat_slot<T>(r); };
   Tile<T, OG, C, RS, SPLIT ? 64 : 256> tw;
   typename M::F dz, dzn;
   auto fetch = [&](int og) {
@@ -149,7 +147,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
         z[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch)
-          z[t] = M::mma(z[t], *(const typename M::F*)(w + (16 * t + pi<T>(i)) * RS + ch * M::CK + EV * g), xf[ch]);
+          z[t] = M::mma(z[t], *(const typename M::F*)(w + (16 * t + i) * RS + ch * M::CK + EV * g), xf[ch]);
       }
       M::unpack(dz, d);
 #pragma unroll
@@ -189,8 +187,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
 template <class T, int C>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k_linear_dw(LinArgs A) {
   using M = MF<T>;
-  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + PADE(sizeof(T));
-  constexpr int OB = 64, RO = OB + PADE(sizeof(T));
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + lds_pad<T>();
+  constexpr int OB = 64, RO = OB + lds_pad<T>();
   __shared__ __align__(16) T s_x[2][CK * RS];
   __shared__ __align__(16) T s_d[2][CK * RO];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
@@ -247,7 +245,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k
           f4 z = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int ch = 0; ch < NC; ++ch)
-            z = M::mma(z, *(const typename M::F*)(xs + (16 * t + pi<T>(i)) * RS + ch * CK + EV * g), wf[ch]);
+            z = M::mma(z, *(const typename M::F*)(xs + (16 * t + i) * RS + ch * CK + EV * g), wf[ch]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float v, e;
