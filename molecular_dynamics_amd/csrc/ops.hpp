@@ -182,6 +182,28 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// barrier of a block for its LDS accesses alone: loads from memory may stay in flight
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Asks the scheduler for LDS reads AHEAD operands before their products: of READS operands and
+// MFMAS products, AHEAD reads first, then the rest spread over the products.  Left alone it reads
+// each operand just before its products and waits out the LDS latency every time.
+template <int READS, int AHEAD, int MFMAS>
+__device__ __forceinline__ void read_ahead() {
+  constexpr int A = AHEAD < READS ? AHEAD : READS, REST = READS - A, PER = MFMAS / READS;
+  __builtin_amdgcn_sched_group_barrier(0x100, A, 0);
+#pragma unroll
+  for (int q = 0; q < REST; ++q) {
+    __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, MFMAS - REST * PER, 0);
+}
+
 // sum over the four lane groups (lanes i, 16 + i, 32 + i, 48 + i)
 __device__ __forceinline__ float gsum(float v) {
   v += __shfl_xor(v, 16, 64);

@@ -26,16 +26,28 @@ struct Chunk {
   static constexpr int SIZE = 2 * CK * RS + C * RD;
   Tile<T, CK, C, RS, NTH> g, u;
   Tile<T, C, CK, RD, NTH> d;
-  __device__ __forceinline__ void fetch(const FfnArgs& A, int h0, int tid) {
+  __device__ __forceinline__ void fetch_gu(const FfnArgs& A, int h0, int tid) {
     g.fetch((const T*)A.wg + (int64_t)h0 * C, C, CK, tid);
     u.fetch((const T*)A.wu + (int64_t)h0 * C, C, CK, tid);
+  }
+  __device__ __forceinline__ void fetch_d(const FfnArgs& A, int h0, int tid) {
     d.fetch((const T*)A.wd + h0, A.hidden, C, tid);
   }
+  __device__ __forceinline__ void fetch(const FfnArgs& A, int h0, int tid) {
+    fetch_gu(A, h0, tid);
+    fetch_d(A, h0, tid);
+  }
   __device__ __forceinline__ void put(T* s, int tid) const {
+    put_gu(s, tid);
+    put_d(s + 2 * CK * RS, tid);
+  }
+  __device__ __forceinline__ void put_gu(T* s, int tid) const {
     auto slot = [](int r) { return nat_slot<T>(r); };
     g.put(s, tid, slot);
     u.put(s + CK * RS, tid, slot);
-    T* sd = s + 2 * CK * RS;
+  }
+  __device__ __forceinline__ void put_d(T* sd, int tid) const {
+    auto slot = [](int r) { return nat_slot<T>(r); };
     if constexpr (!BWD || sizeof(T) == 4) {
       d.put(sd, tid, slot);
     } else {
@@ -65,117 +77,217 @@ __device__ __forceinline__ void load_rows(typename MF<T>::F (&f)[AT][C / MF<T>::
   }
 }
 
-// Forward.  A wave keeps 16 AT atoms' rows in registers and walks the hidden units CK at a
-// time: D[hid][a] = Wg x and Wu x with the hidden rows taken in the order nat_row, so a lane
-// ends with EV consecutive hidden units of its atom, which after act(.) * (.) are the
-// operand of D[c][a] += Wd h as they stand.  Hidden units live in registers only.  The
-// weights of a chunk are shared by the block's four waves through LDS (two buffers, the next
-// chunk's loads in flight during the products).  SPLIT (few rows): the four waves take the same
-// 16 atoms and every fourth chunk each, weights straight from L2, and their sums are joined.
-// Bound: the matrix products and, beside them, the sigmoid of every hidden unit (exp and
-// reciprocal at a quarter of the VALU rate).
-template <class T, int C, int AT, bool SPLIT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn(FfnArgs A) {
+// One chunk of hidden units with 16 AT atoms' rows xf.  D[hid][a] = Wg x and Wu x with the hidden
+// rows taken in the order nat_row, so a lane ends with EV consecutive hidden units of its atom,
+// which after act(.) * (.) are the operand of D[c][a] += Wd h as they stand: hidden units live in
+// registers only.  WG, WU, WD give the operand of (tile, channel chunk) of the three matrices.
+template <class T, int C, int AT, class WG, class WU>
+__device__ __forceinline__ void ffn_in(f4 (&zg)[AT][MF<T>::NT], f4 (&zu)[AT][MF<T>::NT],
+                                       const typename MF<T>::F (&xf)[AT][C / MF<T>::CK], WG wg, WU wu) {
   using M = MF<T>;
-  using CH = Chunk<T, C, 256, false>;
-  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = SPLIT ? C : CH::RS, OS = C + 4;
-  constexpr int LDS = SPLIT ? 64 * OS * 4 : 2 * CH::SIZE * (int)sizeof(T);
-  __shared__ __align__(16) char s_raw[LDS];
-  T* s = (T*)s_raw;
+#pragma unroll
+  for (int t = 0; t < M::NT; ++t) {
+#pragma unroll
+    for (int at = 0; at < AT; ++at) zg[at][t] = zu[at][t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ch = 0; ch < C / M::CK; ++ch) {
+      const typename M::F fg = wg(t, ch), fu = wu(t, ch);
+#pragma unroll
+      for (int at = 0; at < AT; ++at) {
+        zg[at][t] = M::mma(zg[at][t], fg, xf[at][ch]);
+        zu[at][t] = M::mma(zu[at][t], fu, xf[at][ch]);
+      }
+    }
+  }
+}
+template <class T, int AT>
+__device__ __forceinline__ void ffn_act(typename MF<T>::F (&h)[AT], f4 (&zg)[AT][MF<T>::NT],
+                                        const f4 (&zu)[AT][MF<T>::NT], ActAB ab) {
+#pragma unroll
+  for (int at = 0; at < AT; ++at) {
+#pragma unroll
+    for (int t = 0; t < MF<T>::NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) zg[at][t][r] = act_val(zg[at][t][r], ab) * zu[at][t][r];
+    h[at] = MF<T>::pack(zg[at]);
+  }
+}
+template <class T, int C, int AT, class WD>
+__device__ __forceinline__ void ffn_down(f4 (&acc)[AT][C / MF<T>::CK][MF<T>::NT], const typename MF<T>::F (&h)[AT], WD wd) {
+  using M = MF<T>;
+#pragma unroll
+  for (int p = 0; p < C / M::CK; ++p)
+#pragma unroll
+    for (int t = 0; t < M::NT; ++t) {
+      const typename M::F f = wd(p, t);
+#pragma unroll
+      for (int at = 0; at < AT; ++at) acc[at][p][t] = M::mma(acc[at][p][t], f, h[at]);
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void ffn_out(const FfnArgs& A, int64_t a, int c, f4* o) {
+  using M = MF<T>;
+  if (A.res) {
+    f4 q[M::NT];
+    M::unpack(*(const typename M::F*)((const T*)A.res + a * A.ldr + c), q);
+#pragma unroll
+    for (int t = 0; t < M::NT; ++t) o[t] += q[t];
+  }
+  st_row<T>((T*)A.y + a * A.ldy + c, o);
+}
+
+// Forward.  Eight waves of 16 AT atoms each share the weights in LDS and walk tiles of rows with a
+// fixed stride.  A step of a wave is a phase of matrix products (the down product of the chunk
+// before, then the two products of this chunk) and a phase of activations; waves 4-7, the second
+// of each SIMD, run half a step behind waves 0-3, so that at any time one wave of a SIMD feeds the
+// matrix cores and the other the VALU (in step, both would wait for the same unit).  A barrier
+// separates the phases.  Weights have two buffers, a chunk's Wd used a step after its Wg and Wu;
+// a half of the waves writes its half of a chunk in its activation phase: the first half what it
+// needs next (Wg, Wu of chunk j + 1, Wd of chunk j), the second half, whose phase lies one barrier
+// later, a chunk further, so both halves of a buffer are written between the same two barriers'
+// last and first readers.  A wave's next rows of x arrive in LDS piece by piece during the chunks
+// of the present ones, so no tile waits for memory.  Bound: the matrix products and, beside
+// them, the sigmoid of every hidden unit (exp and reciprocal).
+template <class T, int C, int AT>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn(FfnArgs A) {
+  using M = MF<T>;
+  using CH = Chunk<T, C, 512, false>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = CH::RS, RD = CH::RD, ROWS = 16 * AT;
+  constexpr int GU = 2 * CK * RS, DN = C * RD, MPF = sizeof(T) == 2 ? 1 : 4;  // MPF: MFMAs per operand pair
+  __shared__ __align__(16) T s[2 * (GU + DN) + 8 * ROWS * RS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
-  const int64_t a0 = SPLIT ? (int64_t)blockIdx.x * 16 : ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
-  typename M::F xf[AT][NC];
-  load_rows<T, C, AT>(xf, A.x, A.ldx, a0, A.n, i, g);
-  f4 acc[AT][NC][NT];
-#pragma unroll
-  for (int at = 0; at < AT; ++at)
-#pragma unroll
-    for (int p = 0; p < NC; ++p)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[at][p][t] = f4{0.f, 0.f, 0.f, 0.f};
-  CH ck;
-  if constexpr (!SPLIT) {
-    ck.fetch(A, 0, threadIdx.x);
-    ck.put(s, threadIdx.x);
-    __syncthreads();
-  }
-  int b = 0;
-  for (int h0 = SPLIT ? CK * wave : 0; h0 < A.hidden; h0 += SPLIT ? 4 * CK : CK, b ^= 1) {
-    const T *wg, *wu, *wd;
-    int ldd;  // row stride of Wd
-    if constexpr (SPLIT) {
-      wg = (const T*)A.wg + (int64_t)h0 * C, wu = (const T*)A.wu + (int64_t)h0 * C, wd = (const T*)A.wd + h0;
-      ldd = A.hidden;
-    } else {
-      wg = s + b * CH::SIZE, wu = wg + CK * RS, wd = wu + CK * RS;
-      ldd = CH::RD;
-      ck.fetch(A, min(h0 + CK, A.hidden - CK), threadIdx.x);
-    }
-    f4 zg[AT][NT], zu[AT][NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int at = 0; at < AT; ++at) zg[at][t] = zu[at][t] = f4{0.f, 0.f, 0.f, 0.f};
-      const int row = (SPLIT ? nat_row<T>(t, i) : 16 * t + i) * RS + EV * g;
-#pragma unroll
-      for (int ch = 0; ch < NC; ++ch) {
-        const typename M::F fg = *(const typename M::F*)(wg + row + ch * CK);
-        const typename M::F fu = *(const typename M::F*)(wu + row + ch * CK);
-#pragma unroll
-        for (int at = 0; at < AT; ++at) {
-          zg[at][t] = M::mma(zg[at][t], fg, xf[at][ch]);
-          zu[at][t] = M::mma(zu[at][t], fu, xf[at][ch]);
-        }
-      }
-    }
-    typename M::F h[AT];
-#pragma unroll
-    for (int at = 0; at < AT; ++at) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) zg[at][t][r] = act_val(zg[at][t][r], A.ab) * zu[at][t][r];
-      h[at] = M::pack(zg[at]);
-    }
-#pragma unroll
-    for (int p = 0; p < NC; ++p)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int row = p * CK + (SPLIT ? nat_row<T>(t, i) : 16 * t + i);
-        const typename M::F f = *(const typename M::F*)(wd + (int64_t)row * ldd + EV * g);
-#pragma unroll
-        for (int at = 0; at < AT; ++at) acc[at][p][t] = M::mma(acc[at][p][t], f, h[at]);
-      }
-    if constexpr (!SPLIT) {
-      ck.put(s + (b ^ 1) * CH::SIZE, threadIdx.x);
-      __syncthreads();
-    }
-  }
-  auto out = [&](int64_t a, int c, f4* o) {
-    if (A.res) {
-      f4 q[NT];
-      M::unpack(*(const typename M::F*)((const T*)A.res + a * A.ldr + c), q);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) o[t] += q[t];
-    }
-    st_row<T>((T*)A.y + a * A.ldy + c, o);
+  T *s_gu = s, *s_d = s + 2 * GU, *xs = s_d + 2 * DN + wave * ROWS * RS;
+  constexpr int VPR = C / EV, PIECES = ROWS * VPR / 64, RJ = 64 / VPR;  // 16-byte pieces a lane moves per tile
+  static_assert(ROWS * VPR % 64 == 0 && 64 % VPR == 0, "whole waves");
+  const int pr = lane / VPR, pc = (lane % VPR) * EV;
+  const int64_t tiles = (A.n + 8 * ROWS - 1) / (8 * ROWS);
+  auto piece = [&](int64_t tile, int k) {  // rows past the end: the last row
+    const int64_t a = min((tile * 8 + wave) * ROWS + pr + k * RJ, A.n - 1);
+    return *(const u4*)((const T*)A.x + a * A.ldx + pc);
   };
-  if constexpr (SPLIT) {
-    float* slab = (float*)s_raw + (16 * wave + i) * OS;
+  auto keep = [&](u4 v, int k) { *(u4*)(xs + (pr + k * RJ) * RS + pc) = v; };
+  const int nk = A.hidden / CK, late = wave >> 2;
+  // chunk k, modulo their number (the next tile starts over)
+  auto chunk = [&](int k) { return (k < nk ? k : (k - nk) % nk) * CK; };
+  {
+    u4 v[PIECES];
 #pragma unroll
-    for (int p = 0; p < NC; ++p)
+    for (int k = 0; k < PIECES; ++k) v[k] = piece(blockIdx.x, k);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) *(f4*)(slab + p * CK + EV * g + 4 * t) = acc[0][p][t];
-    join_waves<T, C>((float*)s_raw, a0, A.n, out);
-  } else {
+    for (int k = 0; k < PIECES; ++k) keep(v[k], k);
+  }
+  CH ck;
+  ck.fetch_gu(A, 0, threadIdx.x);
+  ck.put_gu(s_gu, threadIdx.x);
+  if (late) {
+    ck.fetch_gu(A, chunk(1), threadIdx.x);
+    ck.fetch_d(A, 0, threadIdx.x);
+    ck.put_gu(s_gu + GU, threadIdx.x);
+    ck.put_d(s_d, threadIdx.x);
+  }
+  lds_barrier();
+  if (late) lds_barrier();
+  f4 zg[AT][NT], zu[AT][NT], acc[AT][NC][NT];
+  typename M::F h[AT], xf[AT][NC], res[AT][NC];
+  auto down = [&](int b) {
+    const T* wd = s_d + b * DN + i * RD + EV * g;
+    ffn_down<T, C, AT>(acc, h, [&](int p, int t) { return *(const typename M::F*)(wd + (p * CK + 16 * t) * RD); });
+    read_ahead<NT * NC, 8, NT * NC * AT * MPF>();
+  };
+  int j = 0;  // steps taken
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t a0 = (tile * 8 + wave) * ROWS, next = tile + gridDim.x < tiles ? tile + gridDim.x : tile;
+    wave_sync();
+#pragma unroll
+    for (int at = 0; at < AT; ++at)
+#pragma unroll
+      for (int ch = 0; ch < NC; ++ch) xf[at][ch] = *(const typename M::F*)(xs + (16 * at + i) * RS + ch * CK + EV * g);
+    wave_sync();
+#pragma unroll
+    for (int at = 0; at < AT; ++at)
+#pragma unroll
+      for (int p = 0; p < NC; ++p)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[at][p][t] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < nk; ++k, ++j) {
+      ck.fetch_gu(A, chunk(k + 1 + late), threadIdx.x);
+      ck.fetch_d(A, chunk(k + late), threadIdx.x);
+      u4 xv;
+      if (k < PIECES) xv = piece(next, k);
+      if (k > 0) down((j - 1) & 1);
+      if (A.res && k == nk - 1) {
+#pragma unroll
+        for (int at = 0; at < AT; ++at)
+#pragma unroll
+          for (int p = 0; p < NC; ++p)
+            res[at][p] = *(const typename M::F*)((const T*)A.res + min(a0 + 16 * at + i, A.n - 1) * A.ldr + p * CK + EV * g);
+      }
+      const T *wg = s_gu + (j & 1) * GU + i * RS + EV * g, *wu = wg + CK * RS;
+      ffn_in<T, C, AT>(zg, zu, xf, [&](int t, int ch) { return *(const typename M::F*)(wg + 16 * t * RS + ch * CK); },
+                       [&](int t, int ch) { return *(const typename M::F*)(wu + 16 * t * RS + ch * CK); });
+      read_ahead<2 * NT * NC, 8, 2 * NT * NC * AT * MPF>();
+      lds_barrier();
+      ffn_act<T, AT>(h, zg, zu, A.ab);
+      ck.put_gu(s_gu + ((j + 1 + late) & 1) * GU, threadIdx.x);
+      ck.put_d(s_d + ((j + late) & 1) * DN, threadIdx.x);
+      if (k < PIECES) keep(xv, k);
+      lds_barrier();
+    }
+    down((j - 1) & 1);
+    for (int k = nk; k < PIECES; ++k) keep(piece(next, k), k);  // fewer chunks than pieces
 #pragma unroll
     for (int at = 0; at < AT; ++at) {
       const int64_t a = a0 + 16 * at + i;
       if (a >= A.n) continue;
 #pragma unroll
-      for (int p = 0; p < NC; ++p) out(a, p * CK + EV * g, acc[at][p]);
+      for (int p = 0; p < NC; ++p) {
+        if (A.res) {
+          f4 q[NT];
+          M::unpack(res[at][p], q);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[at][p][t] += q[t];
+        }
+        st_row<T>((T*)A.y + a * A.ldy + p * CK + EV * g, acc[at][p]);
+      }
     }
   }
+  if (!late) lds_barrier();  // as many as the late half
+}
+
+// Forward for few rows: the four waves of a block take the same 16 atoms and every fourth chunk
+// each, weights straight from L2, and their sums are joined in wave order.
+template <class T, int C>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn_few(FfnArgs A) {
+  using M = MF<T>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, OS = C + 4;
+  __shared__ __align__(16) float s_o[64 * OS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
+  const int64_t a0 = (int64_t)blockIdx.x * 16;
+  typename M::F xf[1][NC];
+  load_rows<T, C, 1>(xf, A.x, A.ldx, a0, A.n, i, g);
+  f4 acc[1][NC][NT];
+#pragma unroll
+  for (int p = 0; p < NC; ++p)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[0][p][t] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int h0 = CK * wave; h0 < A.hidden; h0 += 4 * CK) {
+    const T *wg = (const T*)A.wg + (int64_t)h0 * C + EV * g, *wu = (const T*)A.wu + (int64_t)h0 * C + EV * g;
+    const T* wd = (const T*)A.wd + h0 + EV * g;
+    f4 zg[1][NT], zu[1][NT];
+    typename M::F h[1];
+    ffn_in<T, C, 1>(zg, zu, xf, [&](int t, int ch) { return *(const typename M::F*)(wg + nat_row<T>(t, i) * C + ch * CK); },
+                    [&](int t, int ch) { return *(const typename M::F*)(wu + nat_row<T>(t, i) * C + ch * CK); });
+    ffn_act<T, 1>(h, zg, zu, A.ab);
+    ffn_down<T, C, 1>(
+        acc, h, [&](int p, int t) { return *(const typename M::F*)(wd + (int64_t)(p * CK + nat_row<T>(t, i)) * A.hidden); });
+  }
+  float* slab = s_o + (16 * wave + i) * OS;
+#pragma unroll
+  for (int p = 0; p < NC; ++p)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) *(f4*)(slab + p * CK + EV * g + 4 * t) = acc[0][p][t];
+  join_waves<T, C>(s_o, a0, A.n, [&](int64_t a, int c, f4* o) { ffn_out<T>(A, a, c, o); });
 }
 
 // gradients of the hidden pre-activations: with h = act(zg) zu,
@@ -413,9 +525,9 @@ int launch_ffn_c(FfnArgs A, int what, hipStream_t st) {
     const unsigned blocks = (unsigned)cdiv(A.n, few ? 16 : 64 * AT);
     if (what == 0) {
       if (few)
-        k_ffn<T, C, 1, true><<<blocks, 256, 0, st>>>(A);
+        k_ffn_few<T, C><<<blocks, 256, 0, st>>>(A);
       else
-        k_ffn<T, C, AT, false><<<blocks, 256, 0, st>>>(A);
+        k_ffn<T, C, AT><<<(unsigned)std::min<int64_t>(cdiv(A.n, 128 * AT), 256), 512, 0, st>>>(A);
     } else {
       if (few)
         k_ffn_dx<T, C, 1, true><<<blocks, 256, 0, st>>>(A);
