@@ -17,76 +17,127 @@ struct LinArgs {
   int64_t rows_per_split;
 };
 
-// Forward: D[o][a] = sum_c W[o][c] x[a][c].  A wave keeps the rows of 16 AT atoms in registers
-// as one operand and walks the outputs CK at a time, the other operand read straight from W
-// (at most 256 KB, so L1/L2 hold it).  W's rows are taken in the order nat_row, which leaves
-// EV consecutive outputs of an atom in each lane: bias, activation, residual and the 16-byte
-// stores follow without an exchange.  gridDim.y splits the outputs when there are few rows.
-// Bound: HBM (the y rows).
-template <class T, int C, int AT>
-__global__ __launch_bounds__(256) void k_linear(LinArgs A) {
+// EV outputs of one atom: bias, activation, residual, 16-byte store
+template <class T>
+__device__ __forceinline__ void lin_out(const LinArgs& A, int64_t a, int oe, const f4* bias, f4* o) {
+  using M = MF<T>;
+#pragma unroll
+  for (int t = 0; t < M::NT; ++t) o[t] += bias[t];
+  if (A.act) {
+#pragma unroll
+    for (int t = 0; t < M::NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[t][r] = act_val(o[t][r], A.ab);
+  }
+  if (A.res) {
+    f4 q[M::NT];
+    M::unpack(*(const typename M::F*)((const T*)A.res + a * A.ldr + oe), q);
+#pragma unroll
+    for (int t = 0; t < M::NT; ++t) o[t] += q[t];
+  }
+  st_row<T>((T*)A.y + a * A.ldy + oe, o);
+}
+template <int NT>
+__device__ __forceinline__ void lin_bias(const LinArgs& A, int oe, f4* b) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    b[t] = f4{0.f, 0.f, 0.f, 0.f};
+    if (A.bias && oe < A.out)
+      b[t] = f4{A.bias[oe + 4 * t], A.bias[oe + 4 * t + 1], A.bias[oe + 4 * t + 2], A.bias[oe + 4 * t + 3]};
+  }
+}
+
+// Forward, few rows: D[o][a] = sum_c W[o][c] x[a][c].  A wave keeps 16 atoms' rows in registers as
+// one operand and walks the outputs CK at a time, the other operand read straight from W.  W's
+// rows are taken in the order nat_row, which leaves EV consecutive outputs of an atom in each
+// lane: bias, activation, residual and the 16-byte stores follow without an exchange.
+// gridDim.y splits the outputs.
+template <class T, int C>
+__global__ __launch_bounds__(256) void k_linear_few(LinArgs A) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int64_t a0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
-  if (a0 >= A.n) return;
-  typename M::F xf[AT][NC];
+  const int64_t a = ((int64_t)blockIdx.x * 4 + wave) * 16 + i;
+  if (a - i >= A.n) return;
+  typename M::F xf[NC];
+  const T* p = (const T*)A.x + a * A.ldx + EV * g;
 #pragma unroll
-  for (int at = 0; at < AT; ++at) {
-    const int64_t a = a0 + 16 * at + i;
-    const T* p = (const T*)A.x + a * A.ldx + EV * g;
-#pragma unroll
-    for (int ch = 0; ch < NC; ++ch) xf[at][ch] = ld16<typename M::F>(p + ch * M::CK, a < A.n);
-  }
+  for (int ch = 0; ch < NC; ++ch) xf[ch] = ld16<typename M::F>(p + ch * M::CK, a < A.n);
   const int ngr = (A.out + OG - 1) / OG;
   const int per = (ngr + gridDim.y - 1) / gridDim.y;
   const int g0 = blockIdx.y * per, g1 = min(ngr, g0 + per);
   for (int og = g0; og < g1; ++og) {
-    const int o0 = og * OG, oe = o0 + EV * g;
-    f4 acc[AT][NT];
+    const int oe = og * OG + EV * g;
+    f4 acc[NT], bias[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int row = min(o0 + nat_row<T>(t, i), A.out - 1);
-      const T* wp = (const T*)A.w + (int64_t)row * C + EV * g;
-      typename M::F wf[NC];
+      const T* wp = (const T*)A.w + (int64_t)min(og * OG + nat_row<T>(t, i), A.out - 1) * C + EV * g;
+      acc[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ch = 0; ch < NC; ++ch) wf[ch] = *(const typename M::F*)(wp + ch * M::CK);
-#pragma unroll
-      for (int at = 0; at < AT; ++at) {
-        f4 s = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ch = 0; ch < NC; ++ch) s = M::mma(s, wf[ch], xf[at][ch]);
-        acc[at][t] = s;
-      }
+      for (int ch = 0; ch < NC; ++ch) acc[t] = M::mma(acc[t], *(const typename M::F*)(wp + ch * M::CK), xf[ch]);
     }
-    if (oe >= A.out) continue;
-    if (A.bias) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const f4 b = f4{A.bias[oe + 4 * t], A.bias[oe + 4 * t + 1], A.bias[oe + 4 * t + 2], A.bias[oe + 4 * t + 3]};
-#pragma unroll
-        for (int at = 0; at < AT; ++at) acc[at][t] += b;
-      }
-    }
-    if (A.act) {
-#pragma unroll
-      for (int at = 0; at < AT; ++at)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[at][t][r] = act_val(acc[at][t][r], A.ab);
-    }
+    lin_bias<NT>(A, oe, bias);
+    if (a < A.n && oe < A.out) lin_out<T>(A, a, oe, bias, acc);
+  }
+}
+
+// Forward, many rows: the same product with OB outputs' rows of W resident in LDS (in the order
+// nat_slot) for the whole walk of a block over its rows; each of the eight waves walks tiles of
+// 16 AT atoms by itself, the next tile's rows on their way.  gridDim.y covers the outputs.
+// Bound: HBM (the y rows).  W read from L2 by every wave instead: 160 us for 328,378 rows of
+// 128 -> 384 in bf16 (the traffic of L1).
+template <class T, int C, int OB, int AT>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k_linear(LinArgs A) {
+  using M = MF<T>;
+  constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK, RS = C + lds_pad<T>(), VPR = C / EV;
+  __shared__ __align__(16) T s_w[OB * RS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
+  const int ob = blockIdx.y * OB, no = min(OB, A.out - ob);
+  const int64_t tiles = (A.n + 16 * AT - 1) / (16 * AT), step = (int64_t)gridDim.x * 8;
+  int64_t tile = (int64_t)blockIdx.x * 8 + wave;
+  typename M::F xf[AT][NC], xn[AT][NC];
+  auto fetch = [&](int64_t tl) {  // rows past the end: the last row
 #pragma unroll
     for (int at = 0; at < AT; ++at) {
-      const int64_t a = a0 + 16 * at + i;
-      if (a >= A.n) continue;
-      if (A.res) {
-        f4 q[NT];
-        M::unpack(*(const typename M::F*)((const T*)A.res + a * A.ldr + oe), q);
+      const int64_t a = min(tl * (16 * AT) + 16 * at + i, A.n - 1);
+      const T* p = (const T*)A.x + a * A.ldx + EV * g;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[at][t] += q[t];
+      for (int ch = 0; ch < NC; ++ch) xn[at][ch] = *(const typename M::F*)(p + ch * M::CK);
+    }
+  };
+  fetch(tile);
+  for (int x = threadIdx.x; x < no * VPR; x += 512) {
+    const int r = x / VPR, c = (x % VPR) * EV;
+    *(u4*)(s_w + nat_slot<T>(r) * RS + c) = *(const u4*)((const T*)A.w + (int64_t)(ob + r) * C + c);
+  }
+  __syncthreads();
+  for (; tile < tiles; tile += step) {
+#pragma unroll
+    for (int at = 0; at < AT; ++at)
+#pragma unroll
+      for (int ch = 0; ch < NC; ++ch) xf[at][ch] = xn[at][ch];
+    fetch(tile + step);
+    for (int o0 = 0; o0 < no; o0 += OG) {
+      const int oe = ob + o0 + EV * g;
+      f4 acc[AT][NT], bias[NT];
+      lin_bias<NT>(A, oe, bias);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const T* wp = s_w + (o0 + 16 * t + i) * RS + EV * g;
+#pragma unroll
+        for (int at = 0; at < AT; ++at) acc[at][t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+          const typename M::F f = *(const typename M::F*)(wp + ch * M::CK);
+#pragma unroll
+          for (int at = 0; at < AT; ++at) acc[at][t] = M::mma(acc[at][t], f, xf[at][ch]);
+        }
       }
-      st_row<T>((T*)A.y + a * A.ldy + oe, acc[at]);
+#pragma unroll
+      for (int at = 0; at < AT; ++at) {
+        const int64_t a = tile * (16 * AT) + 16 * at + i;
+        if (a < A.n && oe < A.out) lin_out<T>(A, a, oe, bias, acc[at]);
+      }
     }
   }
 }
@@ -284,21 +335,23 @@ int64_t dw_splits(int64_t n, int out) {
 template <class T>
 int launch_linear(const LinArgs& A0, int C, int what, hipStream_t st) {
   LinArgs A = A0;
-  constexpr int AT = sizeof(T) == 2 ? 2 : 1;
-  const int ngr = (int)cdiv(A.out, MF<T>::CK);
-  // few rows: one 16-atom tile per wave and the outputs split over gridDim.y
-  const bool few = cdiv(A.n, 64 * AT) < 512;
-  const int64_t bx = few ? cdiv(A.n, 64) : cdiv(A.n, 64 * AT);
-  const int by = (int)std::max<int64_t>(1, std::min<int64_t>(ngr, 512 / bx));
+  constexpr int AT = 2, BIG = sizeof(T) == 2 ? 512 : 256;  // outputs whose rows fit LDS at C = 128
+  // few rows: every wave takes one 16-atom tile, and the outputs are split too
+  const bool few = A.n < 65536;
+  const int64_t bx = few ? cdiv(A.n, 64) : std::min<int64_t>(cdiv(A.n, 128 * AT), A.out <= 128 ? 512 : 256);
+  const int by = few ? (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(A.out, MF<T>::CK), 512 / bx))
+                     : (int)cdiv(A.out, A.out <= 128 ? 128 : BIG);
   const int64_t S = dw_splits(A.n, A.out);
   A.rows_per_split = cdiv(cdiv(A.n, S), MF<T>::CK) * MF<T>::CK;
 #define MP_CASE(CC)                                                                         \
   case CC:                                                                                  \
     if (what == 0) {                                                                        \
       if (few)                                                                              \
-        k_linear<T, CC, 1><<<dim3((unsigned)bx, by), 256, 0, st>>>(A);                      \
+        k_linear_few<T, CC><<<dim3((unsigned)bx, by), 256, 0, st>>>(A);                     \
+      else if (A.out <= 128)                                                                \
+        k_linear<T, CC, 128, AT><<<dim3((unsigned)bx, by), 512, 0, st>>>(A);                \
       else                                                                                  \
-        k_linear<T, CC, AT><<<dim3((unsigned)bx, by), 256, 0, st>>>(A);                     \
+        k_linear<T, CC, BIG, AT><<<dim3((unsigned)bx, by), 512, 0, st>>>(A);                \
     } else if (what == 1) {                                                                 \
       if (cdiv(A.n, 64) < 512)                                                              \
         k_linear_dx<T, CC, true><<<(unsigned)cdiv(A.n, 16), 256, 0, st>>>(A);               \

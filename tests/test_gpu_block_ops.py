@@ -43,6 +43,10 @@ LINEAR = [
     (129, 32, 80, "f32", "sigmoid", True, False, 0),
     (700, 64, 208, "f32", "silu", False, True, 12),
     (515, 128, 144, "f32", "none", False, False, 128),
+    (70001, 128, 400, "bf16", "silu", True, True, 8),
+    (66000, 64, 96, "f32", "none", True, False, 4),
+    (65537, 32, 304, "f32", "sigmoid", False, False, 0),
+    (65999, 32, 16, "bf16", "none", False, True, 0),
 ]
 
 
