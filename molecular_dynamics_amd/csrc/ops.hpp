@@ -151,6 +151,16 @@ __device__ __forceinline__ void st_row(T* p, const f4* t) {
   *(typename MF<T>::F*)p = MF<T>::pack(t);
 }
 
+// the same, past the caches if STREAM (a compile-time choice: stores that differ in nothing else are
+// merged, and lose the hint)
+template <bool STREAM, class T>
+__device__ __forceinline__ void st_row(T* p, const f4* t) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(__builtin_bit_cast(u4, MF<T>::pack(t)), (u4*)p);
+  else
+    st_row<T>(p, t);
+}
+
 // four consecutive elements
 __device__ __forceinline__ void st4(float* p, f4 v) { *(f4*)p = v; }
 __device__ __forceinline__ void st4(uint16_t* p, f4 v) { *(u2*)p = u2{pk2bf(v.x, v.y), pk2bf(v.z, v.w)}; }

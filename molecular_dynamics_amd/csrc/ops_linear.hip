@@ -15,10 +15,11 @@ struct LinArgs {
   void *y, *dx;
   float* part;           // [splits][out C + out]: dW, then dbias
   int64_t rows_per_split;
+  bool stream;  // y past the caches
 };
 
 // EV outputs of one atom: bias, activation, residual, 16-byte store
-template <class T>
+template <class T, bool STREAM>
 __device__ __forceinline__ void lin_out(const LinArgs& A, int64_t a, int oe, const f4* bias, f4* o) {
   using M = MF<T>;
 #pragma unroll
@@ -35,7 +36,7 @@ __device__ __forceinline__ void lin_out(const LinArgs& A, int64_t a, int oe, con
 #pragma unroll
     for (int t = 0; t < M::NT; ++t) o[t] += q[t];
   }
-  st_row<T>((T*)A.y + a * A.ldy + oe, o);
+  st_row<STREAM>((T*)A.y + a * A.ldy + oe, o);
 }
 template <int NT>
 __device__ __forceinline__ void lin_bias(const LinArgs& A, int oe, f4* b) {
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(256) void k_linear_few(LinArgs A) {
       for (int ch = 0; ch < NC; ++ch) acc[t] = M::mma(acc[t], *(const typename M::F*)(wp + ch * M::CK), xf[ch]);
     }
     lin_bias<NT>(A, oe, bias);
-    if (a < A.n && oe < A.out) lin_out<T>(A, a, oe, bias, acc);
+    if (a < A.n && oe < A.out) lin_out<T, false>(A, a, oe, bias, acc);
   }
 }
 
@@ -86,7 +87,7 @@ __global__ __launch_bounds__(256) void k_linear_few(LinArgs A) {
 // 16 AT atoms by itself, the next tile's rows on their way.  gridDim.y covers the outputs.
 // Bound: HBM (the y rows).  W read from L2 by every wave instead: 160 us for 328,378 rows of
 // 128 -> 384 in bf16 (the traffic of L1).
-template <class T, int C, int OB, int AT>
+template <class T, int C, int OB, int AT, bool STREAM>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k_linear(LinArgs A) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, OG = M::CK, RS = C + lds_pad<T>(), VPR = C / EV;
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) void k
 #pragma unroll
       for (int at = 0; at < AT; ++at) {
         const int64_t a = tile * (16 * AT) + 16 * at + i;
-        if (a < A.n && oe < A.out) lin_out<T>(A, a, oe, bias, acc[at]);
+        if (a < A.n && oe < A.out) lin_out<T, STREAM>(A, a, oe, bias, acc[at]);
       }
     }
   }
@@ -332,13 +333,19 @@ int64_t dw_splits(int64_t n, int out) {
   return std::max<int64_t>(1, std::min<int64_t>(512 / nb, cdiv(n, 32)));
 }
 
+template <class T, int C, int OB>
+void launch_linear_big(const LinArgs& A, dim3 grid, hipStream_t st) {
+  auto* k = A.stream ? k_linear<T, C, OB, 2, true> : k_linear<T, C, OB, 2, false>;
+  k<<<grid, 512, 0, st>>>(A);
+}
+
 template <class T>
 int launch_linear(const LinArgs& A0, int C, int what, hipStream_t st) {
   LinArgs A = A0;
-  constexpr int AT = 2, BIG = sizeof(T) == 2 ? 512 : 256;  // outputs whose rows fit LDS at C = 128
+  constexpr int BIG = sizeof(T) == 2 ? 512 : 256;  // outputs whose rows fit LDS at C = 128
   // few rows: every wave takes one 16-atom tile, and the outputs are split too
   const bool few = A.n < 65536;
-  const int64_t bx = few ? cdiv(A.n, 64) : std::min<int64_t>(cdiv(A.n, 128 * AT), A.out <= 128 ? 512 : 256);
+  const int64_t bx = few ? cdiv(A.n, 64) : std::min<int64_t>(cdiv(A.n, 256), A.out <= 128 ? 512 : 256);
   const int by = few ? (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(A.out, MF<T>::CK), 512 / bx))
                      : (int)cdiv(A.out, A.out <= 128 ? 128 : BIG);
   const int64_t S = dw_splits(A.n, A.out);
@@ -349,9 +356,9 @@ int launch_linear(const LinArgs& A0, int C, int what, hipStream_t st) {
       if (few)                                                                              \
         k_linear_few<T, CC><<<dim3((unsigned)bx, by), 256, 0, st>>>(A);                     \
       else if (A.out <= 128)                                                                \
-        k_linear<T, CC, 128, AT><<<dim3((unsigned)bx, by), 512, 0, st>>>(A);                \
+        launch_linear_big<T, CC, 128>(A, dim3((unsigned)bx, by), st);                       \
       else                                                                                  \
-        k_linear<T, CC, BIG, AT><<<dim3((unsigned)bx, by), 512, 0, st>>>(A);                \
+        launch_linear_big<T, CC, BIG>(A, dim3((unsigned)bx, by), st);                       \
     } else if (what == 1) {                                                                 \
       if (cdiv(A.n, 64) < 512)                                                              \
         k_linear_dx<T, CC, true><<<(unsigned)cdiv(A.n, 16), 256, 0, st>>>(A);               \
@@ -410,6 +417,7 @@ extern "C" int mp_linear(int32_t n, int32_t in, int32_t out, int32_t dt, int32_t
   if (residual) MP_ROWS("mp_linear", "residual", residual, ldr, out, dt);
   ops::LinArgs A = ops::lin_args(n, out, act, x, ldx, w, bias);
   A.res = residual, A.ldr = ldr, A.y = y, A.ldy = ldy;
+  A.stream = ops::streams((int64_t)n * (in + (int64_t)out * (residual ? 2 : 1)) * (dt == 1 ? 2 : 4));
   ProfScope p("linear", st);
   return dt == 1 ? ops::launch_linear<uint16_t>(A, in, 0, st) : ops::launch_linear<float>(A, in, 0, st);
 }

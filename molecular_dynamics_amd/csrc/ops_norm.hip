@@ -24,11 +24,12 @@ struct Row {
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = t[j / 4][j % 4];
   }
+  template <bool STREAM>
   __device__ __forceinline__ void store(T* p) const {
     f4 t[2];
 #pragma unroll
     for (int j = 0; j < V; ++j) t[j / 4][j % 4] = v[j];
-    *(typename MF<T>::F*)p = MF<T>::pack(t);
+    st_row<STREAM>(p, t);
   }
 };
 
@@ -59,9 +60,10 @@ struct NormPtrs {
   const void *dy, *du;            // backward inputs (either may be null); strides ldy, ldu
   void *dx, *db, *dg;             // backward outputs (nullable)
   float* part;                    // [blocks][3][C]
+  bool stream;                    // outputs past the caches
 };
 
-template <class T, int C>
+template <class T, int C, bool STREAM>
 __global__ __launch_bounds__(256) void k_norm_block(NormPtrs A) {
   constexpr int V = MF<T>::EV, LR = C / V, RPB = 256 / LR;
   const int rl = threadIdx.x / LR, c0 = (threadIdx.x % LR) * V;
@@ -88,7 +90,7 @@ __global__ __launch_bounds__(256) void k_norm_block(NormPtrs A) {
       const float gs = A.gate ? sc[j] * sigm(g.v[j]) : sc[j];
       x.v[j] = fmaf(gs, wp[j] * (b.v[j] * ib), x.v[j]);
     }
-    x.store((T*)A.y + row * A.ldy + c0);
+    x.template store<STREAM>((T*)A.y + row * A.ldy + c0);
     if (A.u) {
       float s = 0.f;
 #pragma unroll
@@ -96,7 +98,7 @@ __global__ __launch_bounds__(256) void k_norm_block(NormPtrs A) {
       const float iy = rsq(group_sum<LR>(s) * (1.0f / C) + A.eps);
 #pragma unroll
       for (int j = 0; j < V; ++j) x.v[j] = wq[j] * (x.v[j] * iy);
-      x.store((T*)A.u + row * A.ldu + c0);
+      x.template store<STREAM>((T*)A.u + row * A.ldu + c0);
     }
   }
 }
@@ -105,7 +107,7 @@ __global__ __launch_bounds__(256) void k_norm_block(NormPtrs A) {
 // gradients follow the chain above, and each lane keeps the sums over its rows of the three
 // parameter gradients of its channels.  Blocks walk rows with a fixed stride and write one
 // partial row each, added up in block order afterwards, so repeated calls give equal bits.
-template <class T, int C>
+template <class T, int C, bool STREAM>
 __global__ __launch_bounds__(256) void k_norm_block_bwd(NormPtrs A) {
   constexpr int V = MF<T>::EV, LR = C / V, RPB = 256 / LR;
   __shared__ float s_p[RPB][3 * C];
@@ -157,7 +159,7 @@ __global__ __launch_bounds__(256) void k_norm_block_bwd(NormPtrs A) {
 #pragma unroll
       for (int j = 0; j < V; ++j) dy.v[j] = fmaf(iy, fmaf(-x.v[j], t, du.v[j]), dy.v[j]);
     }
-    if (A.dx) dy.store((T*)A.dx + row * A.lddx + c0);
+    if (A.dx) dy.template store<STREAM>((T*)A.dx + row * A.lddx + c0);
     float t = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -169,14 +171,14 @@ __global__ __launch_bounds__(256) void k_norm_block_bwd(NormPtrs A) {
       dy.v[j] *= wp[j];
       t = fmaf(dy.v[j], b.v[j], t);
     }
-    if (A.dg) g.store((T*)A.dg + row * A.lddg + c0);
+    if (A.dg) g.template store<STREAM>((T*)A.dg + row * A.lddg + c0);
     if (A.db) {
       if (A.w_post) {
         t = group_sum<LR>(t) * (1.0f / C);
 #pragma unroll
         for (int j = 0; j < V; ++j) dy.v[j] = ib * fmaf(-b.v[j], t, dy.v[j]);
       }
-      dy.store((T*)A.db + row * A.lddb + c0);
+      dy.template store<STREAM>((T*)A.db + row * A.lddb + c0);
     }
   }
   if (!A.part) return;
@@ -195,14 +197,18 @@ __global__ __launch_bounds__(256) void k_norm_block_bwd(NormPtrs A) {
   }
 }
 
+template <class T, int C>
+void launch_norm_c(const NormPtrs& A, bool bwd, int blocks, hipStream_t st) {
+  auto* k = bwd ? (A.stream ? k_norm_block_bwd<T, C, true> : k_norm_block_bwd<T, C, false>)
+                : (A.stream ? k_norm_block<T, C, true> : k_norm_block<T, C, false>);
+  k<<<blocks, 256, 0, st>>>(A);
+}
+
 template <class T>
 int launch_norm(const NormPtrs& A, int C, bool bwd, int blocks, hipStream_t st) {
-#define MP_CASE(CC)                                                                       \
-  case CC:                                                                                \
-    if (bwd)                                                                              \
-      k_norm_block_bwd<T, CC><<<blocks, 256, 0, st>>>(A);                                 \
-    else                                                                                  \
-      k_norm_block<T, CC><<<blocks, 256, 0, st>>>(A);                                     \
+#define MP_CASE(CC)                            \
+  case CC:                                     \
+    launch_norm_c<T, CC>(A, bwd, blocks, st);  \
     break;
   switch (C) {
     MP_CASE(32)
@@ -317,6 +323,7 @@ extern "C" int mp_norm_block(const mp_norm_args* a, void* y, int64_t ldy, void* 
   MP_ROWS("mp_norm_block", "y", y, ldy, a->channels, a->feat_dtype);
   if (u) MP_ROWS("mp_norm_block", "u", u, ldu, a->channels, a->feat_dtype);
   A.y = y, A.ldy = ldy, A.u = u, A.ldu = ldu;
+  A.stream = ops::streams((int64_t)a->n * a->channels * (a->feat_dtype == 1 ? 2 : 4) * (3 + !!a->gate + !!u));
   ProfScope p("norm_block", st);
   const int blocks = ops::norm_blocks(a->n, a->channels, a->feat_dtype == 1, 8192);
   return a->feat_dtype == 1 ? ops::launch_norm<uint16_t>(A, a->channels, false, blocks, st)
@@ -352,6 +359,8 @@ extern "C" int mp_norm_block_bwd(const mp_norm_args* a, const void* dy, int64_t 
   }
   A.dy = dy, A.ldy = lddy, A.du = du, A.ldu = lddu;
   A.dx = dx, A.lddx = lddx, A.db = db, A.lddb = lddb, A.dg = dgate, A.lddg = lddg;
+  A.stream = ops::streams((int64_t)a->n * C * (dt == 1 ? 2 : 4) *
+                          (2 + !!a->gate + !!dy + !!du + !!dx + !!db + !!dgate));
   int blocks = 0;
   if (params) {
     size_t need = 0;
