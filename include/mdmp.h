@@ -372,11 +372,15 @@ typedef struct {
   const void* v;
   int64_t ldv;
 } mp_attention_args;
-/* saved (nullable): float32 of mp_structure_attention_saved count, what the backward
+/* ws: needed where mp_structure_attention_ws reports bytes (few long structures, whose
+ * other side is split over blocks); 0 bytes: may be null.
+ * saved (nullable): float32 of mp_structure_attention_saved count, what the backward
  * pass needs of this call (with it, bf16 attention weights enter the sum with twice
  * the bits, so out may differ from a call without it in its last bit). */
 int mp_structure_attention_saved(int32_t n, int32_t channels, int32_t heads, int32_t feat_dtype, int64_t* floats);
-int mp_structure_attention(const mp_attention_args* a, void* out, int64_t ldo, float* saved, hipStream_t stream);
+int mp_structure_attention_ws(int32_t n, int32_t n_struct, int32_t channels, int32_t heads, size_t* bytes);
+int mp_structure_attention(const mp_attention_args* a, void* out, int64_t ldo, float* saved, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
 /* Gradients for dout: dq, dk, dv rows; dpos [n][3] and dslope [heads] float32 (nullable;
  * need pos and slope).  out: the forward's output. */
 int mp_structure_attention_bwd_ws(int32_t n, int32_t n_struct, int32_t channels, int32_t heads, size_t* bytes);

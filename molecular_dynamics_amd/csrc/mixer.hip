@@ -1,5 +1,6 @@
 // Energy and forces with global blocks (attention beyond the cutoff, feed-forward) between
 // the last layer and the readout: the block operators in sequence, forward and backward.
+#include <algorithm>
 #include <cmath>
 #include <vector>
 
@@ -31,7 +32,7 @@ struct Saved {
 struct Carve {
   Saved s[MP_MAX_BLOCKS];
   void *dx, *du, *db, *da, *dqkv;  // gradients, one block's at a time
-  void* ws;                        // attention backward
+  void* ws;                        // of the attention calls, one at a time
   size_t ws_bytes;
 };
 
@@ -48,7 +49,10 @@ int carve(Arena& a, const mp_mixer* M, int32_t n, int32_t n_struct, Carve& w) {
     s.dpos = a.take<float>((int64_t)n * 3);
   }
   w.dx = rows(M->C), w.du = rows(M->C), w.db = rows(M->C), w.da = rows(M->C), w.dqkv = rows(3 * M->C);
+  size_t fwd = 0;
+  MP_TRY(mp_structure_attention_ws(n, n_struct, M->C, M->H, &fwd));
   MP_TRY(mp_structure_attention_bwd_ws(n, n_struct, M->C, M->H, &w.ws_bytes));
+  w.ws_bytes = std::max(w.ws_bytes, fwd);
   w.ws = a.take<char>((int64_t)w.ws_bytes);
   return MP_OK;
 }
@@ -138,7 +142,7 @@ int mixer_forward(const MixRun& R, const Plan& P, const mp_graph* g, void* h, hi
     Saved& s = w.s[t];
     MP_TRY(mp_linear(n, C, 3 * C, dt, MP_ACT_NONE, s.u1, C, W.wqkv, nullptr, nullptr, 0, s.qkv, 3 * C, st));
     const mp_attention_args aa = attention_args(R, M, W, g, s.qkv);
-    MP_TRY(mp_structure_attention(&aa, s.att, C, s.stat, st));
+    MP_TRY(mp_structure_attention(&aa, s.att, C, s.stat, w.ws, w.ws_bytes, st));
     MP_TRY(mp_linear(n, C, C, dt, MP_ACT_NONE, s.att, C, W.wo, nullptr, nullptr, 0, s.o, C, st));
     na = norm_args(M, n, s.x0, C, s.o, C, W.s1, W.p1, W.w2);
     MP_TRY(mp_norm_block(&na, s.x1, C, s.u2, C, st));

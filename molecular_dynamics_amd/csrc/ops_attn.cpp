@@ -1,4 +1,5 @@
 // C ABI of the attention between all atoms of each structure.
+#include <algorithm>
 #include <cmath>
 
 #include "ops_api.hpp"
@@ -12,6 +13,18 @@ namespace {
 // alone.  Longer ones: four waves share the 16 atoms and split the other side, which fills
 // the chip with a quarter of the atoms and quarters each wave's walk.
 constexpr int kSplitAbove = 64;
+
+bool split_waves(int64_t n, int64_t n_struct) { return n > kSplitAbove * n_struct; }
+
+// Splits of the other side over blocks, for few long structures: towards 4,096 blocks (the chip
+// holds 512 at a time, and a last round that is not full should be a small part of the whole),
+// each with at least 512 atoms of the other side for its four waves, at most 8 (each costs a
+// float32 partial of the rows, written and read once).
+int splits_of(int64_t n, int64_t n_struct) {
+  if (!split_waves(n, n_struct)) return 1;
+  const int64_t blocks = n / 16 + n_struct, mean = n / n_struct;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(4096, blocks), mean / 512, 8}));
+}
 
 // the kernels address the rows of one step by 32-bit offsets from a 64-bit base
 constexpr int64_t kMaxLd = 1 << 24;
@@ -43,6 +56,7 @@ int attn_args(const char* who, const mp_attention_args* a, AttnArgs& A) {
   A.unit = a->box_L > 0 ? (float)((double)a->box_L / 4294967296.0) : 1.0f;
   A.scale = (float)(1.0 / std::sqrt((double)(a->channels / a->heads)));
   A.cap = a->cap;
+  A.splits = 1;
   if (a->n == 0 || a->n_struct == 0) return MP_OK;
   if (!a->struct_ptr) return arg_error(std::string(who) + ": null struct_ptr");
   if (!a->q || !a->k || !a->v) return arg_error(std::string(who) + ": null q, k or v");
@@ -56,10 +70,28 @@ int attn_args(const char* who, const mp_attention_args* a, AttnArgs& A) {
 }
 
 int launch(const mp_attention_args* a, const AttnArgs& A, int what, hipStream_t st) {
-  const bool split = (int64_t)a->n > (int64_t)kSplitAbove * a->n_struct;
+  const bool split = split_waves(a->n, a->n_struct);
   const int dh = a->channels / a->heads;
   return a->feat_dtype == 1 ? launch_attn_bf16(A, a->channels, dh, split, what, st)
                             : launch_attn_f32(A, a->channels, dh, split, what, st);
+}
+
+// workspace of the backward passes
+struct BwdWs {
+  int splits;
+  int64_t blocks;  // of the row pass: partials of dslope
+  float *dsum, *slope, *dq, *dk, *dv, *row, *col;
+};
+void carve_bwd(Arena& ar, int64_t n, int64_t n_struct, int C, int H, BwdWs& w) {
+  w.splits = n > 0 && n_struct > 0 ? splits_of(n, n_struct) : 1;
+  w.blocks = w.splits * (n / 16 + n_struct);
+  w.dsum = ar.take<float>(n * H);
+  w.slope = ar.take<float>(w.blocks * H);
+  w.dq = w.dk = w.dv = w.row = w.col = nullptr;
+  if (w.splits == 1) return;
+  w.dq = ar.take<float>(w.splits * n * C), w.dk = ar.take<float>(w.splits * n * C);
+  w.dv = ar.take<float>(w.splits * n * C);
+  w.row = ar.take<float>(w.splits * n * 3), w.col = ar.take<float>(w.splits * n * 3);
 }
 
 // saved: [n][C] unrounded output (bf16 features only), then [n][H] base-2 log-sums
@@ -78,8 +110,16 @@ extern "C" int mp_structure_attention_saved(int32_t n, int32_t channels, int32_t
   return MP_OK;
 }
 
-extern "C" int mp_structure_attention(const mp_attention_args* a, void* out, int64_t ldo, float* saved,
-                                      hipStream_t st) {
+extern "C" int mp_structure_attention_ws(int32_t n, int32_t n_struct, int32_t channels, int32_t heads, size_t* bytes) {
+  MP_TRY(ops::check_shape("mp_structure_attention_ws", n, channels, heads, 0));
+  if (n_struct < 0 || !bytes) return arg_error("mp_structure_attention_ws: bad arguments");
+  const int64_t S = n > 0 && n_struct > 0 ? ops::splits_of(n, n_struct) : 1;
+  *bytes = S > 1 ? align_up(sizeof(float) * (size_t)(S * n * (channels + 2 * heads))) : 0;
+  return MP_OK;
+}
+
+extern "C" int mp_structure_attention(const mp_attention_args* a, void* out, int64_t ldo, float* saved, void* ws,
+                                      size_t ws_bytes, hipStream_t st) {
   ops::AttnArgs A;
   MP_TRY(ops::attn_args("mp_structure_attention", a, A));
   if (a->n == 0 || a->n_struct == 0) return MP_OK;
@@ -91,6 +131,15 @@ extern "C" int mp_structure_attention(const mp_attention_args* a, void* out, int
     A.o32 = a->feat_dtype == 1 ? saved : nullptr;
     A.lse = saved + ops::saved_o32(a->n, a->channels, a->feat_dtype);
   }
+  size_t need = 0;
+  MP_TRY(mp_structure_attention_ws(a->n, a->n_struct, a->channels, a->heads, &need));
+  if (need > 0) {
+    if (!ws || ((uintptr_t)ws & 15)) return arg_error("mp_structure_attention: workspace null or not 16-byte aligned");
+    if (ws_bytes < need) return arg_error("mp_structure_attention: workspace too small");
+    A.splits = ops::splits_of(a->n, a->n_struct);
+    A.p_out = (float*)ws;
+    A.p_ml = A.p_out + (int64_t)A.splits * a->n * a->channels;
+  }
   ProfScope p("structure_attention", st);
   return ops::launch(a, A, 0, st);
 }
@@ -100,8 +149,8 @@ extern "C" int mp_structure_attention_bwd_ws(int32_t n, int32_t n_struct, int32_
   MP_TRY(ops::check_shape("mp_structure_attention_bwd_ws", n, channels, heads, 0));
   if (n_struct < 0 || !bytes) return arg_error("mp_structure_attention_bwd_ws: bad arguments");
   Arena ar(nullptr, 0, true);
-  ar.take<float>((int64_t)n * heads);
-  ar.take<float>(((int64_t)n / 16 + n_struct) * heads);
+  ops::BwdWs w;
+  ops::carve_bwd(ar, n, n_struct, channels, heads, w);
   *bytes = ar.off;
   return MP_OK;
 }
@@ -128,20 +177,21 @@ extern "C" int mp_structure_attention_bwd(const mp_attention_args* a, const void
   MP_ROWS("mp_structure_attention_bwd", "dv", dv, lddv, C, dt);
   if ((uintptr_t)saved & 15) return arg_error("mp_structure_attention_bwd: saved must be 16-byte aligned");
   if (!ws || ((uintptr_t)ws & 15)) return arg_error("mp_structure_attention_bwd: workspace null or not 16-byte aligned");
-  const int64_t slots = (int64_t)a->n / 16 + a->n_struct;
   Arena ar(ws, ws_bytes);
-  A.dsum = ar.take<float>((int64_t)a->n * H);
-  float* part = ar.take<float>(slots * H);
+  ops::BwdWs w;
+  ops::carve_bwd(ar, a->n, a->n_struct, C, H, w);
+  A.dsum = w.dsum, A.splits = w.splits;
+  A.p_dq = w.dq, A.p_dk = w.dk, A.p_dv = w.dv, A.p_row = w.row, A.p_col = w.col;
   if (!ar.ok()) return arg_error("mp_structure_attention_bwd: workspace too small");
   A.o = out, A.ldo = ldo, A.dout = dout, A.lddo = lddo;
   A.dq = dq, A.lddq = lddq, A.dk = dk, A.lddk = lddk, A.dv = dv, A.lddv = lddv;
   A.o32 = const_cast<float*>(dt == 1 ? saved : nullptr);
   A.lse = const_cast<float*>(saved + ops::saved_o32(a->n, C, dt));
   A.dpos = dpos;
-  A.dslope_part = dslope ? part : nullptr;
+  A.dslope_part = dslope ? w.slope : nullptr;
   ProfScope p("structure_attention_bwd", st);
   MP_TRY(ops::launch(a, A, 1, st));
   MP_TRY(ops::launch(a, A, 2, st));
   const ops::Segment seg{0, H, dslope, false};
-  return ops::reduce_rows(part, slots, H, &seg, 1, st);
+  return ops::reduce_rows(w.slope, w.blocks, H, &seg, 1, st);
 }

@@ -9,7 +9,8 @@
 // are the next product's operand without leaving their lanes, and the distance of a pair is
 // formed once and used by every head (all C channels are in the wave).  The waves of a block
 // own the same 16 atoms and take every KW-th step of the other side; their sums are joined
-// in LDS in wave order, so equal inputs give equal bits.
+// in LDS in wave order, so equal inputs give equal bits.  Few long structures split the other side
+// over gridDim.y blocks as well; those leave float32 partial sums, which a last kernel joins.
 //
 // A wave never straddles structures: tile slots are numbered so that structure b owns slots
 // s_b / 16 + b .. (floor), which needs no pass over the sizes; the structure of a slot is found
@@ -22,6 +23,8 @@
 // rate, beside ~10 plain operations), not MFMA: at 32 channels per head a score costs 128
 // matrix operations, 1/8 of its VALU time.
 #pragma once
+#include <algorithm>
+
 #include "ops.hpp"
 
 namespace mdmp {
@@ -41,7 +44,11 @@ struct AttnArgs {
   float cap;        // 0: none
   void *out, *dq, *dk, *dv;
   float *lse, *o32;    // saved: [n][H] base-2 log-sum, [n][C] unrounded output (bf16 only)
-  float *dpos, *dslope_part, *dsum;  // [n][3]; [slots][H]; [n][H] sum_c dout out
+  float *dpos, *dslope_part, *dsum;  // [n][3]; [splits][slots][H]; [n][H] sum_c dout out
+  // splits of the other side (gridDim.y) and, above 1, their partial sums: rows [splits][n][C] of
+  // out, dq, dk, dv; (m, l) [splits][n][H][2]; position gradients [splits][n][3] of either pass
+  int splits;
+  float *p_out, *p_ml, *p_dq, *p_dk, *p_dv, *p_row, *p_col;
 };
 
 // Coordinates as 32-bit words.  Periodic: fixed point in units of box_L / 2^32, so the
@@ -281,18 +288,19 @@ void k_attn_fwd(AttnArgs A) {
   WaveTile<T, C, RS> tv;
   typename M::F kf[NT][NC];
   P3 kp{0u, 0u, 0u};
-  uint64_t on = live<CK>(A, s + CK * wave, e, lane, true);
+  const int first = blockIdx.y * KW + wave;
+  uint64_t on = live<CK>(A, s + CK * first, e, lane, true);
   auto fetch_v = [&](int k0, uint64_t b) {
     tv.fetch((const T*)A.v, A.ldv, k0, e - k0, lane);
     if (dist && lane < CK) kp = load_pos(A, k0 + lane, (b >> lane) & 1);
   };
-  if (s + CK * wave < e) {
-    fetch_v(s + CK * wave, on);
-    load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, s + CK * wave, e - s - CK * wave, i, g);
+  if (s + CK * first < e) {
+    fetch_v(s + CK * first, on);
+    load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, s + CK * first, e - s - CK * first, i, g);
   }
 
-  for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
-    const int kn = k0 + CK * KW;
+  for (int k0 = s + CK * first; k0 < e; k0 += CK * KW * A.splits) {
+    const int kn = k0 + CK * KW * A.splits;
     const bool part = on != all_live<CK>();
     const uint64_t on_n = live<CK>(A, kn, e, lane, true);
     if (part) tv.clear(on, lane);
@@ -442,6 +450,17 @@ void k_attn_fwd(AttnArgs A) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[t] += f * *(const f4*)((const float*)s_w[w] + ri * OS + c + 4 * t);
       }
+      const int64_t row = row0 + ri;
+      if (A.splits > 1) {
+        float* po = A.p_out + ((int64_t)blockIdx.y * A.n + row) * C + c;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *(f4*)(po + 4 * t) = o[t];
+        if (c % DH == 0) {
+          float* pm = A.p_ml + (((int64_t)blockIdx.y * A.n + row) * H + h) * 2;
+          pm[0] = mm, pm[1] = ll;
+        }
+        continue;
+      }
       const bool any = ll > 0.f || ll != ll;
       const float inv = any ? 1.0f / ll : 0.f;
 #pragma unroll
@@ -500,9 +519,10 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
   __shared__ float s_p[KW][3][16];
   __shared__ float s_s[KW][H];
   const int lane = threadIdx.x & 63, wave = KW > 1 ? uniform(threadIdx.x >> 6) : 0, i = lane & 15, g = lane >> 4;
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   int row0, s, e;
   if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) {
-    if (A.dslope_part && threadIdx.x < H) A.dslope_part[(int64_t)blockIdx.x * H + threadIdx.x] = 0.f;
+    if (A.dslope_part && threadIdx.x < H) A.dslope_part[block * H + threadIdx.x] = 0.f;
     return;
   }
   const int row = row0 + i;
@@ -537,7 +557,7 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     dsum[h] = gsum(dsum[h]);
-    if (wave == 0 && g == 0 && row < e) A.dsum[(int64_t)row * H + h] = dsum[h];
+    if (blockIdx.y == 0 && wave == 0 && g == 0 && row < e) A.dsum[(int64_t)row * H + h] = dsum[h];
   }
   f4 acc[C / 16];
 #pragma unroll
@@ -546,8 +566,9 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
   T* ks = (T*)s_w[wave];
   u4* ps = (u4*)(s_w[wave] + CK * RS * sizeof(T));
   const Score Z = score_of<T>(A);
+  const int first = blockIdx.y * KW + wave;
 
-  for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
+  for (int k0 = s + CK * first; k0 < e; k0 += CK * KW * A.splits) {
     const uint64_t on = live<CK>(A, k0, e, lane, true);
     WaveTile<T, C, RS> tk;
     tk.fetch((const T*)A.k, A.ldk, k0, e - k0, lane);
@@ -632,14 +653,19 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < KW; ++w) v += s_s[w][threadIdx.x];
-    A.dslope_part[(int64_t)blockIdx.x * H + threadIdx.x] = v * A.unit;
+    A.dslope_part[block * H + threadIdx.x] = v * A.unit;
   }
   if (A.dpos && threadIdx.x < 48) {
     const int ri = threadIdx.x / 3, a = threadIdx.x % 3;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < KW; ++w) v += s_p[w][a][ri];
-    if (row0 + ri < e) A.dpos[3 * (int64_t)row0 + threadIdx.x] = v;
+    if (row0 + ri < e) {
+      if (A.splits > 1)
+        A.p_row[3 * ((int64_t)blockIdx.y * A.n + row0) + threadIdx.x] = v;
+      else
+        A.dpos[3 * (int64_t)row0 + threadIdx.x] = v;
+    }
   }
   if constexpr (KW == 1) {
     if (row >= e) return;
@@ -657,7 +683,13 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
         for (int w = 0; w < KW; ++w) o[t] += *(const f4*)((const float*)s_w[w] + ri * OS + c + 4 * t);
         o[t] *= A.scale;
       }
-      st_row<T>((T*)A.dq + (int64_t)(row0 + ri) * A.lddq + c, o);
+      if (A.splits > 1) {
+        float* po = A.p_dq + ((int64_t)blockIdx.y * A.n + row0 + ri) * C + c;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *(f4*)(po + 4 * t) = o[t];
+      } else {
+        st_row<T>((T*)A.dq + (int64_t)(row0 + ri) * A.lddq + c, o);
+      }
     }
   }
 }
@@ -697,9 +729,10 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
   u4* ps = (u4*)(s_w[wave] + 2 * TB);
   float *ls = (float*)(s_w[wave] + 2 * TB + CK * 16), *ss = ls + H * CK;
   const Score Z = score_of<T>(A);
+  const int first = blockIdx.y * KW + wave;
 
   if (own_on != 0) {
-    for (int k0 = s + CK * wave; k0 < e; k0 += CK * KW) {
+    for (int k0 = s + CK * first; k0 < e; k0 += CK * KW * A.splits) {
       const uint64_t on = live<CK>(A, k0, e, lane, false);
       WaveTile<T, C, RS> tq, to;
       tq.fetch((const T*)A.q, A.ldq, k0, e - k0, lane);
@@ -797,7 +830,12 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < KW; ++w) v += s_p[w][a][ri];
-    if (row0 + ri < e) A.dpos[3 * (int64_t)row0 + threadIdx.x] += v;
+    if (row0 + ri < e) {
+      if (A.splits > 1)
+        A.p_col[3 * ((int64_t)blockIdx.y * A.n + row0) + threadIdx.x] = v;
+      else
+        A.dpos[3 * (int64_t)row0 + threadIdx.x] += v;
+    }
   }
   if constexpr (KW == 1) {
     if (row >= e) return;
@@ -821,10 +859,99 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
         }
         o[t] *= A.scale;
       }
-      st_row<T>((T*)A.dk + (int64_t)(row0 + ri) * A.lddk + c, o);
-      st_row<T>((T*)A.dv + (int64_t)(row0 + ri) * A.lddv + c, u);
+      if (A.splits > 1) {
+        const int64_t at = ((int64_t)blockIdx.y * A.n + row0 + ri) * C + c;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          *(f4*)(A.p_dk + at + 4 * t) = o[t];
+          *(f4*)(A.p_dv + at + 4 * t) = u[t];
+        }
+      } else {
+        st_row<T>((T*)A.dk + (int64_t)(row0 + ri) * A.lddk + c, o);
+        st_row<T>((T*)A.dv + (int64_t)(row0 + ri) * A.lddv + c, u);
+      }
     }
   }
+}
+
+// ------------------------------------------------------------------------------ joins of splits
+// rows of the structures: at or past struct_ptr[n_struct] nothing is written
+__device__ __forceinline__ int rows_end(const AttnArgs& A) { return min(max(A.sptr[A.n_struct], 0), A.n); }
+
+// out, saved log-sums: the splits' sums in one reference, in split order; EV channels a thread
+template <class T>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs A, int C, int H) {
+  using M = MF<T>;
+  constexpr int EV = M::EV, NT = M::NT;
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, row = x / (C / EV);
+  if (row >= rows_end(A)) return;
+  const int c = (int)(x % (C / EV)) * EV, h = c / (C / H);
+  float mm = -INFINITY, ll = 0.f;
+  for (int s = 0; s < A.splits; ++s) mm = fmaxf(mm, A.p_ml[((s * (int64_t)A.n + row) * H + h) * 2]);
+  f4 o[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < A.splits; ++s) {
+    const int64_t at = s * (int64_t)A.n + row;
+    const float ms = A.p_ml[(at * H + h) * 2];
+    const float f = mm == -INFINITY ? 1.0f : (ms == -INFINITY ? 0.f : ex2(ms - mm));
+    ll = fmaf(f, A.p_ml[(at * H + h) * 2 + 1], ll);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t] += f * *(const f4*)(A.p_out + at * C + c + 4 * t);
+  }
+  const bool any = ll > 0.f || ll != ll;
+  const float inv = any ? 1.0f / ll : 0.f;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    o[t] *= inv;
+    if (A.o32) st4(A.o32 + row * C + c + 4 * t, o[t]);
+  }
+  st_row<T>((T*)A.out + row * A.ldo + c, o);
+  if (A.lse && c % (C / H) == 0) A.lse[row * H + h] = any ? mm + log2f(ll) : INFINITY;
+}
+
+// dq, dk, dv (blockIdx.y 0, 1, 2) and dpos (3): sums over the splits, in split order
+template <class T>
+__global__ __launch_bounds__(256) void k_attn_join_bwd(AttnArgs A, int C) {
+  using M = MF<T>;
+  constexpr int EV = M::EV, NT = M::NT;
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int which = blockIdx.y, end = rows_end(A);
+  if (which == 3) {
+    if (x >= 3 * (int64_t)end) return;
+    float v = 0.f;
+    for (int s = 0; s < A.splits; ++s) v += A.p_row[3 * s * (int64_t)A.n + x];
+    for (int s = 0; s < A.splits; ++s) v += A.p_col[3 * s * (int64_t)A.n + x];
+    A.dpos[x] = v;
+    return;
+  }
+  const int64_t row = x / (C / EV);
+  if (row >= end) return;
+  const int c = (int)(x % (C / EV)) * EV;
+  const float* p = which == 0 ? A.p_dq : which == 1 ? A.p_dk : A.p_dv;
+  f4 o[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < A.splits; ++s)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t] += *(const f4*)(p + (s * (int64_t)A.n + row) * C + c + 4 * t);
+  if (which == 0)
+    st_row<T>((T*)A.dq + row * A.lddq + c, o);
+  else if (which == 1)
+    st_row<T>((T*)A.dk + row * A.lddk + c, o);
+  else
+    st_row<T>((T*)A.dv + row * A.lddv + c, o);
+}
+
+template <class T>
+int launch_join(const AttnArgs& A, int C, int H, bool bwd, hipStream_t st) {
+  const unsigned blocks = (unsigned)cdiv((int64_t)A.n * (C / MF<T>::EV), 256);
+  if (bwd)  // 3 n position gradients are at most as many as the pieces of one matrix times 3
+    k_attn_join_bwd<T><<<dim3((unsigned)std::max<int64_t>(blocks, cdiv(3 * (int64_t)A.n, 256)), A.dpos ? 4 : 3), 256, 0, st>>>(A, C);
+  else
+    k_attn_join<T><<<blocks, 256, 0, st>>>(A, C, H);
+  MP_CHECK_LAUNCH();
+  return MP_OK;
 }
 
 // what: 0 forward, 1 row pass, 2 column pass
@@ -833,7 +960,7 @@ int launch_attn_f32(const AttnArgs& A, int C, int dh, bool split, int what, hipS
 
 template <class T, int C, int DH>
 int launch_attn_c(const AttnArgs& A, bool split, int what, hipStream_t st) {
-  const unsigned blocks = (unsigned)(A.n / 16 + A.n_struct);
+  const dim3 blocks((unsigned)(A.n / 16 + A.n_struct), (unsigned)A.splits);
   constexpr int KW = 4;
   constexpr bool SAVES = sizeof(T) == 2;  // float32 has no second form
   auto go = [&](void (*save)(AttnArgs), void (*plain)(AttnArgs), int threads) {
@@ -859,6 +986,7 @@ int launch_attn_c(const AttnArgs& A, bool split, int what, hipStream_t st) {
         k_attn_col<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
   }
   MP_CHECK_LAUNCH();
+  if (A.splits > 1 && what != 1) return launch_join<T>(A, C, C / DH, what == 2, st);
   return MP_OK;
 }
 

@@ -39,7 +39,8 @@ EXPORTS = ["mp_version", "mp_last_error", "mp_model_num_weights", "mp_model_crea
            "mp_md_get_state", "mp_md_destroy",
            "mp_linear", "mp_linear_bwd_ws", "mp_linear_bwd", "mp_gated_ffn", "mp_gated_ffn_bwd_ws",
            "mp_gated_ffn_bwd", "mp_norm_block", "mp_norm_block_bwd_ws", "mp_norm_block_bwd",
-           "mp_structure_attention_saved", "mp_structure_attention", "mp_structure_attention_bwd_ws",
+           "mp_structure_attention_saved", "mp_structure_attention_ws", "mp_structure_attention",
+           "mp_structure_attention_bwd_ws",
            "mp_structure_attention_bwd", "mp_mixer_num_weights", "mp_mixer_create", "mp_mixer_destroy",
            "mp_energy_forces_mixer_ws", "mp_energy_forces_mixer",
            "mp_profile_enable",
@@ -131,7 +132,8 @@ _sig = {
     "mp_norm_block_bwd": ([_P(mp_norm_args), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                            _vp, _sz, _vp], ctypes.c_int),
     "mp_structure_attention_saved": ([_i32, _i32, _i32, _i32, _P(_i64)], ctypes.c_int),
-    "mp_structure_attention": ([_P(mp_attention_args), _vp, _i64, _vp, _vp], ctypes.c_int),
+    "mp_structure_attention_ws": ([_i32, _i32, _i32, _i32, _P(_sz)], ctypes.c_int),
+    "mp_structure_attention": ([_P(mp_attention_args), _vp, _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
     "mp_structure_attention_bwd_ws": ([_i32, _i32, _i32, _i32, _P(_sz)], ctypes.c_int),
     "mp_structure_attention_bwd": ([_P(mp_attention_args), _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                     _i64, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
@@ -639,7 +641,10 @@ def structure_attention(q, k, v, struct_ptr, heads, pos=None, slope=None, L=0.0,
         _check(_lib.mp_structure_attention_saved(n, c, heads, a.feat_dtype, ctypes.byref(m)),
                "mp_structure_attention_saved")
         saved = torch.empty(m.value, dtype=torch.float32, device=q.device)
-    _check(_lib.mp_structure_attention(ctypes.byref(a), op, ldo, _ptr(saved), _stream()), "mp_structure_attention")
+    need = _wsbytes(_lib.mp_structure_attention_ws, "mp_structure_attention_ws", n, a.n_struct, c, heads)
+    ws = _ws(need) if need else None
+    _check(_lib.mp_structure_attention(ctypes.byref(a), op, ldo, _ptr(saved), _ptr(ws), need, _stream()),
+           "mp_structure_attention")
     return (out, saved) if save else out
 
 

@@ -124,8 +124,8 @@ def attn_args(n=40, ns=2, c=64, h=2, dt=0, cap=0.0, box=0.0, sp=P, pos=None, slo
 
 
 def test_structure_attention_refusals():
-    def attn(out=P, ldo=64, saved=None, **kw):
-        return L.mp_structure_attention(attn_args(**kw), out, ldo, saved, None)
+    def attn(out=P, ldo=64, saved=None, ws=None, nb=0, **kw):
+        return L.mp_structure_attention(attn_args(**kw), out, ldo, saved, ws, nb, None)
     for h in (0, -1, 3, 8, 64):   # 64 channels: 16, 32 or 64 per head
         refused(attn(h=h), "channels / heads")
     refused(attn(c=128, h=1), "channels / heads")
@@ -146,6 +146,13 @@ def test_structure_attention_refusals():
     refused(attn(out=None), "null out")
     refused(attn(ldo=63), "rows of out")
     refused(attn(saved=ODD), "saved")
+    n = ctypes.c_size_t(0)   # few long structures need a workspace, many short ones none
+    assert L.mp_structure_attention_ws(40, 2, 64, 2, ctypes.byref(n)) == mdmp.MP_OK and n.value == 0
+    assert L.mp_structure_attention_ws(5000, 1, 64, 2, ctypes.byref(n)) == mdmp.MP_OK and n.value > 5000 * 64 * 4
+    refused(attn(n=5000, ns=1), "workspace")
+    refused(attn(n=5000, ns=1, ws=P, nb=n.value - 1), "workspace too small")
+    refused(attn(n=5000, ns=1, ws=ODD, nb=n.value), "workspace")
+    refused(attn(ldq=(1 << 24) + 64), "2^24")
     assert attn(n=0, q=None, sp=None) == mdmp.MP_OK and attn(ns=0, q=None, sp=None) == mdmp.MP_OK
     n = ctypes.c_size_t(0)
     assert L.mp_structure_attention_bwd_ws(40, 2, 64, 2, ctypes.byref(n)) == mdmp.MP_OK

@@ -207,6 +207,11 @@ ATTN = [
     ([100, 0, 99], 64, 1, "f32", True, 0.0, 0.05, 0.0, 0),
     ([70], 32, 1, "f32", True, 30.0, None, 0.0, 0),
     ([131], 128, 2, "f32", True, 0.0, None, 12.0, 0),
+    # long enough for the other side to be split over blocks; one structure without it among them
+    ([1100, 7, 0, 1301], 32, 2, "bf16", True, 8.0, 0.7, 0.0, 0),
+    ([1500], 64, 2, "f32", True, 0.0, 0.9, 25.0, 8),
+    ([1600], 128, 4, "bf16", True, 0.0, None, 26.0, 0),
+    ([1030, 1029], 16, 1, "f32", False, 5.0, None, 0.0, 0),
 ]
 
 
