@@ -9,21 +9,21 @@ namespace mdmp {
 namespace ops {
 namespace {
 
-// Structures of up to this many atoms on average: one wave per 16 atoms walks its structure
-// alone.  Longer ones: four waves share the 16 atoms and split the other side, which fills
-// the chip with a quarter of the atoms and quarters each wave's walk.
-constexpr int kSplitAbove = 64;
+// Structures of up to this many atoms on average: a block is one wave, 16 atoms of a structure.
+// Longer ones: blocks of four waves own 64 atoms and share their way along the other side.
+constexpr int kLongAbove = 64;
+bool long_ones(int64_t n, int64_t n_struct) { return n > kLongAbove * n_struct; }
 
-bool split_waves(int64_t n, int64_t n_struct) { return n > kSplitAbove * n_struct; }
+// Slots of rows in the grid
+int64_t slots_of(int64_t n, int64_t n_struct) { return n / (long_ones(n, n_struct) ? 64 : 16) + n_struct; }
 
-// Splits of the other side over blocks, for few long structures: towards 4,096 blocks (the chip
-// holds 512 at a time, and a last round that is not full should be a small part of the whole),
-// each with at least 512 atoms of the other side for its four waves, at most 8 (each costs a
-// float32 partial of the rows, written and read once).
+// Splits of the other side over blocks, for few long structures: towards 2,048 blocks (the chip
+// holds 768 at a time, and a last round that is not full should be a small part of the whole),
+// each with at least 128 atoms of the other side, at most 16 (each costs a float32 partial of the
+// rows, written and read once).
 int splits_of(int64_t n, int64_t n_struct) {
-  if (!split_waves(n, n_struct)) return 1;
-  const int64_t blocks = n / 16 + n_struct, mean = n / n_struct;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(4096, blocks), mean / 512, 8}));
+  if (!long_ones(n, n_struct)) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(2048, slots_of(n, n_struct)), n / n_struct / 128, 16}));
 }
 
 // the kernels address the rows of one step by 32-bit offsets from a 64-bit base
@@ -70,7 +70,7 @@ int attn_args(const char* who, const mp_attention_args* a, AttnArgs& A) {
 }
 
 int launch(const mp_attention_args* a, const AttnArgs& A, int what, hipStream_t st) {
-  const bool split = split_waves(a->n, a->n_struct);
+  const bool split = long_ones(a->n, a->n_struct);
   const int dh = a->channels / a->heads;
   return a->feat_dtype == 1 ? launch_attn_bf16(A, a->channels, dh, split, what, st)
                             : launch_attn_f32(A, a->channels, dh, split, what, st);
@@ -84,7 +84,7 @@ struct BwdWs {
 };
 void carve_bwd(Arena& ar, int64_t n, int64_t n_struct, int C, int H, BwdWs& w) {
   w.splits = n > 0 && n_struct > 0 ? splits_of(n, n_struct) : 1;
-  w.blocks = w.splits * (n / 16 + n_struct);
+  w.blocks = n_struct > 0 ? w.splits * slots_of(n, n_struct) : 0;
   w.dsum = ar.take<float>(n * H);
   w.slope = ar.take<float>(w.blocks * H);
   w.dq = w.dk = w.dv = w.row = w.col = nullptr;

@@ -7,14 +7,16 @@
 // at a time.  Scores are formed transposed, S[other][own] = K Q^T, so a lane holds scores of
 // ONE own atom against 4 (x NT) others, in tile order: softmax weights and score gradients
 // are the next product's operand without leaving their lanes, and the distance of a pair is
-// formed once and used by every head (all C channels are in the wave).  The waves of a block
-// own the same 16 atoms and take every KW-th step of the other side; their sums are joined
-// in LDS in wave order, so equal inputs give equal bits.  Few long structures split the other side
-// over gridDim.y blocks as well; those leave float32 partial sums, which a last kernel joins.
+// formed once and used by every head (all C channels are in the wave).
+//   NW = 1  short structures: a block is one wave, which stages what it needs for itself
+//   NW = 4  long structures: the four waves of a block own 64 adjacent atoms of one structure and
+//           share each step of the other side in LDS (two buffers, one barrier a step); few long
+//           structures also split the other side over gridDim.y blocks, which leave float32
+//           partial sums that a last kernel joins in order, so equal inputs give equal bits.
 //
-// A wave never straddles structures: tile slots are numbered so that structure b owns slots
-// s_b / 16 + b .. (floor), which needs no pass over the sizes; the structure of a slot is found
-// by a 64-way search.  At most one slot per structure stays empty.
+// A wave never straddles structures: slots of R = 16 NW atoms are numbered so that structure b
+// owns slots s_b / R + b .. (floor), which needs no pass over the sizes; the structure of a slot
+// is found by a 64-way search.  At most one slot per structure stays empty.
 //
 // Masked atoms and rows past the structure are staged as zeros and their scores set to -inf,
 // so nothing they hold (NaN, infinities) reaches another atom.
@@ -126,19 +128,22 @@ constexpr uint64_t all_live() {
   return (1ull << CK) - 1;
 }
 
-// CK rows of a matrix from row k0 on: a wave's copy in LDS (one tile, rows of RS), or MFMA
-// operands in natural order, frag[t][ch] = row 16 t + i.  Row k0 is the same for the wave, so an
-// address is a scalar base and a 32-bit lane offset (rows are at most 2^24 elements long).
-// Rows past the structure (rows < CK of them left) are read as its last row, and cleared where
-// their contents matter by the caller.
-template <class T, int C, int RS>
-struct WaveTile {
-  static constexpr int CK = MF<T>::CK, EV = MF<T>::EV, VPR = C / EV, IT = CK * VPR / 64, RJ = 64 / VPR;
-  static_assert(CK * VPR % 64 == 0 && 64 % VPR == 0, "whole waves");
+// CK rows of a matrix from row k0 on: a copy in LDS by NTH threads (rows of RS), or MFMA operands in
+// natural order, frag[t][ch] = row 16 t + i.  Row k0 is the same for the wave, so an address is a
+// scalar base and a 32-bit lane offset (rows are at most 2^24 elements long).  Rows past the
+// structure (rows < CK of them left) are read as its last row, and cleared where their contents
+// matter by the caller.
+template <class T, int C, int RS, int NTH>
+struct StepTile {
+  static constexpr int CK = MF<T>::CK, EV = MF<T>::EV, VPR = C / EV, TOT = CK * VPR, IT = (TOT + NTH - 1) / NTH;
+  static constexpr int RJ = NTH / VPR;
+  static_assert(NTH % VPR == 0 && (TOT % NTH == 0 || TOT < NTH), "whole rows");
   u4 v[IT];
-  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int64_t k0, int rows, int lane) {
+  static __device__ __forceinline__ bool in(int tid) { return TOT >= NTH || tid < TOT; }
+  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int64_t k0, int rows, int tid) {
     const T* p = src + k0 * ld;
-    const uint32_t r = lane / VPR, c = (lane % VPR) * EV;
+    const uint32_t r = tid / VPR, c = (tid % VPR) * EV;
+    if (!in(tid)) return;
     if (rows >= CK) {
       const uint32_t off = r * (uint32_t)ld + c;
 #pragma unroll
@@ -149,17 +154,26 @@ struct WaveTile {
     }
   }
   // rows without their bit become zeros
-  __device__ __forceinline__ void clear(uint64_t on, int lane) {
-    const uint32_t m = (uint32_t)on >> (lane / VPR);
+  __device__ __forceinline__ void clear(uint64_t on, int tid) {
+    const uint32_t m = (uint32_t)on >> (tid / VPR % 32);
 #pragma unroll
     for (int j = 0; j < IT; ++j)
-      if (!((m >> (j * RJ)) & 1)) v[j] = u4{0u, 0u, 0u, 0u};
+      if (!((m >> (j * RJ % 32)) & 1)) v[j] = u4{0u, 0u, 0u, 0u};
   }
-  __device__ __forceinline__ void put(T* dst, int lane) const {
+  __device__ __forceinline__ void put(T* dst, int tid) const {
+    if (!in(tid)) return;
 #pragma unroll
-    for (int j = 0; j < IT; ++j) *(u4*)(dst + (lane / VPR + j * RJ) * RS + (lane % VPR) * EV) = v[j];
+    for (int j = 0; j < IT; ++j) *(u4*)(dst + (tid / VPR + j * RJ) * RS + (tid % VPR) * EV) = v[j];
   }
 };
+// all waves of a block, or one wave, have written or read their LDS
+template <int NW>
+__device__ __forceinline__ void step_sync() {
+  if constexpr (NW == 1)
+    wave_sync();
+  else
+    lds_barrier();
+}
 // chunks c0 .. c1 - 1 of the operands of NTL tiles
 template <class T, int C, int NTL>
 __device__ __forceinline__ void load_frags(typename MF<T>::F (&f)[NTL][C / MF<T>::CK], const T* src, int64_t ld,
@@ -207,18 +221,17 @@ __device__ __forceinline__ bool lane_in_head(int ch, int g, int h) {
 
 template <class T, int C>
 struct AttnDims {
-  static constexpr int CK = MF<T>::CK, RS = C + lds_pad<T>(), OS = C + 4;
+  static constexpr int RS = C + lds_pad<T>();
 };
 
-// one head's channel chunk range: chunk ch belongs to the operands of head h alone (heads of a
-// chunk or more), or is the last to be read by head h
+// the channel chunks of head h: chunk_of(h) .. + chunks() - 1 (heads of half a chunk: the one it is in)
 template <class T, int DH>
-constexpr int chunk_first(int h) {
-  return DH >= MF<T>::CK ? h * (DH / MF<T>::CK) : h / 2;
+constexpr int chunks() {
+  return DH >= MF<T>::CK ? DH / MF<T>::CK : 1;
 }
 template <class T, int DH>
-constexpr int chunk_end(int h) {
-  return DH >= MF<T>::CK ? (h + 1) * (DH / MF<T>::CK) : (h + 1) / 2;
+constexpr int chunk_of(int h) {
+  return DH >= MF<T>::CK ? h * (DH / MF<T>::CK) : h / 2;
 }
 
 // Scores in the reference of a lane's query: x = log2(e) s + b.  bf16 features: tanh(y) =
@@ -245,25 +258,41 @@ __device__ __forceinline__ float score(const Score& Z, float s, float b) {
   return Z.cap ? fmaf(Z.k, cap_of<T>(s, Z.sc), b) : fmaf(s, Z.sc, b);
 }
 
+// The distances of a step's pairs
+template <int NT>
+__device__ __forceinline__ void distances(f4 (&r)[NT], const P3& own, const u4* ps, bool fix, int g) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float dx, dy, dz;
+      diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
+      r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+    }
+}
+// waves per SIMD that the register budgets aim at, per kernel
+#define ATTN_FWD_WAVES (C == 128 ? (NW == 1 ? 2 : 3) : 3)
+#define ATTN_BWD_WAVES (C == 128 ? 2 : 3)
+
 // ------------------------------------------------------------------------------ forward
-template <class T, int C, int DH, int KW, bool SAVE>
-__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 128 ? 2 : 3)))
+template <class T, int C, int DH, int NW, bool SAVE>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_FWD_WAVES)))
 void k_attn_fwd(AttnArgs A) {
   using M = MF<T>;
   using D = AttnDims<T, C>;
-  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
-  constexpr int TILE = CK * RS * sizeof(T) + CK * 16, SLAB = 16 * OS * 4;
-  constexpr int WB = KW > 1 && SLAB > TILE ? SLAB : TILE;
-  constexpr bool BF = sizeof(T) == 2;
-  __shared__ __align__(16) char s_w[KW][WB];
-  __shared__ float s_m[KW > 1 ? KW : 1][2][H][16];
-  const int lane = threadIdx.x & 63, wave = KW > 1 ? uniform(threadIdx.x >> 6) : 0, i = lane & 15, g = lane >> 4;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, EV = M::EV, NTH = 64 * NW;
+  constexpr bool BF = sizeof(T) == 2, KL = NW > 1;  // KL: keys through LDS as well
+  constexpr int NB = KL ? 2 : 1;
+  __shared__ __align__(16) T s_v[NB][CK * RS];
+  __shared__ __align__(16) T s_k[KL ? NB : 1][KL ? CK * RS : 8];
+  __shared__ u4 s_pos[NB][CK];
+  const int tid = threadIdx.x, lane = tid & 63, wave = NW > 1 ? uniform(tid >> 6) : 0, i = lane & 15, g = lane >> 4;
   int row0, s, e;
-  if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
-  const int row = row0 + i;
+  if (!find_slot<16 * NW>(A, blockIdx.x, lane, row0, s, e)) return;
+  const int own0 = row0 + 16 * wave, row = own0 + i;
   const bool fix = A.to_fix > 0, dist = A.pos != nullptr;
   typename M::F qf[1][NC];
-  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
+  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, min(own0, e - 1), max(e - own0, 1), i, g);
   const P3 own = load_pos(A, row, row < e);
   // thr: a score above it (in the reference m) raises the reference; -inf until there is one
   float m[H], thr[H];
@@ -277,37 +306,50 @@ void k_attn_fwd(AttnArgs A) {
   f4 acc[C / 16];
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
-  T* vs = (T*)s_w[wave];
-  u4* ps = (u4*)(s_w[wave] + CK * RS * sizeof(T));
   const Score Z = score_of<T>(A);
   typename M::F ones;
   if constexpr (BF) ones = __builtin_bit_cast(typename M::F, u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
 
-  // A step's loads are issued during the step before: values and coordinates at its start, each
-  // head's keys as soon as its scores have read the ones they replace
-  WaveTile<T, C, RS> tv;
+  // A step's loads are issued during the step before; without LDS for the keys, each head's keys
+  // as soon as its scores have read the ones they replace
+  StepTile<T, C, RS, NTH> tv, tk;
   typename M::F kf[NT][NC];
   P3 kp{0u, 0u, 0u};
-  const int first = blockIdx.y * KW + wave;
-  uint64_t on = live<CK>(A, s + CK * first, e, lane, true);
-  auto fetch_v = [&](int k0, uint64_t b) {
-    tv.fetch((const T*)A.v, A.ldv, k0, e - k0, lane);
-    if (dist && lane < CK) kp = load_pos(A, k0 + lane, (b >> lane) & 1);
+  const int first = s + CK * (int)blockIdx.y, stride = CK * A.splits;
+  uint64_t on = live<CK>(A, first, e, lane, true);
+  auto fetch = [&](int k0, uint64_t b) {
+    tv.fetch((const T*)A.v, A.ldv, k0, e - k0, tid);
+    if constexpr (KL) tk.fetch((const T*)A.k, A.ldk, k0, e - k0, tid);
+    if (dist && tid < CK) kp = load_pos(A, k0 + tid, (b >> tid) & 1);
   };
-  if (s + CK * first < e) {
-    fetch_v(s + CK * first, on);
-    load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, s + CK * first, e - s - CK * first, i, g);
+  auto put = [&](int b, uint64_t live_bits) {
+    if (live_bits != all_live<CK>()) tv.clear(live_bits, tid);
+    tv.put(s_v[b], tid);
+    if constexpr (KL) tk.put(s_k[b], tid);
+    if (dist && tid < CK) s_pos[b][tid] = u4{kp.x, kp.y, kp.z, 0u};
+  };
+  if (first < e) {
+    fetch(first, on);
+    if constexpr (KL) {
+      put(0, on);
+      lds_barrier();
+    } else {
+      load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, first, e - first, i, g);
+    }
   }
-
-  for (int k0 = s + CK * first; k0 < e; k0 += CK * KW * A.splits) {
-    const int kn = k0 + CK * KW * A.splits;
+  int b = 0;
+  for (int k0 = first; k0 < e; k0 += stride) {
+    const int kn = k0 + stride;
     const bool part = on != all_live<CK>();
     const uint64_t on_n = live<CK>(A, kn, e, lane, true);
-    if (part) tv.clear(on, lane);
-    tv.put(vs, lane);
-    if (dist && lane < CK) ps[lane] = u4{kp.x, kp.y, kp.z, 0u};
-    wave_sync();
-    if (kn < e) fetch_v(kn, on_n);
+    if constexpr (!KL) {
+      put(0, on);
+      wave_sync();
+    }
+    if (kn < e) fetch(kn, on_n);
+    const T *vs = s_v[b], *ks = s_k[KL ? b : 0];
+    const u4* ps = s_pos[b];
+    if (own0 < e) {  // a wave past the structure only keeps step
     bool lv[NT][4];
     f4 r[NT];
 #pragma unroll
@@ -316,23 +358,24 @@ void k_attn_fwd(AttnArgs A) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) lv[t][q] = ((uint32_t)on >> (4 * g)) >> (16 * t + q) & 1;
     }
-    if (dist) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float dx, dy, dz;
-          diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
-          r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
-        }
-    }
+    if (dist) distances<NT>(r, own, ps, fix, g);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       f4 x[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
-      if (kn < e)
-        load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, kn, e - kn, i, g, chunk_first<T, DH>(h), chunk_end<T, DH>(h));
+      for (int t = 0; t < NT; ++t) {
+        if constexpr (KL) {
+#pragma unroll
+          for (int ch = chunk_of<T, DH>(h); ch < chunk_of<T, DH>(h) + chunks<T, DH>(); ++ch)
+            kf[t][ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
+        }
+        x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
+      }
+      if constexpr (!KL) {
+        if (kn < e && (DH >= CK || h % 2 == 1))
+          load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, kn, e - kn, i, g, chunk_of<T, DH>(h),
+                               chunk_of<T, DH>(h) + chunks<T, DH>());
+      }
       const float sl = dist ? A.slope[h] * (kLog2e * A.unit) : 0.f;
       if (Z.cap) {
 #pragma unroll
@@ -358,11 +401,11 @@ void k_attn_fwd(AttnArgs A) {
       for (int t = 0; t < NT; ++t) lm = fmaxf(lm, fmaxf(fmaxf(x[t].x, x[t].y), fmaxf(x[t].z, x[t].w)));
       if (__any(lm > thr[h])) {
         const float mt = gmax(lm);
-        const bool first = thr[h] == -INFINITY;
-        const float d = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f), al = ex2(-d);
+        const bool none = thr[h] == -INFINITY;
+        const float d = none ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f), al = ex2(-d);
         if (mt > -INFINITY) thr[h] = 8.0f;
         m[h] += d;
-        if (!first) {
+        if (!none) {
           l[h] *= al;
 #pragma unroll
           for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] *= al;
@@ -400,77 +443,46 @@ void k_attn_fwd(AttnArgs A) {
           acc[ct] = M::mma(acc[ct], ldt<RS>(vs, 0, 16 * ct, lane), p);
       }
     }
+    }
     on = on_n;
-    wave_sync();
+    if constexpr (KL) {
+      if (kn < e) put(b ^ 1, on_n);
+      lds_barrier();
+      b ^= 1;
+    } else {
+      wave_sync();
+    }
   }
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     if constexpr (!BF) l[h].x = gsum(l[h].x);
     if (thr[h] == -INFINITY) m[h] = -INFINITY;
   }
-
-  if constexpr (KW == 1) {
-    if (row >= e) return;
+  if (row >= e) return;
+  if (A.splits > 1) {
+    const int64_t at = (int64_t)blockIdx.y * A.n + row;
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const float inv = l[h].x > 0.f || l[h].x != l[h].x ? 1.0f / l[h].x : 0.f;
-#pragma unroll
-      for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
-        acc[ct] *= inv;
-        const int c = 16 * ct + 4 * g;
-        st4((T*)A.out + (int64_t)row * A.ldo + c, acc[ct]);
-        if (A.o32) st4(A.o32 + (int64_t)row * C + c, acc[ct]);
-      }
-      if (A.lse && g == 0) A.lse[(int64_t)row * H + h] = l[h].x > 0.f || l[h].x != l[h].x ? m[h] + log2f(l[h].x) : INFINITY;
-    }
-  } else {
-    float* slab = (float*)s_w[wave];
-#pragma unroll
-    for (int ct = 0; ct < C / 16; ++ct) *(f4*)(slab + i * OS + 16 * ct + 4 * g) = acc[ct];
+    for (int ct = 0; ct < C / 16; ++ct) *(f4*)(A.p_out + at * C + 16 * ct + 4 * g) = acc[ct];
 #pragma unroll
     for (int h = 0; h < H; ++h)
       if (g == 0) {
-        s_m[wave][0][h][i] = m[h];
-        s_m[wave][1][h][i] = l[h].x;
+        A.p_ml[(at * H + h) * 2] = m[h];
+        A.p_ml[(at * H + h) * 2 + 1] = l[h].x;
       }
-    __syncthreads();
-    for (int x = threadIdx.x; x < 16 * (C / EV); x += 64 * KW) {
-      const int ri = x / (C / EV), c = (x % (C / EV)) * EV, h = c / DH;
-      if (row0 + ri >= e) break;
-      float mm = -INFINITY, ll = 0.f;
+    return;
+  }
 #pragma unroll
-      for (int w = 0; w < KW; ++w) mm = fmaxf(mm, s_m[w][0][h][ri]);
-      f4 o[NT];
+  for (int h = 0; h < H; ++h) {
+    const bool any = l[h].x > 0.f || l[h].x != l[h].x;
+    const float inv = any ? 1.0f / l[h].x : 0.f;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const float mw = s_m[w][0][h][ri], f = mw == -INFINITY && mm != -INFINITY ? 0.f : (mm == -INFINITY ? 1.0f : ex2(mw - mm));
-        ll = fmaf(f, s_m[w][1][h][ri], ll);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) o[t] += f * *(const f4*)((const float*)s_w[w] + ri * OS + c + 4 * t);
-      }
-      const int64_t row = row0 + ri;
-      if (A.splits > 1) {
-        float* po = A.p_out + ((int64_t)blockIdx.y * A.n + row) * C + c;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) *(f4*)(po + 4 * t) = o[t];
-        if (c % DH == 0) {
-          float* pm = A.p_ml + (((int64_t)blockIdx.y * A.n + row) * H + h) * 2;
-          pm[0] = mm, pm[1] = ll;
-        }
-        continue;
-      }
-      const bool any = ll > 0.f || ll != ll;
-      const float inv = any ? 1.0f / ll : 0.f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        o[t] *= inv;
-        if (A.o32) st4(A.o32 + (int64_t)(row0 + ri) * C + c + 4 * t, o[t]);
-      }
-      st_row<T>((T*)A.out + (int64_t)(row0 + ri) * A.ldo + c, o);
-      if (A.lse && c % DH == 0) A.lse[(int64_t)(row0 + ri) * H + h] = any ? mm + log2f(ll) : INFINITY;
+    for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
+      acc[ct] *= inv;
+      const int c = 16 * ct + 4 * g;
+      st4((T*)A.out + (int64_t)row * A.ldo + c, acc[ct]);
+      if (A.o32) st4(A.o32 + (int64_t)row * C + c, acc[ct]);
     }
+    if (A.lse && g == 0) A.lse[(int64_t)row * H + h] = any ? m[h] + log2f(l[h].x) : INFINITY;
   }
 }
 
@@ -504,37 +516,52 @@ __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4
   }
 }
 
+// p += sum over the pairs of wgt (other - own) / r, nothing where r = 0
+template <int NT>
+__device__ __forceinline__ void add_pairs(float (&p)[3], const f4 (&wgt)[NT], const f4 (&r)[NT], const P3& own,
+                                          const u4* ps, bool fix, int g) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float dx, dy, dz;
+      diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
+      const float f = r[t][q] > 0.f ? wgt[t][q] * rcp(r[t][q]) : 0.f;
+      p[0] = fmaf(f, dx, p[0]), p[1] = fmaf(f, dy, p[1]), p[2] = fmaf(f, dz, p[2]);
+    }
+}
+
 // ------------------------------------------------------------------------------ row pass
 // For 16 queries: dsum_i = sum_c dout out (per head), dq_i = scale sum_j ds_ij k_j, the queries'
 // side of the position gradient, and the block's partial of dslope.  out enters unrounded (o32)
 // so that dsum, and with it the float32 gradients, do not carry bf16's rounding.
-template <class T, int C, int DH, int KW>
-__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 128 ? 2 : 3))) void k_attn_row(AttnArgs A) {
+template <class T, int C, int DH, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BWD_WAVES))) void k_attn_row(AttnArgs A) {
   using M = MF<T>;
   using D = AttnDims<T, C>;
-  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
-  constexpr int TILE = CK * RS * sizeof(T) + CK * 16, SLAB = 16 * OS * 4;
-  constexpr int WB = KW > 1 && SLAB > TILE ? SLAB : TILE;
-  __shared__ __align__(16) char s_w[KW][WB];
-  __shared__ float s_p[KW][3][16];
-  __shared__ float s_s[KW][H];
-  const int lane = threadIdx.x & 63, wave = KW > 1 ? uniform(threadIdx.x >> 6) : 0, i = lane & 15, g = lane >> 4;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, EV = M::EV, NTH = 64 * NW;
+  constexpr bool VL = NW > 1;  // values through LDS as well
+  constexpr int NB = VL ? 2 : 1;
+  __shared__ __align__(16) T s_k[NB][CK * RS];
+  __shared__ __align__(16) T s_v[VL ? NB : 1][VL ? CK * RS : 8];
+  __shared__ u4 s_pos[NB][CK];
+  __shared__ float s_s[NW][H];
+  const int tid = threadIdx.x, lane = tid & 63, wave = NW > 1 ? uniform(tid >> 6) : 0, i = lane & 15, g = lane >> 4;
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   int row0, s, e;
-  if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) {
-    if (A.dslope_part && threadIdx.x < H) A.dslope_part[block * H + threadIdx.x] = 0.f;
+  if (!find_slot<16 * NW>(A, blockIdx.x, lane, row0, s, e)) {
+    if (A.dslope_part && tid < H) A.dslope_part[block * H + tid] = 0.f;
     return;
   }
-  const int row = row0 + i;
-  const bool fix = A.to_fix > 0;
+  const int own0 = row0 + 16 * wave, row = own0 + i;
+  const bool fix = A.to_fix > 0, dist = A.pos != nullptr;
   typename M::F qf[1][NC], of[1][NC];
-  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, row0, e - row0, i, g);
-  load_frags<T, C, 1>(of, (const T*)A.dout, A.lddo, row0, e - row0, i, g);
+  load_frags<T, C, 1>(qf, (const T*)A.q, A.ldq, min(own0, e - 1), max(e - own0, 1), i, g);
+  load_frags<T, C, 1>(of, (const T*)A.dout, A.lddo, min(own0, e - 1), max(e - own0, 1), i, g);
   const P3 own = load_pos(A, row, row < e);
-  float slope[H], lse[H], dsum[H], dsl[H];
+  float lse[H], dsum[H], dsl[H];
 #pragma unroll
   for (int h = 0; h < H; ++h) {
-    slope[h] = A.slope ? A.slope[h] * (kLog2e * A.unit) : 0.f;
     lse[h] = row < e ? A.lse[(int64_t)row * H + h] : INFINITY;
     dsum[h] = dsl[h] = 0.f;
   }
@@ -557,58 +584,75 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     dsum[h] = gsum(dsum[h]);
-    if (blockIdx.y == 0 && wave == 0 && g == 0 && row < e) A.dsum[(int64_t)row * H + h] = dsum[h];
+    if (blockIdx.y == 0 && g == 0 && row < e) A.dsum[(int64_t)row * H + h] = dsum[h];
   }
   f4 acc[C / 16];
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
-  float px = 0.f, py = 0.f, pz = 0.f;
-  T* ks = (T*)s_w[wave];
-  u4* ps = (u4*)(s_w[wave] + CK * RS * sizeof(T));
+  float px[3] = {0.f, 0.f, 0.f};
   const Score Z = score_of<T>(A);
-  const int first = blockIdx.y * KW + wave;
 
-  for (int k0 = s + CK * first; k0 < e; k0 += CK * KW * A.splits) {
-    const uint64_t on = live<CK>(A, k0, e, lane, true);
-    WaveTile<T, C, RS> tk;
-    tk.fetch((const T*)A.k, A.ldk, k0, e - k0, lane);
-    typename M::F vf[NT][NC];
-    load_frags<T, C, NT>(vf, (const T*)A.v, A.ldv, k0, e - k0, i, g);
-    if (on != all_live<CK>()) tk.clear(on, lane);
-    if (A.pos && lane < CK) {
-      const P3 p = load_pos(A, k0 + lane, (on >> lane) & 1);
-      ps[lane] = u4{p.x, p.y, p.z, 0u};
+  StepTile<T, C, RS, NTH> tk, tv;
+  typename M::F vf[NT][NC];
+  P3 kp{0u, 0u, 0u};
+  const int first = s + CK * (int)blockIdx.y, stride = CK * A.splits;
+  uint64_t on = live<CK>(A, first, e, lane, true);
+  auto fetch = [&](int k0, uint64_t b) {
+    tk.fetch((const T*)A.k, A.ldk, k0, e - k0, tid);
+    if constexpr (VL) tv.fetch((const T*)A.v, A.ldv, k0, e - k0, tid);
+    if (dist && tid < CK) kp = load_pos(A, k0 + tid, (b >> tid) & 1);
+  };
+  auto put = [&](int b, uint64_t live_bits) {
+    if (live_bits != all_live<CK>()) tk.clear(live_bits, tid);
+    tk.put(s_k[b], tid);
+    if constexpr (VL) tv.put(s_v[b], tid);
+    if (dist && tid < CK) s_pos[b][tid] = u4{kp.x, kp.y, kp.z, 0u};
+  };
+  if constexpr (VL) {
+    if (first < e) {
+      fetch(first, on);
+      put(0, on);
+      lds_barrier();
     }
-    tk.put(ks, lane);
-    wave_sync();
+  }
+  int b = 0;
+  for (int k0 = first; k0 < e; k0 += stride) {
+    const int kn = k0 + stride;
+    const uint64_t on_n = live<CK>(A, kn, e, lane, true);
+    if constexpr (VL) {
+      if (kn < e) fetch(kn, on_n);
+    } else {  // mostly a single step: the registers of a step ahead are better left to the wave
+      fetch(k0, on);
+      load_frags<T, C, NT>(vf, (const T*)A.v, A.ldv, k0, e - k0, i, g);
+      put(0, on);
+      wave_sync();
+    }
+    const T *ks = s_k[b], *vs = s_v[VL ? b : 0];
+    const u4* ps = s_pos[b];
+    if (own0 < e) {  // a wave past the structure only keeps step
     f4 r[NT], wgt[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
-      if (A.pos) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float dx, dy, dz;
-          diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
-          r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
-        }
-      }
-    }
+    for (int t = 0; t < NT; ++t) wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
+    if (dist) distances<NT>(r, own, ps, fix, g);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
+      const float sl = dist ? A.slope[h] : 0.f, sl2 = sl * (kLog2e * A.unit);
       f4 ds[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         typename M::F kf[NC];
 #pragma unroll
-        for (int ch = 0; ch < NC; ++ch) kf[ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
+        for (int ch = chunk_of<T, DH>(h); ch < chunk_of<T, DH>(h) + chunks<T, DH>(); ++ch) {
+          kf[ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
+          if constexpr (VL) vf[t][ch] = *(const typename M::F*)(vs + (16 * t + i) * RS + ch * CK + EV * g);
+        }
         const f4 z = f4{0.f, 0.f, 0.f, 0.f};
         const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
         f4 p, dl;
         const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
-        pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl, ds[t]);
-        if (A.pos) {
-          const float sl = A.slope[h];
+        pair_grad<T>(Z, dist, x, dp, r[t], sl2, L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl,
+                     ds[t]);
+        if (dist) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
@@ -620,175 +664,152 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
 #pragma unroll
       for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] = M::mma(acc[ct], ldt<RS>(ks, 0, 16 * ct, lane), pd);
     }
-    if (A.dpos) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float dx, dy, dz;
-          diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
-          const float f = r[t][q] > 0.f ? wgt[t][q] * rcp(r[t][q]) : 0.f;
-          px = fmaf(f, dx, px), py = fmaf(f, dy, py), pz = fmaf(f, dz, pz);
-        }
+    if (A.dpos) add_pairs<NT>(px, wgt, r, own, ps, fix, g);
     }
-    wave_sync();
+    on = on_n;
+    if constexpr (VL) {
+      if (kn < e) put(b ^ 1, on_n);
+      lds_barrier();
+      b ^= 1;
+    } else {
+      wave_sync();
+    }
   }
   if (A.dslope_part) {
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      dsl[h] = row < e ? dsl[h] : 0.f;
-      dsl[h] = group_sum<64>(dsl[h]);
+      dsl[h] = group_sum<64>(row < e ? dsl[h] : 0.f);
       if (lane == 0) s_s[wave][h] = dsl[h];
     }
-  }
-  px = gsum(px), py = gsum(py), pz = gsum(pz);
-  if (g == 0) s_p[wave][0][i] = px, s_p[wave][1][i] = py, s_p[wave][2][i] = pz;
-  if constexpr (KW > 1) {
-    float* slab = (float*)s_w[wave];
+    __syncthreads();
+    if (tid < H) {
+      float v = 0.f;
 #pragma unroll
-    for (int ct = 0; ct < C / 16; ++ct) *(f4*)(slab + i * OS + 16 * ct + 4 * g) = acc[ct];
-  }
-  __syncthreads();
-  if (A.dslope_part && threadIdx.x < H) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) v += s_s[w][threadIdx.x];
-    A.dslope_part[block * H + threadIdx.x] = v * A.unit;
-  }
-  if (A.dpos && threadIdx.x < 48) {
-    const int ri = threadIdx.x / 3, a = threadIdx.x % 3;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) v += s_p[w][a][ri];
-    if (row0 + ri < e) {
-      if (A.splits > 1)
-        A.p_row[3 * ((int64_t)blockIdx.y * A.n + row0) + threadIdx.x] = v;
-      else
-        A.dpos[3 * (int64_t)row0 + threadIdx.x] = v;
+      for (int w = 0; w < NW; ++w) v += s_s[w][tid];
+      A.dslope_part[block * H + tid] = v * A.unit;
     }
   }
-  if constexpr (KW == 1) {
-    if (row >= e) return;
 #pragma unroll
-    for (int ct = 0; ct < C / 16; ++ct) st4((T*)A.dq + (int64_t)row * A.lddq + 16 * ct + 4 * g, acc[ct] * A.scale);
-  } else {
-    for (int x = threadIdx.x; x < 16 * (C / EV); x += 64 * KW) {
-      const int ri = x / (C / EV), c = (x % (C / EV)) * EV;
-      if (row0 + ri >= e) break;
-      f4 o[NT];
+  for (int a = 0; a < 3; ++a) px[a] = gsum(px[a]);
+  if (row >= e) return;
+  const int64_t at = (int64_t)blockIdx.y * A.n + row;
+  if (A.dpos && g < 3) (A.splits > 1 ? A.p_row + 3 * at : A.dpos + 3 * (int64_t)row)[g] = g == 0 ? px[0] : g == 1 ? px[1] : px[2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        o[t] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < KW; ++w) o[t] += *(const f4*)((const float*)s_w[w] + ri * OS + c + 4 * t);
-        o[t] *= A.scale;
-      }
-      if (A.splits > 1) {
-        float* po = A.p_dq + ((int64_t)blockIdx.y * A.n + row0 + ri) * C + c;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) *(f4*)(po + 4 * t) = o[t];
-      } else {
-        st_row<T>((T*)A.dq + (int64_t)(row0 + ri) * A.lddq + c, o);
-      }
-    }
+  for (int ct = 0; ct < C / 16; ++ct) {
+    const int c = 16 * ct + 4 * g;
+    if (A.splits > 1)
+      *(f4*)(A.p_dq + at * C + c) = acc[ct] * A.scale;
+    else
+      st4((T*)A.dq + (int64_t)row * A.lddq + c, acc[ct] * A.scale);
   }
 }
 
 // ------------------------------------------------------------------------------ column pass
 // For 16 keys: dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij dout_i, and the keys' side of the
 // position gradient, added to what the row pass wrote.
-template <class T, int C, int DH, int KW>
-__global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 128 ? 2 : 3))) void k_attn_col(AttnArgs A) {
+template <class T, int C, int DH, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BWD_WAVES))) void k_attn_col(AttnArgs A) {
   using M = MF<T>;
   using D = AttnDims<T, C>;
-  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, OS = D::OS, EV = M::EV;
-  constexpr int TB = CK * RS * sizeof(T);
-  constexpr int TILE = 2 * TB + CK * 16 + 2 * H * CK * 4, SLAB = 2 * 16 * OS * 4;
-  constexpr int WB = KW > 1 && SLAB > TILE ? SLAB : TILE;
-  __shared__ __align__(16) char s_w[KW][WB];
-  __shared__ float s_p[KW][3][16];
-  const int lane = threadIdx.x & 63, wave = KW > 1 ? uniform(threadIdx.x >> 6) : 0, i = lane & 15, g = lane >> 4;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, EV = M::EV, NTH = 64 * NW;
+  constexpr int NB = NW > 1 ? 2 : 1;
+  __shared__ __align__(16) T s_q[NB][CK * RS];
+  __shared__ __align__(16) T s_o[NB][CK * RS];
+  __shared__ u4 s_pos[NB][CK];
+  __shared__ __align__(16) float s_ls[NB][2][H][CK];  // log-sums and dsum of the step's queries
+  const int tid = threadIdx.x, lane = tid & 63, wave = NW > 1 ? uniform(tid >> 6) : 0, i = lane & 15, g = lane >> 4;
   int row0, s, e;
-  if (!find_slot<16>(A, blockIdx.x, lane, row0, s, e)) return;
-  const int row = row0 + i;
-  const bool fix = A.to_fix > 0;
-  const uint64_t own_on = live<16>(A, row0, e, lane, true);
-  const bool own_live = (own_on >> i) & 1;
+  if (!find_slot<16 * NW>(A, blockIdx.x, lane, row0, s, e)) return;
+  const int own0 = row0 + 16 * wave, row = own0 + i;
+  const bool fix = A.to_fix > 0, dist = A.pos != nullptr;
+  const uint64_t own_on = live<16>(A, own0, e, lane, true);
+  const bool own_live = (own_on >> i) & 1, all_own = own_on == 0xffffull;
+  const uint32_t own_bits = own_live ? ~0u : 0u;
   typename M::F kf[1][NC], vf[1][NC];
-  load_frags<T, C, 1>(kf, (const T*)A.k, A.ldk, row0, e - row0, i, g);
-  load_frags<T, C, 1>(vf, (const T*)A.v, A.ldv, row0, e - row0, i, g);
+  load_frags<T, C, 1>(kf, (const T*)A.k, A.ldk, min(own0, e - 1), max(e - own0, 1), i, g);
+  load_frags<T, C, 1>(vf, (const T*)A.v, A.ldv, min(own0, e - 1), max(e - own0, 1), i, g);
   const P3 own = load_pos(A, row, own_live);
-  float slope[H];
-#pragma unroll
-  for (int h = 0; h < H; ++h) slope[h] = A.slope ? A.slope[h] * (kLog2e * A.unit) : 0.f;
   f4 ak[C / 16], av[C / 16];
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) ak[ct] = av[ct] = f4{0.f, 0.f, 0.f, 0.f};
-  float px = 0.f, py = 0.f, pz = 0.f;
-  T *qs = (T*)s_w[wave], *os = (T*)(s_w[wave] + TB);
-  u4* ps = (u4*)(s_w[wave] + 2 * TB);
-  float *ls = (float*)(s_w[wave] + 2 * TB + CK * 16), *ss = ls + H * CK;
+  float px[3] = {0.f, 0.f, 0.f};
   const Score Z = score_of<T>(A);
-  const int first = blockIdx.y * KW + wave;
 
-  if (own_on != 0) {
-    for (int k0 = s + CK * first; k0 < e; k0 += CK * KW * A.splits) {
-      const uint64_t on = live<CK>(A, k0, e, lane, false);
-      WaveTile<T, C, RS> tq, to;
-      tq.fetch((const T*)A.q, A.ldq, k0, e - k0, lane);
-      to.fetch((const T*)A.dout, A.lddo, k0, e - k0, lane);
-      if (on != all_live<CK>()) {
-        tq.clear(on, lane);
-        to.clear(on, lane);
-      }
-      if (lane < CK) {
-        const bool l = (on >> lane) & 1;
-        if (A.pos) {
-          const P3 p = load_pos(A, k0 + lane, l);
-          ps[lane] = u4{p.x, p.y, p.z, 0u};
-        }
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          ls[h * CK + lane] = l ? A.lse[(int64_t)(k0 + lane) * H + h] : INFINITY;
-          ss[h * CK + lane] = l ? A.dsum[(int64_t)(k0 + lane) * H + h] : 0.f;
-        }
-      }
-      tq.put(qs, lane);
-      to.put(os, lane);
-      wave_sync();
-      f4 r[NT], wgt[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
-        if (A.pos) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float dx, dy, dz;
-            diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
-            r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
-          }
-        }
-      }
-      const uint32_t own_bits = own_live ? ~0u : 0u;
-      const bool all_own = own_on == 0xffffull;
+  StepTile<T, C, RS, NTH> tq, to;
+  P3 kp{0u, 0u, 0u};
+  float ln[H], sn[H];
+  const int first = s + CK * (int)blockIdx.y, stride = CK * A.splits;
+  auto fetch = [&](int k0) {
+    tq.fetch((const T*)A.q, A.ldq, k0, e - k0, tid);
+    to.fetch((const T*)A.dout, A.lddo, k0, e - k0, tid);
+    if (tid < CK) {
+      const bool l = k0 + tid < e;
+      if (dist) kp = load_pos(A, k0 + tid, l);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
+        ln[h] = l ? A.lse[(int64_t)(k0 + tid) * H + h] : INFINITY;
+        sn[h] = l ? A.dsum[(int64_t)(k0 + tid) * H + h] : 0.f;
+      }
+    }
+  };
+  auto put = [&](int b, int k0) {
+    if (e - k0 < CK) {
+      tq.clear((1ull << (e - k0)) - 1, tid);
+      to.clear((1ull << (e - k0)) - 1, tid);
+    }
+    tq.put(s_q[b], tid);
+    to.put(s_o[b], tid);
+    if (tid < CK) {
+      if (dist) s_pos[b][tid] = u4{kp.x, kp.y, kp.z, 0u};
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        s_ls[b][0][h][tid] = ln[h];
+        s_ls[b][1][h][tid] = sn[h];
+      }
+    }
+  };
+  if constexpr (NW > 1) {
+    if (first < e) {
+      fetch(first);
+      put(0, first);
+      lds_barrier();
+    }
+  }
+  int b = 0;
+  for (int k0 = first; k0 < e; k0 += stride) {
+    const int kn = k0 + stride;
+    if constexpr (NW == 1) {
+      fetch(k0);
+      put(0, k0);
+      wave_sync();
+    } else {
+      if (kn < e) fetch(kn);
+    }
+    const T *qs = s_q[b], *os = s_o[b];
+    const u4* ps = s_pos[b];
+    if (own_on != 0) {
+      f4 r[NT], wgt[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
+      if (dist) distances<NT>(r, own, ps, fix, g);
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const float sl = dist ? A.slope[h] : 0.f, sl2 = sl * (kLog2e * A.unit);
         f4 p[NT], ds[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           typename M::F qf[NC], of[NC];
 #pragma unroll
-          for (int ch = 0; ch < NC; ++ch) {
+          for (int ch = chunk_of<T, DH>(h); ch < chunk_of<T, DH>(h) + chunks<T, DH>(); ++ch) {
             qf[ch] = *(const typename M::F*)(qs + (16 * t + i) * RS + ch * CK + EV * g);
             of[ch] = *(const typename M::F*)(os + (16 * t + i) * RS + ch * CK + EV * g);
           }
           const f4 z = f4{0.f, 0.f, 0.f, 0.f};
           const f4 x = head_mma<T, DH, NC>(z, qf, kf[0], h, g), dp = head_mma<T, DH, NC>(z, of, vf[0], h, g);
-          const f4 L = *(const f4*)(ls + h * CK + 16 * t + 4 * g), S = *(const f4*)(ss + h * CK + 16 * t + 4 * g);
+          const f4 L = *(const f4*)(s_ls[b][0][h] + 16 * t + 4 * g), S = *(const f4*)(s_ls[b][1][h] + 16 * t + 4 * g);
           f4 dl;
-          pair_grad<T>(Z, A.pos != nullptr, x, dp, r[t], slope[h], L, S, all_own, own_bits, p[t], dl, ds[t]);
-          if (A.pos) {
-            const float sl = A.slope[h];
+          pair_grad<T>(Z, dist, x, dp, r[t], sl2, L, S, all_own, own_bits, p[t], dl, ds[t]);
+          if (dist) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
           }
@@ -800,76 +821,36 @@ __global__ __launch_bounds__(64 * KW) __attribute__((amdgpu_waves_per_eu(C == 12
           ak[ct] = M::mma(ak[ct], ldt<RS>(qs, 0, 16 * ct, lane), pd);
         }
       }
-      if (A.dpos) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float dx, dy, dz;
-            diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
-            const float f = r[t][q] > 0.f ? wgt[t][q] * rcp(r[t][q]) : 0.f;
-            px = fmaf(f, dx, px), py = fmaf(f, dy, py), pz = fmaf(f, dz, pz);
-          }
-      }
+      if (A.dpos) add_pairs<NT>(px, wgt, r, own, ps, fix, g);
+    }
+    if constexpr (NW > 1) {
+      if (kn < e) put(b ^ 1, kn);
+      lds_barrier();
+      b ^= 1;
+    } else {
       wave_sync();
     }
   }
-  px = gsum(px), py = gsum(py), pz = gsum(pz);
-  if (g == 0) s_p[wave][0][i] = px, s_p[wave][1][i] = py, s_p[wave][2][i] = pz;
-  if constexpr (KW > 1) {
-    float* slab = (float*)s_w[wave];
 #pragma unroll
-    for (int ct = 0; ct < C / 16; ++ct) {
-      *(f4*)(slab + i * OS + 16 * ct + 4 * g) = ak[ct];
-      *(f4*)(slab + (16 + i) * OS + 16 * ct + 4 * g) = av[ct];
-    }
+  for (int a = 0; a < 3; ++a) px[a] = gsum(px[a]);
+  if (row >= e) return;
+  const int64_t at = (int64_t)blockIdx.y * A.n + row;
+  if (A.dpos && g < 3) {
+    const float v = g == 0 ? px[0] : g == 1 ? px[1] : px[2];
+    if (A.splits > 1)
+      A.p_col[3 * at + g] = v;
+    else
+      A.dpos[3 * (int64_t)row + g] += v;
   }
-  __syncthreads();
-  if (A.dpos && threadIdx.x < 48) {
-    const int ri = threadIdx.x / 3, a = threadIdx.x % 3;
-    float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < KW; ++w) v += s_p[w][a][ri];
-    if (row0 + ri < e) {
-      if (A.splits > 1)
-        A.p_col[3 * ((int64_t)blockIdx.y * A.n + row0) + threadIdx.x] = v;
-      else
-        A.dpos[3 * (int64_t)row0 + threadIdx.x] += v;
-    }
-  }
-  if constexpr (KW == 1) {
-    if (row >= e) return;
-#pragma unroll
-    for (int ct = 0; ct < C / 16; ++ct) {
-      st4((T*)A.dk + (int64_t)row * A.lddk + 16 * ct + 4 * g, ak[ct] * A.scale);
-      st4((T*)A.dv + (int64_t)row * A.lddv + 16 * ct + 4 * g, av[ct]);
-    }
-  } else {
-    for (int x = threadIdx.x; x < 16 * (C / EV); x += 64 * KW) {
-      const int ri = x / (C / EV), c = (x % (C / EV)) * EV;
-      if (row0 + ri >= e) break;
-      f4 o[NT], u[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        o[t] = u[t] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          o[t] += *(const f4*)((const float*)s_w[w] + ri * OS + c + 4 * t);
-          u[t] += *(const f4*)((const float*)s_w[w] + (16 + ri) * OS + c + 4 * t);
-        }
-        o[t] *= A.scale;
-      }
-      if (A.splits > 1) {
-        const int64_t at = ((int64_t)blockIdx.y * A.n + row0 + ri) * C + c;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          *(f4*)(A.p_dk + at + 4 * t) = o[t];
-          *(f4*)(A.p_dv + at + 4 * t) = u[t];
-        }
-      } else {
-        st_row<T>((T*)A.dk + (int64_t)(row0 + ri) * A.lddk + c, o);
-        st_row<T>((T*)A.dv + (int64_t)(row0 + ri) * A.lddv + c, u);
-      }
+  for (int ct = 0; ct < C / 16; ++ct) {
+    const int c = 16 * ct + 4 * g;
+    if (A.splits > 1) {
+      *(f4*)(A.p_dk + at * C + c) = ak[ct] * A.scale;
+      *(f4*)(A.p_dv + at * C + c) = av[ct];
+    } else {
+      st4((T*)A.dk + (int64_t)row * A.lddk + c, ak[ct] * A.scale);
+      st4((T*)A.dv + (int64_t)row * A.lddv + c, av[ct]);
     }
   }
 }
@@ -960,8 +941,8 @@ int launch_attn_f32(const AttnArgs& A, int C, int dh, bool split, int what, hipS
 
 template <class T, int C, int DH>
 int launch_attn_c(const AttnArgs& A, bool split, int what, hipStream_t st) {
-  const dim3 blocks((unsigned)(A.n / 16 + A.n_struct), (unsigned)A.splits);
-  constexpr int KW = 4;
+  constexpr int NW = 4;
+  const dim3 blocks((unsigned)(A.n / (split ? 16 * NW : 16) + A.n_struct), (unsigned)A.splits);
   constexpr bool SAVES = sizeof(T) == 2;  // float32 has no second form
   auto go = [&](void (*save)(AttnArgs), void (*plain)(AttnArgs), int threads) {
     (A.lse ? save : plain)<<<blocks, threads, 0, st>>>(A);
@@ -969,19 +950,19 @@ int launch_attn_c(const AttnArgs& A, bool split, int what, hipStream_t st) {
   switch (what) {
     case 0:
       if (split)
-        go(k_attn_fwd<T, C, DH, KW, SAVES>, k_attn_fwd<T, C, DH, KW, false>, 64 * KW);
+        go(k_attn_fwd<T, C, DH, NW, SAVES>, k_attn_fwd<T, C, DH, NW, false>, 64 * NW);
       else
         go(k_attn_fwd<T, C, DH, 1, SAVES>, k_attn_fwd<T, C, DH, 1, false>, 64);
       break;
     case 1:
       if (split)
-        k_attn_row<T, C, DH, KW><<<blocks, 64 * KW, 0, st>>>(A);
+        k_attn_row<T, C, DH, NW><<<blocks, 64 * NW, 0, st>>>(A);
       else
         k_attn_row<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
       break;
     default:
       if (split)
-        k_attn_col<T, C, DH, KW><<<blocks, 64 * KW, 0, st>>>(A);
+        k_attn_col<T, C, DH, NW><<<blocks, 64 * NW, 0, st>>>(A);
       else
         k_attn_col<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
   }
