@@ -98,21 +98,39 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 
 // Structure and row range of tile slot `slot` (R rows per slot); false: the slot is empty.
 // Row bounds are clamped to [0, n], so no struct_ptr can lead out of the arrays.
+// The first 64 entries looked at lie about where the slot is if sizes are even, which mostly holds
+// them; they are read once and the structure's bounds taken from their lanes.
 template <int R>
 __device__ __forceinline__ bool find_slot(const AttnArgs& A, int slot, int lane, int& row0, int& s, int& e) {
-  int lo = 0, hi = A.n_struct - 1;
-  while (lo < hi) {
-    const int step = (hi - lo + 64) / 64;  // ceil((hi - lo + 1) / 64)
-    const int b = lo + lane * step;
-    const bool le = b <= hi && min(max(A.sptr[min(b, hi)], 0), A.n) / R + b <= slot;
-    const int k = __popcll(__ballot(le));
-    if (k == 0) return false;
-    lo += (k - 1) * step;
-    hi = min(hi, lo + step - 1);
+  auto at = [&](int b) { return min(max(A.sptr[min(b, A.n_struct)], 0), A.n); };
+  const int guess = (int)((int64_t)slot * A.n_struct / (A.n / R + A.n_struct));
+  int base = max(0, min(guess - 32, A.n_struct - 63)), b, lo = 0, hi = A.n_struct - 1;
+  int v = at(base + lane);
+  int k = __popcll(__ballot(base + lane < A.n_struct && v / R + base + lane <= slot));
+  if (k > 0 && k < 64) {
+    b = base + k - 1;
+    s = __builtin_amdgcn_readlane(v, k - 1);
+    e = __builtin_amdgcn_readlane(v, k);
+  } else {
+    if (k == 0)
+      hi = base - 1;
+    else
+      lo = base + 63;
+    while (lo < hi) {
+      const int step = (hi - lo + 64) / 64;  // ceil((hi - lo + 1) / 64)
+      const int p = lo + lane * step;
+      k = __popcll(__ballot(p <= hi && at(min(p, hi)) / R + p <= slot));
+      if (k == 0) return false;
+      lo += (k - 1) * step;
+      hi = min(hi, lo + step - 1);
+    }
+    if (lo > hi) return false;
+    b = lo;
+    s = uniform(at(b));
+    e = uniform(at(b + 1));
   }
-  s = uniform(min(max(A.sptr[lo], 0), A.n));
-  e = uniform(min(max(A.sptr[lo + 1], s), A.n));
-  const int t = slot - (s / R + lo);
+  e = max(e, s);
+  const int t = slot - (s / R + b);
   row0 = s + t * R;
   return t >= 0 && row0 < e;
 }
@@ -270,9 +288,11 @@ __device__ __forceinline__ void distances(f4 (&r)[NT], const P3& own, const u4* 
       r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
     }
 }
-// waves per SIMD that the register budgets aim at, per kernel
-#define ATTN_FWD_WAVES (C == 128 ? (NW == 1 ? 2 : 3) : 3)
-#define ATTN_BWD_WAVES (C == 128 ? 2 : 3)
+// Waves per SIMD that the register budgets aim at.  More heads hold more running sums and
+// statistics: 8 heads at three waves (forward) or 4 heads of 16 channels at three (backward) spill
+// (11,000 atoms bf16: 720 us against 577; 1,571 against 1,382).
+#define ATTN_FWD_WAVES (C == 128 && C / DH > 4 ? 2 : 3)
+#define ATTN_BWD_WAVES (C == 128 || (C == 64 && C / DH > 2) ? 2 : 3)
 
 // ------------------------------------------------------------------------------ forward
 template <class T, int C, int DH, int NW, bool SAVE>
@@ -310,8 +330,8 @@ void k_attn_fwd(AttnArgs A) {
   typename M::F ones;
   if constexpr (BF) ones = __builtin_bit_cast(typename M::F, u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
 
-  // A step's loads are issued during the step before; without LDS for the keys, each head's keys
-  // as soon as its scores have read the ones they replace
+  // NW = 4: a step's loads are issued during the step before.  NW = 1: mostly a single step, the
+  // registers of a step ahead are better left to more waves.
   StepTile<T, C, RS, NTH> tv, tk;
   typename M::F kf[NT][NC];
   P3 kp{0u, 0u, 0u};
@@ -328,13 +348,11 @@ void k_attn_fwd(AttnArgs A) {
     if constexpr (KL) tk.put(s_k[b], tid);
     if (dist && tid < CK) s_pos[b][tid] = u4{kp.x, kp.y, kp.z, 0u};
   };
-  if (first < e) {
-    fetch(first, on);
-    if constexpr (KL) {
+  if constexpr (KL) {
+    if (first < e) {
+      fetch(first, on);
       put(0, on);
       lds_barrier();
-    } else {
-      load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, first, e - first, i, g);
     }
   }
   int b = 0;
@@ -342,11 +360,14 @@ void k_attn_fwd(AttnArgs A) {
     const int kn = k0 + stride;
     const bool part = on != all_live<CK>();
     const uint64_t on_n = live<CK>(A, kn, e, lane, true);
-    if constexpr (!KL) {
+    if constexpr (KL) {
+      if (kn < e) fetch(kn, on_n);
+    } else {
+      fetch(k0, on);
+      load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, k0, e - k0, i, g);
       put(0, on);
       wave_sync();
     }
-    if (kn < e) fetch(kn, on_n);
     const T *vs = s_v[b], *ks = s_k[KL ? b : 0];
     const u4* ps = s_pos[b];
     if (own0 < e) {  // a wave past the structure only keeps step
@@ -370,11 +391,6 @@ void k_attn_fwd(AttnArgs A) {
             kf[t][ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
         }
         x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
-      }
-      if constexpr (!KL) {
-        if (kn < e && (DH >= CK || h % 2 == 1))
-          load_frags<T, C, NT>(kf, (const T*)A.k, A.ldk, kn, e - kn, i, g, chunk_of<T, DH>(h),
-                               chunk_of<T, DH>(h) + chunks<T, DH>());
       }
       const float sl = dist ? A.slope[h] * (kLog2e * A.unit) : 0.f;
       if (Z.cap) {

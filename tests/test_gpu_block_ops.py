@@ -212,6 +212,10 @@ ATTN = [
     ([1500], 64, 2, "f32", True, 0.0, 0.9, 25.0, 8),
     ([1600], 128, 4, "bf16", True, 0.0, None, 26.0, 0),
     ([1030, 1029], 16, 1, "f32", False, 5.0, None, 0.0, 0),
+    # sizes far from even: the structure of a slot is far from where even sizes would put it
+    ([900] + [1] * 300 + [0] * 90 + [3] * 100, 32, 1, "bf16", True, 0.0, None, 0.0, 0),
+    ([2] * 150 + [0] * 200 + [1] * 200 + [700, 1], 16, 1, "f32", True, 0.0, 0.8, 0.0, 0),
+    ([1] * 70 + [6500], 16, 1, "f32", False, 0.0, None, 0.0, 0),
 ]
 
 
