@@ -276,9 +276,18 @@ __device__ __forceinline__ float score(const Score& Z, float s, float b) {
   return Z.cap ? fmaf(Z.k, cap_of<T>(s, Z.sc), b) : fmaf(s, Z.sc, b);
 }
 
-// The distances of a step's pairs
-template <int NT>
-__device__ __forceinline__ void distances(f4 (&r)[NT], const P3& own, const u4* ps, bool fix, int g) {
+// The distances of a step's pairs: float32 in lengths, so that the slope in base 2 is rounded once;
+// bf16 in units of the coordinates, the unit in the slope
+template <class T>
+__device__ __forceinline__ float r_unit(const AttnArgs& A) {
+  return sizeof(T) == 4 ? A.unit : 1.0f;
+}
+template <class T>
+__device__ __forceinline__ float slope2(const AttnArgs& A, float slope) {
+  return sizeof(T) == 4 ? slope * kLog2e : slope * (kLog2e * A.unit);
+}
+template <class T, int NT>
+__device__ __forceinline__ void distances(f4 (&r)[NT], const AttnArgs& A, const P3& own, const u4* ps, bool fix, int g) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -286,12 +295,13 @@ __device__ __forceinline__ void distances(f4 (&r)[NT], const P3& own, const u4* 
       float dx, dy, dz;
       diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
       r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+      if constexpr (sizeof(T) == 4) r[t][q] *= A.unit;
     }
 }
 // Waves per SIMD that the register budgets aim at.  More heads hold more running sums and
 // statistics: 8 heads at three waves (forward) or 4 heads of 16 channels at three (backward) spill
 // (11,000 atoms bf16: 720 us against 577; 1,571 against 1,382).
-#define ATTN_FWD_WAVES (C == 128 && C / DH > 4 ? 2 : 3)
+#define ATTN_FWD_WAVES (C == 128 && (C / DH > 4 || sizeof(T) == 4) ? 2 : 3)
 #define ATTN_BWD_WAVES (C == 128 || (C == 64 && C / DH > 2) ? 2 : 3)
 
 // ------------------------------------------------------------------------------ forward
@@ -379,7 +389,7 @@ void k_attn_fwd(AttnArgs A) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) lv[t][q] = ((uint32_t)on >> (4 * g)) >> (16 * t + q) & 1;
     }
-    if (dist) distances<NT>(r, own, ps, fix, g);
+    if (dist) distances<T, NT>(r, A, own, ps, fix, g);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       f4 x[NT];
@@ -392,7 +402,7 @@ void k_attn_fwd(AttnArgs A) {
         }
         x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
       }
-      const float sl = dist ? A.slope[h] * (kLog2e * A.unit) : 0.f;
+      const float sl = dist ? slope2<T>(A, A.slope[h]) : 0.f;
       if (Z.cap) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -440,18 +450,22 @@ void k_attn_fwd(AttnArgs A) {
       // weights that the values get
       if constexpr (BF) l[h] = M::mma(l[h], ones, p);
       if constexpr (BF && SAVE) {
-        // for a backward pass the weights enter as two bf16 values, p and its remainder
-        // (2^-18): o32, and with it dsum and the float32 gradients, keep float32's quality
-        f4 y[NT];
+        // for a backward pass the weights enter as three bf16 values, p and its remainders (2^-27):
+        // o32, and with it dsum and the float32 gradients, keep float32's quality
+        f4 y[NT], z[NT];
         M::unpack(p, y);
 #pragma unroll
         for (int t = 0; t < NT; ++t) y[t] = x[t] - y[t];
         const typename M::F p2 = M::pack(y);
-        l[h] = M::mma(l[h], ones, p2);
+        M::unpack(p2, z);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) z[t] = y[t] - z[t];
+        const typename M::F p3 = M::pack(z);
+        l[h] = M::mma(M::mma(l[h], ones, p3), ones, p2);
 #pragma unroll
         for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
           const typename M::F f = ldt<RS>(vs, 0, 16 * ct, lane);
-          acc[ct] = M::mma(M::mma(acc[ct], f, p2), f, p);
+          acc[ct] = M::mma(M::mma(M::mma(acc[ct], f, p3), f, p2), f, p);
         }
       } else {
 #pragma unroll
@@ -532,7 +546,7 @@ __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4
   }
 }
 
-// p += sum over the pairs of wgt (other - own) / r, nothing where r = 0
+// p += sum over the pairs of wgt (other - own) / r, nothing where r = 0 (other - own in units)
 template <int NT>
 __device__ __forceinline__ void add_pairs(float (&p)[3], const f4 (&wgt)[NT], const f4 (&r)[NT], const P3& own,
                                           const u4* ps, bool fix, int g) {
@@ -649,10 +663,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
     f4 r[NT], wgt[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
-    if (dist) distances<NT>(r, own, ps, fix, g);
+    if (dist) distances<T, NT>(r, A, own, ps, fix, g);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const float sl = dist ? A.slope[h] : 0.f, sl2 = sl * (kLog2e * A.unit);
+      const float sl = dist ? A.slope[h] : 0.f, sl2 = slope2<T>(A, sl);
       f4 ds[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -702,11 +716,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) v += s_s[w][tid];
-      A.dslope_part[block * H + tid] = v * A.unit;
+      A.dslope_part[block * H + tid] = sizeof(T) == 4 ? v : v * A.unit;
     }
   }
 #pragma unroll
-  for (int a = 0; a < 3; ++a) px[a] = gsum(px[a]);
+  for (int a = 0; a < 3; ++a) px[a] = r_unit<T>(A) * gsum(px[a]);
   if (row >= e) return;
   const int64_t at = (int64_t)blockIdx.y * A.n + row;
   if (A.dpos && g < 3) (A.splits > 1 ? A.p_row + 3 * at : A.dpos + 3 * (int64_t)row)[g] = g == 0 ? px[0] : g == 1 ? px[1] : px[2];
@@ -807,10 +821,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
       f4 r[NT], wgt[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
-      if (dist) distances<NT>(r, own, ps, fix, g);
+      if (dist) distances<T, NT>(r, A, own, ps, fix, g);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        const float sl = dist ? A.slope[h] : 0.f, sl2 = sl * (kLog2e * A.unit);
+        const float sl = dist ? A.slope[h] : 0.f, sl2 = slope2<T>(A, sl);
         f4 p[NT], ds[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -848,7 +862,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
     }
   }
 #pragma unroll
-  for (int a = 0; a < 3; ++a) px[a] = gsum(px[a]);
+  for (int a = 0; a < 3; ++a) px[a] = r_unit<T>(A) * gsum(px[a]);
   if (row >= e) return;
   const int64_t at = (int64_t)blockIdx.y * A.n + row;
   if (A.dpos && g < 3) {

@@ -520,8 +520,10 @@ int launch_ffn_c(FfnArgs A, int what, hipStream_t st) {
     A.rows_per_split = cdiv(cdiv(A.n, S), MF<T>::CK) * MF<T>::CK;
     k_ffn_dw<T, C><<<dim3((unsigned)cdiv(A.hidden, 64), (unsigned)S), 256, 0, st>>>(A);
   } else {
-    // few rows: the hidden units are split over the waves of a block
-    const bool few = cdiv(A.n, 64 * AT) < 256;
+    // Few rows: the hidden units are split over the waves of a block.  128 channels, 512 hidden
+    // units: bf16 27 us split and 28 not at 8,000 rows, 61 and 30 at 20,000; float32 50 and 108 at
+    // 8,000, 109 and 114 at 20,000.
+    const bool few = A.n < (sizeof(T) == 2 ? 8192 : 20480);
     const unsigned blocks = (unsigned)cdiv(A.n, few ? 16 : 64 * AT);
     if (what == 0) {
       if (few)

@@ -343,8 +343,10 @@ template <class T>
 int launch_linear(const LinArgs& A0, int C, int what, hipStream_t st) {
   LinArgs A = A0;
   constexpr int BIG = sizeof(T) == 2 ? 512 : 256;  // outputs whose rows fit LDS at C = 128
-  // few rows: every wave takes one 16-atom tile, and the outputs are split too
-  const bool few = A.n < 65536;
+  // Few rows: every wave takes one 16-atom tile, and the outputs are split too.  128 -> 384: bf16
+  // 16 us so and 19 with W in LDS at 8,000 rows, 33 and 23 at 32,000; float32 21 and 48 at 8,000,
+  // 60 and 53 at 32,000.
+  const bool few = A.n < (sizeof(T) == 2 ? 16384 : 28672);
   const int64_t bx = few ? cdiv(A.n, 64) : std::min<int64_t>(cdiv(A.n, 256), A.out <= 128 ? 512 : 256);
   const int by = few ? (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(A.out, MF<T>::CK), 512 / bx))
                      : (int)cdiv(A.out, A.out <= 128 ? 128 : BIG);
@@ -360,7 +362,7 @@ int launch_linear(const LinArgs& A0, int C, int what, hipStream_t st) {
       else                                                                                  \
         launch_linear_big<T, CC, BIG>(A, dim3((unsigned)bx, by), st);                       \
     } else if (what == 1) {                                                                 \
-      if (cdiv(A.n, 64) < 512)                                                              \
+      if (A.n < 32768)                                                                      \
         k_linear_dx<T, CC, true><<<(unsigned)cdiv(A.n, 16), 256, 0, st>>>(A);               \
       else                                                                                  \
         k_linear_dx<T, CC, false><<<(unsigned)cdiv(A.n, 64), 256, 0, st>>>(A);              \

@@ -7,6 +7,7 @@ fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -429,7 +430,8 @@ def energy_forces_heads(model, heads, g, perm=None, ws=None):
 # Rows are 2-d cuda tensors of float32 or bfloat16 (torch.bfloat16, or its bits as int16, as in
 # feat_dtype), unit stride in the second dimension and any row stride of a multiple of 16 bytes:
 # h[:, 0] of a feature tensor [n, K, C] is such a matrix.  Outputs are of the rows' dtype unless
-# said otherwise, allocated here when not given.  All calls enqueue on the current stream.
+# said otherwise, allocated here when not given.  All calls enqueue on the current stream of the
+# current device, where every tensor has to be.
 
 ACTS = {"none": 0, "silu": 1, "sigmoid": 2}  # MP_ACT_* of mdmp.h
 
@@ -439,48 +441,67 @@ def _need(ok, where, what):
         raise ValueError(f"{where}: {what}")
 
 
-def _rows(where, name, t, n=None, width=None, like=None):
-    """(pointer, row stride) of a matrix of rows, checked."""
+def _raw_stream(dev):
     import torch
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2, where, f"{name} must be a 2-d cuda tensor")
-    _need(t.device.index == torch.cuda.current_device(), where, f"{name} must be on the current device")
-    _need(t.dtype in (torch.float32, torch.bfloat16, torch.int16), where, f"{name} must be float32 or bfloat16")
-    rows, cols = t.shape
-    if like is not None:
-        _need(t.dtype == like.dtype, where, f"{name} must have the dtype of the other rows")
-    _need(n is None or rows == n, where, f"{name} must have {n} rows")
-    _need(width is None or cols == width, where, f"{name} must have {width} columns")
-    s0, s1 = t.stride()
-    _need(s1 == 1 or cols == 1, where, f"{name} must have unit stride along a row")
-    return t.data_ptr(), (s0 if rows > 1 else max(s0, cols) if (s0 * t.element_size()) % 16 == 0 else cols)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _vec(where, name, t, size, dtype=None):
-    """pointer of a contiguous float32 (or given dtype) device array, None allowed."""
-    import torch
-    if t is None:
-        return None
-    _need(t.is_cuda and t.device.index == torch.cuda.current_device() and t.is_contiguous(), where,
-          f"{name} must be a contiguous tensor on the current device")
-    _need(t.dtype == (dtype or torch.float32), where, f"{name} must be {dtype or torch.float32}")
-    _need(tuple(t.shape) == tuple(size), where, f"{name} must have shape {tuple(size)}")
-    return t.data_ptr()
+class _Rows:
+    """Checks of one call: its rows' number, dtype and device, taken from the first matrix."""
+
+    def __init__(self, where, x):
+        import torch
+        _need(isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda, where, "rows must be 2-d cuda tensors")
+        self.dt = x.dtype
+        self.bf16 = 0 if x.dtype == torch.float32 else 1
+        _need(self.dt in (torch.float32, torch.bfloat16, torch.int16), where, "rows must be float32 or bfloat16")
+        self.dev = torch.cuda.current_device()
+        self.where, self.n, self.c, self.f32 = where, x.shape[0], x.shape[1], torch.float32
+
+    def rows(self, name, t, width=None):
+        """(pointer, row stride) of an [n][width] matrix of rows; (None, 0) for None"""
+        if t is None:
+            return None, 0
+        w = self.c if width is None else width
+        if t.get_device() == self.dev and t.dtype == self.dt and t.dim() == 2 and t.shape[0] == self.n and t.shape[1] == w:
+            s0, s1 = t.stride()
+            if s1 == 1:
+                return t.data_ptr(), s0 if self.n > 1 else w
+        _need(t.get_device() == self.dev, self.where, f"{name} must be on the current device")
+        _need(t.dtype == self.dt, self.where, f"{name} must have the dtype of the other rows")
+        _need(tuple(t.shape) == (self.n, w), self.where, f"{name} must have {self.n} rows of {w}")
+        raise ValueError(f"{self.where}: {name} must have unit stride along a row")
+
+    def vec(self, name, t, shape, dtype=None):
+        """pointer of a contiguous float32 (or given dtype) array, None for None"""
+        if t is None:
+            return None
+        if (t.get_device() == self.dev and t.dtype == (dtype or self.f32) and t.shape == shape and t.is_contiguous()):
+            return t.data_ptr()
+        _need(t.get_device() == self.dev and t.is_contiguous(), self.where,
+              f"{name} must be a contiguous tensor on the current device")
+        _need(t.dtype == (dtype or self.f32), self.where, f"{name} must be {dtype or self.f32}")
+        raise ValueError(f"{self.where}: {name} must have shape {tuple(shape)}")
+
+    def new(self, width=None, dtype=None):
+        import torch
+        return torch.empty(self.n, self.c if width is None else width, dtype=dtype or self.dt, device=self.dev)
+
+    def vec_new(self, size):
+        import torch
+        return torch.empty(size, dtype=self.f32, device=self.dev)
+
+    def ws(self, nbytes):
+        import torch
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.dev)
 
 
-def _is_bf16(t):
-    import torch
-    return 0 if t.dtype == torch.float32 else 1
-
-
-def _new_rows(n, width, like):
-    import torch
-    return torch.empty(n, width, dtype=like.dtype, device=like.device)
-
-
-def _wsbytes(fn, where, *args):
-    nbytes = ctypes.c_size_t(0)
-    _check(fn(*args, ctypes.byref(nbytes)), where)
-    return nbytes.value
+@functools.lru_cache(maxsize=512)
+def _size_of(fn, ctype, *args):
+    """what a size query of the library answers for a shape"""
+    n = ctype(0)
+    _check(getattr(_lib, fn)(*args, ctypes.byref(n)), fn)
+    return n.value
 
 
 def _act_id(where, act):
@@ -491,16 +512,12 @@ def _act_id(where, act):
 def linear(x, weight, bias=None, act="none", residual=None, out=None):
     """residual + act(x weight^T + bias): x [n][in], weight [out][in], bias float32 [out] -> [n][out].
     out may be residual."""
-    n, k = x.shape
+    r = _Rows("linear", x)
     o = weight.shape[0]
-    xp, ldx = _rows("linear", "x", x)
-    wp = _vec("linear", "weight", weight, (o, k), x.dtype)
-    bp = _vec("linear", "bias", bias, (o,))
-    rp, ldr = _rows("linear", "residual", residual, n, o, x) if residual is not None else (None, 0)
-    out = _new_rows(n, o, x) if out is None else out
-    yp, ldy = _rows("linear", "out", out, n, o, x)
-    _check(_lib.mp_linear(n, k, o, _is_bf16(x), _act_id("linear", act), xp, ldx, wp, bp, rp, ldr, yp, ldy, _stream()),
-           "mp_linear")
+    out = r.new(o) if out is None else out
+    _check(_lib.mp_linear(r.n, r.c, o, r.bf16, _act_id("linear", act), *r.rows("x", x),
+                          r.vec("weight", weight, (o, r.c), r.dt), r.vec("bias", bias, (o,)),
+                          *r.rows("residual", residual, o), *r.rows("out", out, o), _raw_stream(r.dev)), "mp_linear")
     return out
 
 
@@ -508,37 +525,33 @@ def linear_bwd(x, weight, dy, bias=None, act="none", weight_grads=True):
     """(dx, dweight, dbias) of linear for dy [n][out]; the residual's gradient is dy.  dbias is
     float32, None without a bias; without weight_grads (forces only) dweight and dbias are None."""
     import torch
-    n, k = x.shape
+    r = _Rows("linear_bwd", x)
     o = weight.shape[0]
-    xp, ldx = _rows("linear_bwd", "x", x)
-    wp = _vec("linear_bwd", "weight", weight, (o, k), x.dtype)
-    bp = _vec("linear_bwd", "bias", bias, (o,))
-    dp, ldd = _rows("linear_bwd", "dy", dy, n, o, x)
-    dx = _new_rows(n, k, x)
+    dx = r.new()
     dw = db = ws = None
+    nws = 0
     if weight_grads:
         dw = torch.empty_like(weight)
-        db = torch.empty(o, dtype=torch.float32, device=x.device) if bias is not None else None
-        ws = _ws(_wsbytes(_lib.mp_linear_bwd_ws, "mp_linear_bwd_ws", n, k, o, _is_bf16(x)))
-    _check(_lib.mp_linear_bwd(n, k, o, _is_bf16(x), _act_id("linear_bwd", act), xp, ldx, wp, bp, dp, ldd,
-                              dx.data_ptr(), k, _ptr(dw), _ptr(db), _ptr(ws), ws.numel() if ws is not None else 0,
-                              _stream()), "mp_linear_bwd")
+        db = r.vec_new(o) if bias is not None else None
+        nws = _size_of("mp_linear_bwd_ws", ctypes.c_size_t, r.n, r.c, o, r.bf16)
+        ws = r.ws(nws)
+    _check(_lib.mp_linear_bwd(r.n, r.c, o, r.bf16, _act_id("linear_bwd", act), *r.rows("x", x),
+                              r.vec("weight", weight, (o, r.c), r.dt), r.vec("bias", bias, (o,)),
+                              *r.rows("dy", dy, o), dx.data_ptr(), r.c, _ptr(dw), _ptr(db), _ptr(ws), nws,
+                              _raw_stream(r.dev)), "mp_linear_bwd")
     return dx, dw, db
 
 
 def gated_ffn(x, w_gate, w_up, w_down, act="silu", residual=None, out=None):
     """residual + (act(x w_gate^T) * (x w_up^T)) w_down^T: x [n][C], w_gate and w_up [hidden][C],
     w_down [C][hidden] -> [n][C].  out may be residual."""
-    n, c = x.shape
+    r = _Rows("gated_ffn", x)
     f = w_gate.shape[0]
-    xp, ldx = _rows("gated_ffn", "x", x)
-    w = [_vec("gated_ffn", k, t, s, x.dtype) for k, t, s in
-         (("w_gate", w_gate, (f, c)), ("w_up", w_up, (f, c)), ("w_down", w_down, (c, f)))]
-    rp, ldr = _rows("gated_ffn", "residual", residual, n, c, x) if residual is not None else (None, 0)
-    out = _new_rows(n, c, x) if out is None else out
-    yp, ldy = _rows("gated_ffn", "out", out, n, c, x)
-    _check(_lib.mp_gated_ffn(n, c, f, _is_bf16(x), _act_id("gated_ffn", act), xp, ldx, *w, rp, ldr, yp, ldy,
-                             _stream()), "mp_gated_ffn")
+    out = r.new() if out is None else out
+    _check(_lib.mp_gated_ffn(r.n, r.c, f, r.bf16, _act_id("gated_ffn", act), *r.rows("x", x),
+                             r.vec("w_gate", w_gate, (f, r.c), r.dt), r.vec("w_up", w_up, (f, r.c), r.dt),
+                             r.vec("w_down", w_down, (r.c, f), r.dt), *r.rows("residual", residual),
+                             *r.rows("out", out), _raw_stream(r.dev)), "mp_gated_ffn")
     return out
 
 
@@ -546,30 +559,25 @@ def gated_ffn_bwd(x, w_gate, w_up, w_down, dy, act="silu", weight_grads=True):
     """(dx, dw_gate, dw_up, dw_down) of gated_ffn for dy [n][C]; the residual's gradient is dy.
     Without weight_grads (forces only) the last three are None."""
     import torch
-    n, c = x.shape
+    r = _Rows("gated_ffn_bwd", x)
     f = w_gate.shape[0]
-    xp, ldx = _rows("gated_ffn_bwd", "x", x)
-    w = [_vec("gated_ffn_bwd", k, t, s, x.dtype) for k, t, s in
-         (("w_gate", w_gate, (f, c)), ("w_up", w_up, (f, c)), ("w_down", w_down, (c, f)))]
-    dp, ldd = _rows("gated_ffn_bwd", "dy", dy, n, c, x)
-    dx = _new_rows(n, c, x)
-    g, ws = [None] * 3, None
+    dx = r.new()
+    g, ws, nws = [None] * 3, None, 0
     if weight_grads:
         g = [torch.empty_like(t) for t in (w_gate, w_up, w_down)]
-        ws = _ws(_wsbytes(_lib.mp_gated_ffn_bwd_ws, "mp_gated_ffn_bwd_ws", n, c, f, _is_bf16(x)))
-    _check(_lib.mp_gated_ffn_bwd(n, c, f, _is_bf16(x), _act_id("gated_ffn_bwd", act), xp, ldx, *w, dp, ldd,
-                                 dx.data_ptr(), c, *[_ptr(t) for t in g], _ptr(ws),
-                                 ws.numel() if ws is not None else 0, _stream()), "mp_gated_ffn_bwd")
+        nws = _size_of("mp_gated_ffn_bwd_ws", ctypes.c_size_t, r.n, r.c, f, r.bf16)
+        ws = r.ws(nws)
+    _check(_lib.mp_gated_ffn_bwd(r.n, r.c, f, r.bf16, _act_id("gated_ffn_bwd", act), *r.rows("x", x),
+                                 r.vec("w_gate", w_gate, (f, r.c), r.dt), r.vec("w_up", w_up, (f, r.c), r.dt),
+                                 r.vec("w_down", w_down, (r.c, f), r.dt), *r.rows("dy", dy), dx.data_ptr(), r.c,
+                                 *[_ptr(t) for t in g], _ptr(ws), nws, _raw_stream(r.dev)), "mp_gated_ffn_bwd")
     return (dx, *g)
 
 
-def _norm_args(where, x, b, scale, gate, w_post, w_pre, eps):
-    n, c = x.shape
-    xp, ldx = _rows(where, "x", x)
-    bp, ldb = _rows(where, "b", b, n, c, x)
-    gp, ldg = _rows(where, "gate", gate, n, c, x) if gate is not None else (None, 0)
-    return mp_norm_args(n, c, _is_bf16(x), eps, xp, ldx, bp, ldb, gp, ldg, _vec(where, "scale", scale, (c,)),
-                        _vec(where, "w_post", w_post, (c,)), _vec(where, "w_pre", w_pre, (c,)))
+def _norm_args(r, x, b, scale, gate, w_post, w_pre, eps):
+    c = (r.c,)
+    return mp_norm_args(r.n, r.c, r.bf16, eps, *r.rows("x", x), *r.rows("b", b), *r.rows("gate", gate),
+                        r.vec("scale", scale, c), r.vec("w_post", w_post, c), r.vec("w_pre", w_pre, c))
 
 
 def norm_block(x, b, scale=None, gate=None, w_post=None, w_pre=None, eps=1e-6, out=None):
@@ -577,49 +585,42 @@ def norm_block(x, b, scale=None, gate=None, w_post=None, w_pre=None, eps=1e-6, o
     norm after a block with its gate and residual scale and the norm before the next block.
     scale, w_post, w_pre float32 [C] or None (no factor; no norm of b; u = None); gate rows or None.
     out (for y) may be x or b."""
-    n, c = x.shape
-    a = _norm_args("norm_block", x, b, scale, gate, w_post, w_pre, eps)
-    y = _new_rows(n, c, x) if out is None else out
-    yp, ldy = _rows("norm_block", "out", y, n, c, x)
-    u = _new_rows(n, c, x) if w_pre is not None else None
-    _check(_lib.mp_norm_block(ctypes.byref(a), yp, ldy, _ptr(u), c, _stream()), "mp_norm_block")
+    r = _Rows("norm_block", x)
+    a = _norm_args(r, x, b, scale, gate, w_post, w_pre, eps)
+    y = r.new() if out is None else out
+    u = r.new() if w_pre is not None else None
+    _check(_lib.mp_norm_block(ctypes.byref(a), *r.rows("out", y), _ptr(u), r.c, _raw_stream(r.dev)), "mp_norm_block")
     return y, u
 
 
 def norm_block_bwd(x, b, dy, du=None, scale=None, gate=None, w_post=None, w_pre=None, eps=1e-6, param_grads=True):
     """Gradients of norm_block for dy and du (either may be None: zero) as a dict: dx, db, dgate
     (rows) and dscale, dw_post, dw_pre (float32); None for what was not given."""
-    import torch
-    w = "norm_block_bwd"
-    n, c = x.shape
-    a = _norm_args(w, x, b, scale, gate, w_post, w_pre, eps)
-    dyp, lddy = _rows(w, "dy", dy, n, c, x) if dy is not None else (None, 0)
-    dup, lddu = _rows(w, "du", du, n, c, x) if du is not None else (None, 0)
-    g = {"dx": _new_rows(n, c, x), "db": _new_rows(n, c, x), "dgate": _new_rows(n, c, x) if gate is not None else None}
-    ws = None
+    r = _Rows("norm_block_bwd", x)
+    a = _norm_args(r, x, b, scale, gate, w_post, w_pre, eps)
+    g = {"dx": r.new(), "db": r.new(), "dgate": r.new() if gate is not None else None}
+    ws, nws = None, 0
     for k, p in (("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
-        g[k] = torch.empty(c, dtype=torch.float32, device=x.device) if p is not None and param_grads else None
+        g[k] = r.vec_new(r.c) if p is not None and param_grads else None
         if g[k] is not None and ws is None:
-            ws = _ws(_wsbytes(_lib.mp_norm_block_bwd_ws, "mp_norm_block_bwd_ws", n, c, _is_bf16(x)))
-    _check(_lib.mp_norm_block_bwd(ctypes.byref(a), dyp, lddy, dup, lddu, _ptr(g["dx"]), c, _ptr(g["db"]), c,
-                                  _ptr(g["dgate"]), c, _ptr(g["dscale"]), _ptr(g["dw_post"]), _ptr(g["dw_pre"]),
-                                  _ptr(ws), ws.numel() if ws is not None else 0, _stream()), "mp_norm_block_bwd")
+            nws = _size_of("mp_norm_block_bwd_ws", ctypes.c_size_t, r.n, r.c, r.bf16)
+            ws = r.ws(nws)
+    _check(_lib.mp_norm_block_bwd(ctypes.byref(a), *r.rows("dy", dy), *r.rows("du", du), _ptr(g["dx"]), r.c,
+                                  _ptr(g["db"]), r.c, _ptr(g["dgate"]), r.c, _ptr(g["dscale"]), _ptr(g["dw_post"]),
+                                  _ptr(g["dw_pre"]), _ptr(ws), nws, _raw_stream(r.dev)), "mp_norm_block_bwd")
     return g
 
 
-def _attention_args(where, q, k, v, struct_ptr, heads, pos, slope, L, mask, cap):
+def _attention_args(r, q, k, v, struct_ptr, heads, pos, slope, L, mask, cap):
     import torch
-    n, c = q.shape
-    qp, ldq = _rows(where, "q", q)
-    kp, ldk = _rows(where, "k", k, n, c, q)
-    vp, ldv = _rows(where, "v", v, n, c, q)
-    sp = _vec(where, "struct_ptr", struct_ptr, (struct_ptr.numel(),), torch.int32)
-    _need(struct_ptr.numel() >= 1, where, "struct_ptr must hold n_struct + 1 entries")
+    nst = struct_ptr.numel() - 1
+    _need(nst >= 0, r.where, "struct_ptr must hold n_struct + 1 entries")
     if mask is not None and mask.dtype == torch.bool:
         mask = mask.view(torch.uint8)
-    return mp_attention_args(n, struct_ptr.numel() - 1, c, heads, _is_bf16(q), cap, L, sp,
-                             _vec(where, "pos", pos, (n, 3)), _vec(where, "slope", slope, (heads,)),
-                             _vec(where, "mask", mask, (n,), torch.uint8), qp, ldq, kp, ldk, vp, ldv)
+    return mp_attention_args(r.n, nst, r.c, heads, r.bf16, cap, L, r.vec("struct_ptr", struct_ptr, (nst + 1,), torch.int32),
+                             r.vec("pos", pos, (r.n, 3)), r.vec("slope", slope, (heads,)),
+                             r.vec("mask", mask, (r.n,), torch.uint8), *r.rows("q", q), *r.rows("k", k),
+                             *r.rows("v", v))
 
 
 def structure_attention(q, k, v, struct_ptr, heads, pos=None, slope=None, L=0.0, mask=None, cap=0.0, out=None,
@@ -630,21 +631,14 @@ def structure_attention(q, k, v, struct_ptr, heads, pos=None, slope=None, L=0.0,
     image if L > 0), over the atoms with mask != 0 (bool or uint8 [n]).  Rows past the last structure are
     not written (an out allocated here holds anything there).  save: returns (out, saved), saved for
     structure_attention_bwd."""
-    import torch
-    n, c = q.shape
-    a = _attention_args("structure_attention", q, k, v, struct_ptr, heads, pos, slope, L, mask, cap)
-    out = _new_rows(n, c, q) if out is None else out
-    op, ldo = _rows("structure_attention", "out", out, n, c, q)
-    saved = None
-    if save:
-        m = ctypes.c_int64(0)
-        _check(_lib.mp_structure_attention_saved(n, c, heads, a.feat_dtype, ctypes.byref(m)),
-               "mp_structure_attention_saved")
-        saved = torch.empty(m.value, dtype=torch.float32, device=q.device)
-    need = _wsbytes(_lib.mp_structure_attention_ws, "mp_structure_attention_ws", n, a.n_struct, c, heads)
-    ws = _ws(need) if need else None
-    _check(_lib.mp_structure_attention(ctypes.byref(a), op, ldo, _ptr(saved), _ptr(ws), need, _stream()),
-           "mp_structure_attention")
+    r = _Rows("structure_attention", q)
+    a = _attention_args(r, q, k, v, struct_ptr, heads, pos, slope, L, mask, cap)
+    out = r.new() if out is None else out
+    saved = r.vec_new(_size_of("mp_structure_attention_saved", ctypes.c_int64, r.n, r.c, heads, r.bf16)) if save else None
+    nws = _size_of("mp_structure_attention_ws", ctypes.c_size_t, r.n, a.n_struct, r.c, heads)
+    ws = r.ws(nws) if nws else None
+    _check(_lib.mp_structure_attention(ctypes.byref(a), *r.rows("out", out), _ptr(saved), _ptr(ws), nws,
+                                       _raw_stream(r.dev)), "mp_structure_attention")
     return (out, saved) if save else out
 
 
@@ -654,24 +648,19 @@ def structure_attention_bwd(q, k, v, struct_ptr, heads, out, saved, dout, pos=No
     dslope float32 [heads] (None without pos).  out, saved: what the forward call returned.  dq, dk, dv
     and dpos may be given to be written into (column slices of one matrix, say).  Rows past the last
     structure are not written (tensors allocated here hold anything there)."""
-    import torch
-    w = "structure_attention_bwd"
-    n, c = q.shape
-    a = _attention_args(w, q, k, v, struct_ptr, heads, pos, slope, L, mask, cap)
-    op, ldo = _rows(w, "out", out, n, c, q)
-    dp, ldd = _rows(w, "dout", dout, n, c, q)
-    m = ctypes.c_int64(0)
-    _check(_lib.mp_structure_attention_saved(n, c, heads, a.feat_dtype, ctypes.byref(m)),
-           "mp_structure_attention_saved")
-    sp = _vec(w, "saved", saved, (m.value,))
-    g = {key: _new_rows(n, c, q) if t is None else t for key, t in (("dq", dq), ("dk", dk), ("dv", dv))}
-    rows = [x for key in ("dq", "dk", "dv") for x in _rows(w, key, g[key], n, c, q)]
-    g["dpos"] = torch.empty(n, 3, dtype=torch.float32, device=q.device) if pos is not None and dpos is None else dpos
-    g["dslope"] = torch.empty(heads, dtype=torch.float32, device=q.device) if pos is not None else None
-    ws = _ws(_wsbytes(_lib.mp_structure_attention_bwd_ws, "mp_structure_attention_bwd_ws", n, a.n_struct, c, heads))
-    _check(_lib.mp_structure_attention_bwd(ctypes.byref(a), op, ldo, sp, dp, ldd, *rows,
-                                           _vec(w, "dpos", g["dpos"], (n, 3)), _ptr(g["dslope"]), _ptr(ws),
-                                           ws.numel(), _stream()),
+    r = _Rows("structure_attention_bwd", q)
+    a = _attention_args(r, q, k, v, struct_ptr, heads, pos, slope, L, mask, cap)
+    _need(dpos is None or pos is not None, r.where, "dpos without pos")
+    m = _size_of("mp_structure_attention_saved", ctypes.c_int64, r.n, r.c, heads, r.bf16)
+    g = {"dq": r.new() if dq is None else dq, "dk": r.new() if dk is None else dk, "dv": r.new() if dv is None else dv,
+         "dpos": r.new(3, r.f32) if pos is not None and dpos is None else dpos,
+         "dslope": r.vec_new(heads) if pos is not None else None}
+    nws = _size_of("mp_structure_attention_bwd_ws", ctypes.c_size_t, r.n, a.n_struct, r.c, heads)
+    ws = r.ws(nws)
+    _check(_lib.mp_structure_attention_bwd(ctypes.byref(a), *r.rows("out", out), r.vec("saved", saved, (m,)),
+                                           *r.rows("dout", dout), *r.rows("dq", g["dq"]), *r.rows("dk", g["dk"]),
+                                           *r.rows("dv", g["dv"]), r.vec("dpos", g["dpos"], (r.n, 3)),
+                                           _ptr(g["dslope"]), _ptr(ws), nws, _raw_stream(r.dev)),
            "mp_structure_attention_bwd")
     return g
 
@@ -717,7 +706,9 @@ def energy_forces_mixer(model, mixer, g, struct_ptr=None, perm=None, atom_energy
         _check(_lib.mp_energy_forces_mixer_ws(model.h, mixer.h, g.n, nst, max(g.n_edges, 1), ctypes.byref(nbytes)),
                "mp_energy_forces_mixer_ws")
         ws = _ws(nbytes.value)
-    sp = _vec("energy_forces_mixer", "struct_ptr", struct_ptr, (nst + 1,), torch.int32)
+    _need(struct_ptr.is_cuda and struct_ptr.is_contiguous() and struct_ptr.dtype == torch.int32 and struct_ptr.dim() == 1,
+          "energy_forces_mixer", "struct_ptr must be a contiguous 1-d int32 cuda tensor")
+    sp = struct_ptr.data_ptr()
     energy = torch.zeros(1, dtype=torch.float64, device="cuda")
     forces = torch.empty(g.n, 3, dtype=torch.float32, device="cuda")
     gs = g.struct()
