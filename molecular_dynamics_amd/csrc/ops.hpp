@@ -199,19 +199,18 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Asks the scheduler for LDS reads AHEAD operands before their products: of READS operands and
-// MFMAS products, AHEAD reads first, then the rest spread over the products.  Left alone it reads
-// each operand just before its products and waits out the LDS latency every time.
-template <int READS, int AHEAD, int MFMAS>
+// Asks the scheduler to read operands from LDS ahead of their products: AHEAD reads first, then N
+// times MFMAS products and READS reads, then REST products.  Left alone it reads each operand just
+// before its products and waits out the LDS latency every time.
+template <int AHEAD, int N, int MFMAS, int READS, int REST>
 __device__ __forceinline__ void read_ahead() {
-  constexpr int A = AHEAD < READS ? AHEAD : READS, REST = READS - A, PER = MFMAS / READS;
-  __builtin_amdgcn_sched_group_barrier(0x100, A, 0);
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
 #pragma unroll
-  for (int q = 0; q < REST; ++q) {
-    __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  for (int q = 0; q < N; ++q) {
+    __builtin_amdgcn_sched_group_barrier(0x008, MFMAS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
   }
-  __builtin_amdgcn_sched_group_barrier(0x008, MFMAS - REST * PER, 0);
+  __builtin_amdgcn_sched_group_barrier(0x008, REST, 0);
 }
 
 // sum over the four lane groups (lanes i, 16 + i, 32 + i, 48 + i)
