@@ -272,17 +272,17 @@ int mp_energy_forces_heads(const mp_model* m, const mp_heads* heads, const mp_gr
  *
  * Rows: a matrix of n rows is a device pointer and a row stride ld (elements), so
  * h^0 of a feature array [n][K][C] is (h, K C); rows must be 16-byte aligned and
- * ld a multiple of 16 bytes (attention: at most 2^24).  Features and weight matrices are of feat_dtype
- * (0 float32, 1 bfloat16); vectors of parameters, positions and slopes and the
- * gradients of those are float32.  bfloat16: products take bf16 operands with
- * float32 accumulation, everything else is float32, and each output is rounded
- * once; an intermediate that is the operand of a second product (hidden units,
- * attention weights, their gradients) is rounded to bf16 on the way in.  channels
- * C: 16 (float32 only), 32, 64 or 128.  n = 0 is allowed: no row is touched and
- * parameter gradients are zeros.  Outputs must not overlap inputs or one another
- * unless a call says so.  All calls only enqueue work (no host sync, no
- * allocation, no memset nodes, so they can be captured) and give equal bits for
- * equal inputs.  ws: device scratch of at least the _ws call's bytes, 16-byte
+ * ld a multiple of 16 bytes (attention: at most 2^24).  Features and weight
+ * matrices are of feat_dtype (0 float32, 1 bfloat16); vectors of parameters,
+ * positions and slopes and the gradients of those are float32.  bfloat16: products
+ * take bf16 operands with float32 accumulation, everything else is float32, and
+ * each output is rounded once; an intermediate that is the operand of a second
+ * product (hidden units, attention weights, their gradients) is rounded to bf16 on
+ * the way in.  channels C: 16 (float32 only), 32, 64 or 128.  n is at most 2^26;
+ * n = 0 is allowed: no row is touched and parameter gradients are zeros.  Outputs
+ * must not overlap inputs or one another unless a call says so (column slices of one
+ * matrix do not).  All calls only enqueue work (no host sync, no allocation, no
+ * memset nodes, so they can be captured) and give equal bits for equal inputs.  ws: device scratch of at least the _ws call's bytes, 16-byte
  * aligned, used by one call at a time. */
 #define MP_ACT_NONE 0
 #define MP_ACT_SILU 1
@@ -347,17 +347,18 @@ int mp_norm_block_bwd(const mp_norm_args* a, const void* dy, int64_t lddy, const
 
 /* Attention between all atoms of each structure, beyond the cutoff.  For atom i of
  * structure b and head k (channels k d .. k d + d - 1, d = C / heads):
- *   t_ij = q_i^k . k_j^k / sqrt(d),   s_ij = cap tanh(t_ij / cap)  (cap = 0: t_ij)
+ *   t_ij = q_i^k . k_j^k / sqrt(d),   s_ij = cap tanh(t_ij / cap)  (cap = 0: t_ij;
+ *                                                        else cap in 1e-3 .. 1e4)
  *   a_ij = softmax_j(s_ij - slope_k r_ij) over the atoms j of b with mask_j != 0
  *   out_i = sum_j a_ij v_j
  * r_ij = |x_j - x_i|, minimum image if box_L > 0 (positions may be unwrapped).  An
  * atom whose structure has no unmasked atom gets zeros.  Masked atoms' keys and
- * values are not used, whatever they hold (their own rows of out are written), and
- * structures do not see one another.  The atoms of structure b are rows
- * struct_ptr[b] .. struct_ptr[b+1] - 1 (device, int32 [n_struct + 1], struct_ptr[0] =
- * 0, ascending, empty structures allowed); rows at or past struct_ptr[n_struct] are
- * left as they are in every output.  pos and slope both null: no distance term.
- * heads: C / heads is 16, 32 or 64. */
+ * values are not used, whatever they hold; their own rows of out are written, so their
+ * queries and positions, like slopes, are finite.  Structures do not see one another.
+ * The atoms of structure b are rows struct_ptr[b] .. struct_ptr[b+1] - 1 (device, int32
+ * [n_struct + 1], struct_ptr[0] = 0, ascending, empty structures allowed); rows at or
+ * past struct_ptr[n_struct] are left as they are in every output.  pos and slope both null: no distance term.
+ * n_struct is at most 2^25.  heads: C / heads is 16, 32 or 64. */
 typedef struct {
   int32_t n, n_struct, channels, heads, feat_dtype;
   float cap, box_L;
@@ -410,7 +411,7 @@ int mp_mixer_destroy(mp_mixer* mixer);
  * (device, int32 [n_struct + 1], ascending, struct_ptr[n_struct] = n): the structures, in
  * the graph's slot order ({0, n} for one box).  atom_energy nullable.  ws: at least
  * mp_energy_forces_mixer_ws bytes, 256-byte aligned; mp_energy_forces_status reads its
- * flag.  MP_ERR_ARG if the mixer was made for other channels or feat_dtype. */
+ * flag, and is MP_ERR_ARG after a struct_ptr that did not ascend from 0 to n.  MP_ERR_ARG if the mixer was made for other channels or feat_dtype. */
 int mp_energy_forces_mixer_ws(const mp_model* m, const mp_mixer* mixer, int32_t n, int32_t n_struct, int64_t n_edges,
                               size_t* bytes);
 int mp_energy_forces_mixer(const mp_model* m, const mp_mixer* mixer, const mp_graph* g, const int32_t* struct_ptr,
@@ -470,7 +471,8 @@ int mp_md_destroy(mp_md* md);
 /* ------------------------------------------------------------ profiling ----
  * Optional kernel timing with hipEvents recorded on the launching stream
  * around the named launches: "build_neighbors", "geometry", "edge_fwd",
- * "edge_bwd_recv", "edge_bwd_send", "forces".  Off by default; recording is
+ * "edge_bwd_recv", "edge_bwd_send", "forces", and the block operators' calls by their
+ * names without mp_ ("linear", "gated_ffn_bwd", ...).  Off by default; recording is
  * skipped while a stream is being captured.  mp_profile_read synchronises the
  * recorded events and returns the summed time and the launch count for one
  * name since the last reset.  Host-side registry, not thread-safe across

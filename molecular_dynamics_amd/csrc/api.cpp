@@ -608,6 +608,7 @@ extern "C" int mp_energy_forces_status(const void* ws, hipStream_t st) {
   int32_t hflag = 0;
   MP_HIP(hipMemcpyAsync(&hflag, ws, sizeof(int32_t), hipMemcpyDeviceToHost, st));
   MP_HIP(hipStreamSynchronize(st));
+  if (hflag & 2) return arg_error("mp_energy_forces_mixer: struct_ptr must ascend from 0 to n");
   if (hflag) {
     set_error("non-finite energy or force");
     return MP_ERR_NUMERIC;

@@ -1,7 +1,6 @@
 // Energy and forces with global blocks (attention beyond the cutoff, feed-forward) between
 // the last layer and the readout: the block operators in sequence, forward and backward.
 #include <algorithm>
-#include <cmath>
 #include <vector>
 
 #include "model.hpp"
@@ -93,10 +92,16 @@ __global__ __launch_bounds__(256) void k_grad_rows(float* __restrict__ g_h, int6
 struct DposList {
   const float* p[MP_MAX_BLOCKS];
 };
-// forces[perm] -= the blocks' position gradients, in block order; non-finite sums set the flag
+// forces[perm] -= the blocks' position gradients, in block order; non-finite sums set the flag's
+// first bit, a struct_ptr that does not go from 0 to n in ascending order its second (rows outside
+// the structures have no attention, so their sums mean nothing)
 __global__ __launch_bounds__(256) void k_mixer_forces(DposList L, int B, int n, const int32_t* __restrict__ perm,
+                                                      const int32_t* __restrict__ sptr, int n_struct,
                                                       float* __restrict__ F, int32_t* __restrict__ flag) {
   const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  bool bad = x == 0 && (sptr[0] != 0 || sptr[n_struct] != n);
+  for (int64_t b = x; b < n_struct; b += (int64_t)gridDim.x * 256) bad |= sptr[b] > sptr[b + 1];
+  if (bad) atomicOr(flag, 2);
   if (x >= 3 * (int64_t)n) return;
   float s = 0.f;
   for (int t = 0; t < B; ++t) s += L.p[t][x];
@@ -207,7 +212,8 @@ int mixer_forces(const MixRun& R, const Plan& P, const int32_t* perm, float* for
   MP_TRY(carve(a, R.mixer, P.n, R.n_struct, w));
   DposList L{};
   for (int t = 0; t < R.mixer->B; ++t) L.p[t] = w.s[t].dpos;
-  k_mixer_forces<<<(int)cdiv(3 * (int64_t)P.n, 256), 256, 0, st>>>(L, R.mixer->B, P.n, perm, forces, flag);
+  k_mixer_forces<<<(int)cdiv(3 * (int64_t)P.n, 256), 256, 0, st>>>(L, R.mixer->B, P.n, perm, R.struct_ptr, R.n_struct,
+                                                                 forces, flag);
   MP_CHECK_LAUNCH();
   return MP_OK;
 }
@@ -227,7 +233,7 @@ extern "C" int mp_mixer_create(const mp_model* m, int32_t n_blocks, int32_t head
                                const float* w, int64_t nw, mp_mixer** out) {
   MP_TRY(check_shape(m, n_blocks, heads, hidden));
   if (!w || !out) return arg_error("mp_mixer_create: null weights or out");
-  if (!(cap >= 0) || !std::isfinite(cap)) return arg_error("mp_mixer_create: cap must be finite and >= 0");
+  if (!(cap == 0.f || (cap >= 1e-3f && cap <= 1e4f))) return arg_error("mp_mixer_create: cap must be 0 or in 1e-3..1e4");
   if (nw != count(m, n_blocks, heads, hidden)) return arg_error("mp_mixer_create: weight count does not match");
   const int C = m->cfg.channels, dt = m->cfg.feat_dtype, es = dt == 1 ? 2 : 4;
   const int64_t CC = (int64_t)C * C, CF = (int64_t)C * hidden;

@@ -28,6 +28,9 @@ inline int check_width(const char* who, int32_t channels, int32_t feat_dtype) {
   return MP_OK;
 }
 
+// rows that a launch can cover (threads of a grid dimension are counted in 32 bits)
+constexpr int32_t kMaxRows = 1 << 26;
+
 #define MP_ROWS(who, name, p, ld, width, dt)                                                                     \
   do {                                                                                                           \
     if (!::mdmp::ops::rows_ok(p, ld, width, (dt) == 1 ? 2 : 4))                                                  \

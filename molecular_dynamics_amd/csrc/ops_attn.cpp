@@ -26,12 +26,14 @@ int splits_of(int64_t n, int64_t n_struct) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(2048, slots_of(n, n_struct)), n / n_struct / 128, 16}));
 }
 
+constexpr int32_t kMaxStruct = 1 << 25;  // with kMaxRows: slots of 64 threads in 32 bits
+
 // the kernels address the rows of one step by 32-bit offsets from a 64-bit base
 constexpr int64_t kMaxLd = 1 << 24;
 
 int check_shape(const char* who, int32_t n, int32_t channels, int32_t heads, int32_t dt) {
   MP_TRY(check_width(who, channels, dt));
-  if (n < 0) return arg_error(std::string(who) + ": n must be >= 0");
+  if (n < 0 || n > kMaxRows) return arg_error(std::string(who) + ": n must be in 0..2^26");
   const int dh = heads >= 1 && channels % heads == 0 ? channels / heads : 0;
   if (dh != 16 && dh != 32 && dh != 64) return arg_error(std::string(who) + ": channels / heads must be 16, 32 or 64");
   return MP_OK;
@@ -40,13 +42,12 @@ int check_shape(const char* who, int32_t n, int32_t channels, int32_t heads, int
 int attn_args(const char* who, const mp_attention_args* a, AttnArgs& A) {
   if (!a) return arg_error(std::string(who) + ": null arguments");
   MP_TRY(check_shape(who, a->n, a->channels, a->heads, a->feat_dtype));
-  if (a->n_struct < 0) return arg_error(std::string(who) + ": n_struct must be >= 0");
-  if (!(a->cap >= 0) || !std::isfinite(a->cap)) return arg_error(std::string(who) + ": cap must be finite and >= 0");
+  if (a->n_struct < 0 || a->n_struct > kMaxStruct) return arg_error(std::string(who) + ": n_struct must be in 0..2^25");
+  if (!cap_ok(a->cap)) return arg_error(std::string(who) + ": cap must be 0 or in 1e-3..1e4");
   if (!(a->box_L >= 0) || !std::isfinite(a->box_L))
     return arg_error(std::string(who) + ": box_L must be finite and >= 0 (0: open boundary)");
-  if ((a->pos != nullptr) != (a->slope != nullptr))
+  if (a->n > 0 && (a->pos != nullptr) != (a->slope != nullptr))  // no atoms: pos may be null
     return arg_error(std::string(who) + ": give both pos and slope, or neither");
-  if ((int64_t)a->n / 16 + a->n_struct > INT32_MAX) return arg_error(std::string(who) + ": too many structures");
   A = AttnArgs{};
   A.n = a->n, A.n_struct = a->n_struct;
   A.sptr = a->struct_ptr, A.pos = a->pos, A.slope = a->slope, A.mask = a->mask;
@@ -112,7 +113,8 @@ extern "C" int mp_structure_attention_saved(int32_t n, int32_t channels, int32_t
 
 extern "C" int mp_structure_attention_ws(int32_t n, int32_t n_struct, int32_t channels, int32_t heads, size_t* bytes) {
   MP_TRY(ops::check_shape("mp_structure_attention_ws", n, channels, heads, 0));
-  if (n_struct < 0 || !bytes) return arg_error("mp_structure_attention_ws: bad arguments");
+  if (n_struct < 0 || n_struct > ops::kMaxStruct || !bytes)
+    return arg_error("mp_structure_attention_ws: bad arguments");
   const int64_t S = n > 0 && n_struct > 0 ? ops::splits_of(n, n_struct) : 1;
   *bytes = S > 1 ? align_up(sizeof(float) * (size_t)(S * n * (channels + 2 * heads))) : 0;
   return MP_OK;
@@ -140,6 +142,7 @@ extern "C" int mp_structure_attention(const mp_attention_args* a, void* out, int
     A.p_out = (float*)ws;
     A.p_ml = A.p_out + (int64_t)A.splits * a->n * a->channels;
   }
+  if (out == a->q || out == a->k || out == a->v) return arg_error("mp_structure_attention: out must not be q, k or v");
   ProfScope p("structure_attention", st);
   return ops::launch(a, A, 0, st);
 }
@@ -147,7 +150,8 @@ extern "C" int mp_structure_attention(const mp_attention_args* a, void* out, int
 extern "C" int mp_structure_attention_bwd_ws(int32_t n, int32_t n_struct, int32_t channels, int32_t heads,
                                              size_t* bytes) {
   MP_TRY(ops::check_shape("mp_structure_attention_bwd_ws", n, channels, heads, 0));
-  if (n_struct < 0 || !bytes) return arg_error("mp_structure_attention_bwd_ws: bad arguments");
+  if (n_struct < 0 || n_struct > ops::kMaxStruct || !bytes)
+    return arg_error("mp_structure_attention_bwd_ws: bad arguments");
   Arena ar(nullptr, 0, true);
   ops::BwdWs w;
   ops::carve_bwd(ar, n, n_struct, channels, heads, w);
@@ -161,7 +165,7 @@ extern "C" int mp_structure_attention_bwd(const mp_attention_args* a, const void
                                           size_t ws_bytes, hipStream_t st) {
   ops::AttnArgs A;
   MP_TRY(ops::attn_args("mp_structure_attention_bwd", a, A));
-  if ((dpos || dslope) && !a->pos) return arg_error("mp_structure_attention_bwd: dpos and dslope need pos and slope");
+  if ((dpos || dslope) && !a->slope) return arg_error("mp_structure_attention_bwd: dpos and dslope need pos and slope");
   const int C = a->channels, H = a->heads, dt = a->feat_dtype;
   if (a->n == 0 || a->n_struct == 0) {  // no pair: the sum over nothing
     const ops::Segment none{0, H, dslope, false};
@@ -183,6 +187,10 @@ extern "C" int mp_structure_attention_bwd(const mp_attention_args* a, const void
   A.dsum = w.dsum, A.splits = w.splits;
   A.p_dq = w.dq, A.p_dk = w.dk, A.p_dv = w.dv, A.p_row = w.row, A.p_col = w.col;
   if (!ar.ok()) return arg_error("mp_structure_attention_bwd: workspace too small");
+  const void* const grads[3] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i)  // the column pass reads what the row pass read
+    for (const void* p : {a->q, a->k, a->v, dout, out, (const void*)grads[(i + 1) % 3]})
+      if (grads[i] == p) return arg_error("mp_structure_attention_bwd: dq, dk and dv must not be each other or an input");
   A.o = out, A.ldo = ldo, A.dout = dout, A.lddo = lddo;
   A.dq = dq, A.lddq = lddq, A.dk = dk, A.lddk = lddk, A.dv = dv, A.lddv = lddv;
   A.o32 = const_cast<float*>(dt == 1 ? saved : nullptr);

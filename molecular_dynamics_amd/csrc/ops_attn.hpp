@@ -1,4 +1,4 @@
-// Attention between all atoms of each structure: kernels (see ops_attn_api.hip for the calls).
+// Attention between all atoms of each structure: kernels (the calls: ops_attn.cpp).
 //
 // Scores are held in base 2: x = log2(e) (s - slope r), p = 2^(x - m).
 //
@@ -31,6 +31,9 @@
 
 namespace mdmp {
 namespace ops {
+
+// A cap far above the scores does nothing, and 1 - 2 / (e^2y + 1) would spend its digits on it
+inline bool cap_ok(float cap) { return cap == 0.f || (cap >= 1e-3f && cap <= 1e4f); }
 
 struct AttnArgs {
   int n, n_struct;
@@ -227,8 +230,7 @@ __device__ __forceinline__ f4 head_mma(f4 acc, const typename MF<T>::F (&a)[NC],
   return acc;
 }
 
-// per own atom and head: sum over the lane's values of a channel sum that is spread over lane
-// groups; every lane group gets the total
+// whether chunk ch of a row holds channels of head h in lane group g
 template <class T, int DH>
 __device__ __forceinline__ bool lane_in_head(int ch, int g, int h) {
   if constexpr (DH >= MF<T>::CK)
@@ -236,11 +238,6 @@ __device__ __forceinline__ bool lane_in_head(int ch, int g, int h) {
   else
     return 2 * ch + (g >> 1) == h;
 }
-
-template <class T, int C>
-struct AttnDims {
-  static constexpr int RS = C + lds_pad<T>();
-};
 
 // the channel chunks of head h: chunk_of(h) .. + chunks() - 1 (heads of half a chunk: the one it is in)
 template <class T, int DH>
@@ -270,10 +267,6 @@ template <class T>
 __device__ __forceinline__ float cap_of(float s, float sc) {
   if constexpr (sizeof(T) == 2) return rcp(ex2(s * sc) + 1.0f);
   return tanh_of<T>(s * sc);
-}
-template <class T>
-__device__ __forceinline__ float score(const Score& Z, float s, float b) {
-  return Z.cap ? fmaf(Z.k, cap_of<T>(s, Z.sc), b) : fmaf(s, Z.sc, b);
 }
 
 // The distances of a step's pairs: float32 in lengths, so that the slope in base 2 is rounded once;
@@ -309,8 +302,7 @@ template <class T, int C, int DH, int NW, bool SAVE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_FWD_WAVES)))
 void k_attn_fwd(AttnArgs A) {
   using M = MF<T>;
-  using D = AttnDims<T, C>;
-  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, EV = M::EV, NTH = 64 * NW;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = C + lds_pad<T>(), EV = M::EV, NTH = 64 * NW;
   constexpr bool BF = sizeof(T) == 2, KL = NW > 1;  // KL: keys through LDS as well
   constexpr int NB = KL ? 2 : 1;
   __shared__ __align__(16) T s_v[NB][CK * RS];
@@ -381,98 +373,98 @@ void k_attn_fwd(AttnArgs A) {
     const T *vs = s_v[b], *ks = s_k[KL ? b : 0];
     const u4* ps = s_pos[b];
     if (own0 < e) {  // a wave past the structure only keeps step
-    bool lv[NT][4];
-    f4 r[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      r[t] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) lv[t][q] = ((uint32_t)on >> (4 * g)) >> (16 * t + q) & 1;
-    }
-    if (dist) distances<T, NT>(r, A, own, ps, fix, g);
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      f4 x[NT];
+      bool lv[NT][4];
+      f4 r[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if constexpr (KL) {
+        r[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int ch = chunk_of<T, DH>(h); ch < chunk_of<T, DH>(h) + chunks<T, DH>(); ++ch)
-            kf[t][ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
-        }
-        x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
+        for (int q = 0; q < 4; ++q) lv[t][q] = ((uint32_t)on >> (4 * g)) >> (16 * t + q) & 1;
       }
-      const float sl = dist ? slope2<T>(A, A.slope[h]) : 0.f;
-      if (Z.cap) {
+      if (dist) distances<T, NT>(r, A, own, ps, fix, g);
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        f4 x[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if constexpr (KL) {
+#pragma unroll
+            for (int ch = chunk_of<T, DH>(h); ch < chunk_of<T, DH>(h) + chunks<T, DH>(); ++ch)
+              kf[t][ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
+          }
+          x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
+        }
+        const float sl = dist ? slope2<T>(A, A.slope[h]) : 0.f;
+        if (Z.cap) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[t][q] = cap_of<T>(x[t][q], Z.sc);
+        }
+        const float kk = Z.cap ? Z.k : Z.sc;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) x[t][q] = cap_of<T>(x[t][q], Z.sc);
-      }
-      const float kk = Z.cap ? Z.k : Z.sc;
+          for (int q = 0; q < 4; ++q) x[t][q] = fmaf(kk, x[t][q], fmaf(-sl, r[t][q], -m[h]));
+        if (part) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[t][q] = fmaf(kk, x[t][q], fmaf(-sl, r[t][q], -m[h]));
-      if (part) {
+            for (int q = 0; q < 4; ++q) x[t][q] = lv[t][q] ? x[t][q] : -INFINITY;
+        }
+        // the reference is raised only when a score passes it by 8 (p <= 2^8): the sums are exact
+        // relative to any reference, so most steps need no exchange and no rescale
+        float lm = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) lm = fmaxf(lm, fmaxf(fmaxf(x[t].x, x[t].y), fmaxf(x[t].z, x[t].w)));
+        if (__any(lm > thr[h])) {
+          const float mt = gmax(lm);
+          const bool none = thr[h] == -INFINITY;
+          const float d = none ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f), al = ex2(-d);
+          if (mt > -INFINITY) thr[h] = 8.0f;
+          m[h] += d;
+          if (!none) {
+            l[h] *= al;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) x[t][q] = lv[t][q] ? x[t][q] : -INFINITY;
-      }
-      // the reference is raised only when a score passes it by 8 (p <= 2^8): the sums are exact
-      // relative to any reference, so most steps need no exchange and no rescale
-      float lm = -INFINITY;
+            for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] *= al;
+          }
 #pragma unroll
-      for (int t = 0; t < NT; ++t) lm = fmaxf(lm, fmaxf(fmaxf(x[t].x, x[t].y), fmaxf(x[t].z, x[t].w)));
-      if (__any(lm > thr[h])) {
-        const float mt = gmax(lm);
-        const bool none = thr[h] == -INFINITY;
-        const float d = none ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f), al = ex2(-d);
-        if (mt > -INFINITY) thr[h] = 8.0f;
-        m[h] += d;
-        if (!none) {
-          l[h] *= al;
-#pragma unroll
-          for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] *= al;
+          for (int t = 0; t < NT; ++t) x[t] -= d;
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x[t] -= d;
-      }
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) x[t][q] = ex2(x[t][q]);
-        if constexpr (!BF) l[h].x += (x[t].x + x[t].y) + (x[t].z + x[t].w);
-      }
-      const typename M::F p = M::pack(x);
-      // bf16: the sum of the weights is a product with ones, off the VALU and of the same rounded
-      // weights that the values get
-      if constexpr (BF) l[h] = M::mma(l[h], ones, p);
-      if constexpr (BF && SAVE) {
-        // for a backward pass the weights enter as three bf16 values, p and its remainders (2^-27):
-        // o32, and with it dsum and the float32 gradients, keep float32's quality
-        f4 y[NT], z[NT];
-        M::unpack(p, y);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) y[t] = x[t] - y[t];
-        const typename M::F p2 = M::pack(y);
-        M::unpack(p2, z);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) z[t] = y[t] - z[t];
-        const typename M::F p3 = M::pack(z);
-        l[h] = M::mma(M::mma(l[h], ones, p3), ones, p2);
-#pragma unroll
-        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
-          const typename M::F f = ldt<RS>(vs, 0, 16 * ct, lane);
-          acc[ct] = M::mma(M::mma(M::mma(acc[ct], f, p3), f, p2), f, p);
+          for (int q = 0; q < 4; ++q) x[t][q] = ex2(x[t][q]);
+          if constexpr (!BF) l[h].x += (x[t].x + x[t].y) + (x[t].z + x[t].w);
         }
-      } else {
+        const typename M::F p = M::pack(x);
+        // bf16: the sum of the weights is a product with ones, off the VALU and of the same rounded
+        // weights that the values get
+        if constexpr (BF) l[h] = M::mma(l[h], ones, p);
+        if constexpr (BF && SAVE) {
+          // for a backward pass the weights enter as three bf16 values, p and its remainders (2^-27):
+          // o32, and with it dsum and the float32 gradients, keep float32's quality
+          f4 y[NT], z[NT];
+          M::unpack(p, y);
 #pragma unroll
-        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct)
-          acc[ct] = M::mma(acc[ct], ldt<RS>(vs, 0, 16 * ct, lane), p);
+          for (int t = 0; t < NT; ++t) y[t] = x[t] - y[t];
+          const typename M::F p2 = M::pack(y);
+          M::unpack(p2, z);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) z[t] = y[t] - z[t];
+          const typename M::F p3 = M::pack(z);
+          l[h] = M::mma(M::mma(l[h], ones, p3), ones, p2);
+#pragma unroll
+          for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
+            const typename M::F f = ldt<RS>(vs, 0, 16 * ct, lane);
+            acc[ct] = M::mma(M::mma(M::mma(acc[ct], f, p3), f, p2), f, p);
+          }
+        } else {
+#pragma unroll
+          for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct)
+            acc[ct] = M::mma(acc[ct], ldt<RS>(vs, 0, 16 * ct, lane), p);
+        }
       }
-    }
     }
     on = on_n;
     if constexpr (KL) {
@@ -568,8 +560,7 @@ __device__ __forceinline__ void add_pairs(float (&p)[3], const f4 (&wgt)[NT], co
 template <class T, int C, int DH, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BWD_WAVES))) void k_attn_row(AttnArgs A) {
   using M = MF<T>;
-  using D = AttnDims<T, C>;
-  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, EV = M::EV, NTH = 64 * NW;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = C + lds_pad<T>(), EV = M::EV, NTH = 64 * NW;
   constexpr bool VL = NW > 1;  // values through LDS as well
   constexpr int NB = VL ? 2 : 1;
   __shared__ __align__(16) T s_k[NB][CK * RS];
@@ -660,41 +651,41 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
     const T *ks = s_k[b], *vs = s_v[VL ? b : 0];
     const u4* ps = s_pos[b];
     if (own0 < e) {  // a wave past the structure only keeps step
-    f4 r[NT], wgt[NT];
+      f4 r[NT], wgt[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
-    if (dist) distances<T, NT>(r, A, own, ps, fix, g);
+      for (int t = 0; t < NT; ++t) wgt[t] = r[t] = f4{0.f, 0.f, 0.f, 0.f};
+      if (dist) distances<T, NT>(r, A, own, ps, fix, g);
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const float sl = dist ? A.slope[h] : 0.f, sl2 = slope2<T>(A, sl);
-      f4 ds[NT];
+      for (int h = 0; h < H; ++h) {
+        const float sl = dist ? A.slope[h] : 0.f, sl2 = slope2<T>(A, sl);
+        f4 ds[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        typename M::F kf[NC];
+        for (int t = 0; t < NT; ++t) {
+          typename M::F kf[NC];
 #pragma unroll
-        for (int ch = chunk_of<T, DH>(h); ch < chunk_of<T, DH>(h) + chunks<T, DH>(); ++ch) {
-          kf[ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
-          if constexpr (VL) vf[t][ch] = *(const typename M::F*)(vs + (16 * t + i) * RS + ch * CK + EV * g);
-        }
-        const f4 z = f4{0.f, 0.f, 0.f, 0.f};
-        const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
-        f4 p, dl;
-        const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
-        pair_grad<T>(Z, dist, x, dp, r[t], sl2, L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl,
-                     ds[t]);
-        if (dist) {
+          for (int ch = chunk_of<T, DH>(h); ch < chunk_of<T, DH>(h) + chunks<T, DH>(); ++ch) {
+            kf[ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
+            if constexpr (VL) vf[t][ch] = *(const typename M::F*)(vs + (16 * t + i) * RS + ch * CK + EV * g);
+          }
+          const f4 z = f4{0.f, 0.f, 0.f, 0.f};
+          const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
+          f4 p, dl;
+          const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
+          pair_grad<T>(Z, dist, x, dp, r[t], sl2, L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl,
+                       ds[t]);
+          if (dist) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
-            dsl[h] = fmaf(-dl[q], r[t][q], dsl[h]);
+            for (int q = 0; q < 4; ++q) {
+              wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
+              dsl[h] = fmaf(-dl[q], r[t][q], dsl[h]);
+            }
           }
         }
-      }
-      const typename M::F pd = M::pack(ds);
+        const typename M::F pd = M::pack(ds);
 #pragma unroll
-      for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] = M::mma(acc[ct], ldt<RS>(ks, 0, 16 * ct, lane), pd);
-    }
-    if (A.dpos) add_pairs<NT>(px, wgt, r, own, ps, fix, g);
+        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] = M::mma(acc[ct], ldt<RS>(ks, 0, 16 * ct, lane), pd);
+      }
+      if (A.dpos) add_pairs<NT>(px, wgt, r, own, ps, fix, g);
     }
     on = on_n;
     if constexpr (VL) {
@@ -740,8 +731,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
 template <class T, int C, int DH, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BWD_WAVES))) void k_attn_col(AttnArgs A) {
   using M = MF<T>;
-  using D = AttnDims<T, C>;
-  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = D::RS, EV = M::EV, NTH = 64 * NW;
+  constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = C + lds_pad<T>(), EV = M::EV, NTH = 64 * NW;
   constexpr int NB = NW > 1 ? 2 : 1;
   __shared__ __align__(16) T s_q[NB][CK * RS];
   __shared__ __align__(16) T s_o[NB][CK * RS];

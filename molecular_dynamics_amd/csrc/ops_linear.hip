@@ -386,7 +386,7 @@ int launch_linear(const LinArgs& A0, int C, int what, hipStream_t st) {
 
 int check_linear(const char* who, int32_t n, int32_t in, int32_t out, int32_t dt, int32_t act) {
   MP_TRY(check_width(who, in, dt));
-  if (n < 0) return arg_error(std::string(who) + ": n must be >= 0");
+  if (n < 0 || n > kMaxRows) return arg_error(std::string(who) + ": n must be in 0..2^26");
   if (out < 16 || out > 1024 || out % 16) return arg_error(std::string(who) + ": out must be a multiple of 16 in 16..1024");
   if (act < MP_ACT_NONE || act > MP_ACT_SIGMOID) return arg_error(std::string(who) + ": unknown activation");
   return MP_OK;
@@ -413,6 +413,7 @@ extern "C" int mp_linear(int32_t n, int32_t in, int32_t out, int32_t dt, int32_t
   MP_TRY(ops::check_linear("mp_linear", n, in, out, dt, act));
   if (n == 0) return MP_OK;
   if (!x || !w || !y) return arg_error("mp_linear: null x, w or y");
+  if (x == y) return arg_error("mp_linear: y must not be x");
   if ((uintptr_t)w & 15) return arg_error("mp_linear: w must be 16-byte aligned");
   MP_ROWS("mp_linear", "x", x, ldx, in, dt);
   MP_ROWS("mp_linear", "y", y, ldy, out, dt);
@@ -438,6 +439,7 @@ extern "C" int mp_linear_bwd(int32_t n, int32_t in, int32_t out, int32_t dt, int
   MP_TRY(ops::check_linear("mp_linear_bwd", n, in, out, dt, act));
   if (n > 0) {
     if (!x || !w || !dy) return arg_error("mp_linear_bwd: null x, w or dy");
+    if (dx && (dx == x || dx == dy)) return arg_error("mp_linear_bwd: dx must not be x or dy");
     if ((uintptr_t)w & 15) return arg_error("mp_linear_bwd: w must be 16-byte aligned");
     MP_ROWS("mp_linear_bwd", "x", x, ldx, in, dt);
     MP_ROWS("mp_linear_bwd", "dy", dy, lddy, out, dt);

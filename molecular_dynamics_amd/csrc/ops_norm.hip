@@ -290,7 +290,7 @@ int reduce_rows(const float* part, int64_t S, int64_t ldp, const Segment* seg, i
 static int check_norm(const mp_norm_args* a, ops::NormPtrs& A) {
   if (!a) return arg_error("mp_norm_block: null arguments");
   MP_TRY(ops::check_width("mp_norm_block", a->channels, a->feat_dtype));
-  if (a->n < 0) return arg_error("mp_norm_block: n must be >= 0");
+  if (a->n < 0 || a->n > ops::kMaxRows) return arg_error("mp_norm_block: n must be in 0..2^26");
   // below that the hardware's reciprocal square root takes a zero row to infinity
   if (!(a->eps >= 1e-30f) || !std::isfinite(a->eps)) return arg_error("mp_norm_block: eps must be finite and >= 1e-30");
   if (((uintptr_t)a->scale | (uintptr_t)a->w_post | (uintptr_t)a->w_pre) & 15)
@@ -332,7 +332,7 @@ extern "C" int mp_norm_block(const mp_norm_args* a, void* y, int64_t ldy, void* 
 
 extern "C" int mp_norm_block_bwd_ws(int32_t n, int32_t channels, int32_t feat_dtype, size_t* bytes) {
   MP_TRY(ops::check_width("mp_norm_block_bwd_ws", channels, feat_dtype));
-  if (n < 0 || !bytes) return arg_error("mp_norm_block_bwd_ws: bad arguments");
+  if (n < 0 || n > ops::kMaxRows || !bytes) return arg_error("mp_norm_block_bwd_ws: bad arguments");
   *bytes = align_up(sizeof(float) * 3 * channels * (size_t)std::max(1, ops::norm_blocks(n, channels, feat_dtype == 1)));
   return MP_OK;
 }

@@ -9,8 +9,8 @@ from molecular_dynamics_amd import mdmp
 
 L = mdmp._lib
 P = 0x1000          # an aligned address; never dereferenced by a refused call
+Y = 0x2000
 ODD = 0x1008        # 8-byte aligned only
-BIG = 1 << 40
 
 
 def refused(rc, *words):
@@ -19,12 +19,14 @@ def refused(rc, *words):
     assert all(w in msg for w in words), msg
 
 
-def lin(n=8, k=64, o=64, dt=0, act=0, x=P, ldx=64, w=P, bias=None, res=None, ldr=64, y=P, ldy=64):
+def lin(n=8, k=64, o=64, dt=0, act=0, x=P, ldx=64, w=P, bias=None, res=None, ldr=64, y=Y, ldy=64):
     return L.mp_linear(n, k, o, dt, act, x, ldx, w, bias, res, ldr, y, ldy, None)
 
 
 def test_linear_refusals():
     refused(lin(n=-1), "n must")
+    refused(lin(n=2 ** 26 + 1), "n must")
+    refused(lin(y=P), "y must not be x")
     refused(lin(k=48), "channels")
     refused(lin(k=16, dt=1), "16 channels")
     refused(lin(dt=2), "feat_dtype")
@@ -59,7 +61,7 @@ def test_linear_bwd_refusals():
     refused(bwd(dx=ODD, dw=None), "rows of dx")
 
 
-def ffn(n=8, c=64, f=64, dt=0, act=1, x=P, ldx=64, g=P, u=P, d=P, y=P, ldy=64):
+def ffn(n=8, c=64, f=64, dt=0, act=1, x=P, ldx=64, g=P, u=P, d=P, y=Y, ldy=64):
     return L.mp_gated_ffn(n, c, f, dt, act, x, ldx, g, u, d, None, 0, y, ldy, None)
 
 
@@ -70,6 +72,7 @@ def test_gated_ffn_refusals():
         refused(ffn(f=f), "hidden")
     refused(ffn(act=0), "act")
     refused(ffn(x=None), "null")
+    refused(ffn(y=P), "y must not be x")
     refused(ffn(d=None), "null")
     refused(ffn(u=ODD), "aligned")
     refused(ffn(ldx=62), "rows of x")
@@ -132,13 +135,14 @@ def test_structure_attention_refusals():
     refused(attn(c=40), "channels")
     refused(attn(n=-1), "n must")
     refused(attn(ns=-1), "n_struct")
-    for cap in (-1.0, float("nan"), float("inf")):
+    for cap in (-1.0, float("nan"), float("inf"), 1e-4, 1e5):
         refused(attn(cap=cap), "cap")
     for box in (-1.0, float("nan"), float("inf")):
         refused(attn(box=box), "box_L")
     refused(attn(pos=P), "both pos and slope")
     refused(attn(slope=P), "both pos and slope")
-    refused(attn(n=2 ** 31 - 1, ns=2 ** 31 - 1), "too many structures")
+    refused(attn(n=2 ** 26 + 1), "n must")
+    refused(attn(ns=2 ** 25 + 1), "n_struct")
     refused(attn(sp=None), "struct_ptr")
     refused(attn(k=None), "null")
     refused(attn(ldv=60), "row")

@@ -296,6 +296,211 @@ def test_structure_attention_coincident_atoms():
         R.check(name, g[name], *ref[name])
 
 
+def test_structure_attention_large_cap():
+    """cap = 200 in bf16: the cap's own arithmetic error grows with it (in the bound)"""
+    n, q, k, v, do, sptr, kw = structure_case([90, 33], 64, 2, "bf16", True, 200.0, None, 0.0, 31)
+    ref = R.attention(q, k, v, sptr, 2, dout=do, save=True, **kw)
+    out, saved = m().structure_attention(q, k, v, sptr, 2, save=True, **kw)
+    g = m().structure_attention_bwd(q, k, v, sptr, 2, out, saved, do, **kw)
+    R.check("out", out, *ref["out"])
+    for name in ("dq", "dk", "dv", "dpos", "dslope"):
+        R.check(name, g[name], *ref[name])
+
+
+# ------------------------------------------------------------------------------ how they are called
+def _one_of_each(dt, seed, n=700, c=64, sizes=(300, 21, 0, 350)):
+    """Closures over fixed inputs: every operator and its backward, as lists of tensors."""
+    g, t = gen(seed), DT[dt]
+    x, b, dy, gate = (randn(g, n, c, dtype=t) for _ in range(4))
+    w, wg, wu, wd = (randn(g, *s, scale=0.1, dtype=t) for s in ((96, c), (128, c), (128, c), (c, 128)))
+    bias, sc, wp, wq = randn(g, 96), randn(g, c), randn(g, c), randn(g, c)
+    dyw = randn(g, n, 96, dtype=t)
+    n2, q, k, v, do, sptr, kw = structure_case(list(sizes), c, 2, dt, True, 5.0, 0.8, 0.0, seed, n - sum(sizes))
+    nk = dict(scale=sc, gate=gate, w_post=wp, w_pre=wq)
+
+    def attn():
+        out = torch.zeros_like(q)
+        out, saved = m().structure_attention(q, k, v, sptr, 2, out=out, save=True, **kw)
+        g = [torch.zeros_like(q) for _ in range(3)] + [torch.zeros(n, 3, device="cuda")]
+        gr = m().structure_attention_bwd(q, k, v, sptr, 2, out, saved, do, dq=g[0], dk=g[1], dv=g[2], dpos=g[3], **kw)
+        return [out, *g, gr["dslope"]]
+    return {
+        "linear": lambda: [m().linear(x, w, bias=bias, act="silu"), *m().linear_bwd(x, w, dyw, bias=bias, act="silu")],
+        "ffn": lambda: [m().gated_ffn(x, wg, wu, wd), *m().gated_ffn_bwd(x, wg, wu, wd, dy)],
+        "norm": lambda: [*m().norm_block(x, b, **nk), *[v for v in m().norm_block_bwd(x, b, dy, du=dy, **nk).values()]],
+        "attention": attn,
+    }
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_repeats_streams_and_graphs_give_the_same_bits(dt):
+    """A second call, a call on another stream, and replays of a captured call (with the program's
+    own work between them) give the bits of the first call."""
+    for name, f in _one_of_each(dt, 77).items():
+        print(f"{name} {dt}", flush=True)
+        ref = [t.clone() for t in f()]
+        torch.cuda.synchronize()
+        same = lambda got: all(torch.equal(a, b) for a, b in zip(ref, got))  # noqa: E731
+        assert same(f())
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = f()
+        torch.cuda.current_stream().wait_stream(side)
+        assert same(got), (name, "another stream")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = f()
+        for k in range(3):
+            for h in held:
+                h.fill_(3)
+            graph.replay()
+            f()                       # the program's own work beside the replays
+            torch.cuda.synchronize()
+            assert same(held), (name, "replay", k)
+
+
+def test_two_calls_at_once():
+    """The same operators enqueued on two streams at a time, each with its own scratch, keep their bits."""
+    a, b = _one_of_each("bf16", 78), _one_of_each("f32", 79, n=900, sizes=(800, 40))
+    for name in a:
+        ra, rb = [t.clone() for t in a[name]()], [t.clone() for t in b[name]()]
+        torch.cuda.synchronize()
+        s = [torch.cuda.Stream() for _ in range(2)]
+        got = [None, None]
+        for st, k, f in ((s[0], 0, a[name]), (s[1], 1, b[name])):
+            with torch.cuda.stream(st):
+                for _ in range(3):
+                    got[k] = f()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(ra, got[0])), name
+        assert all(torch.equal(x, y) for x, y in zip(rb, got[1])), name
+
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that the last ones lie past 2^32 elements."""
+    g, n, ld = gen(9), 530, 1 << 23
+    big = torch.empty(n * ld, dtype=torch.bfloat16, device="cuda").as_strided((n, ld), (ld, 1))
+    assert (n - 1) * ld > 2 ** 32
+    x, y = big[:, :64], big[:, 128:192]
+    x.copy_(randn(g, n, 64, dtype=torch.bfloat16))
+    xc = x.contiguous()
+    w, wg = randn(g, 64, 64, scale=0.1, dtype=torch.bfloat16), randn(g, 96, 64, scale=0.1, dtype=torch.bfloat16)
+    wd, s = randn(g, 64, 96, scale=0.1, dtype=torch.bfloat16), randn(g, 64)
+    same = lambda got: torch.equal(got.contiguous(), ref)  # noqa: E731
+    ref = m().linear(xc, w, residual=xc)
+    assert same(m().linear(x, w, residual=x, out=y))
+    ref = m().gated_ffn(xc, wg, wg, wd)
+    assert same(m().gated_ffn(x, wg, wg, wd, out=y))
+    ref = m().norm_block(xc, xc, gate=xc, w_post=s)[0]
+    assert same(m().norm_block(x, x, gate=x, w_post=s, out=y)[0])
+    pairs = [(m().linear_bwd(xc, w, xc), m().linear_bwd(x, w, x)),
+             (m().gated_ffn_bwd(xc, wg, wg, wd, xc), m().gated_ffn_bwd(x, wg, wg, wd, x)),
+             (list(m().norm_block_bwd(xc, xc, xc, w_post=s).values()), list(m().norm_block_bwd(x, x, x, w_post=s).values()))]
+    for a, b in pairs:
+        assert all((u is None and v is None) or torch.equal(u, v) for u, v in zip(a, b))
+    for sizes in ([n], [25, 30] * 9 + [35]):   # long structures, short ones
+        sptr = torch.tensor([0, *torch.tensor(sizes).cumsum(0)], dtype=torch.int32, device="cuda")
+        assert int(sptr[-1]) == n
+        kw = dict(pos=randn(g, n, 3, scale=3.0), slope=torch.tensor([0.2, 0.4], device="cuda"))
+        ref, saved = m().structure_attention(xc, xc, xc, sptr, 2, save=True, **kw)
+        got, saved2 = m().structure_attention(x, x, x, sptr, 2, save=True, out=y, **kw)
+        assert same(got) and torch.equal(saved, saved2)
+        ga = m().structure_attention_bwd(xc, xc, xc, sptr, 2, ref, saved, xc, **kw)
+        d = [big[:, 256 + 64 * k:320 + 64 * k] for k in range(3)]
+        gb = m().structure_attention_bwd(x, x, x, sptr, 2, y, saved, x, dq=d[0], dk=d[1], dv=d[2], **kw)
+        assert all(torch.equal(ga[k], gb[k].contiguous()) for k in ga)
+
+
+def test_bf16_bits_as_int16():
+    """Rows as int16 bit patterns (the feature tensors' form) give the same bits as bfloat16."""
+    g = gen(5)
+    x, w = randn(g, 100, 64, dtype=torch.bfloat16), randn(g, 48, 64, dtype=torch.bfloat16)
+    y = m().linear(x, w)
+    y2 = m().linear(x.view(torch.int16), w.view(torch.int16))
+    assert y2.dtype == torch.int16 and torch.equal(y2.view(torch.bfloat16), y)
+
+
+def test_scalar_rows_of_a_feature_tensor():
+    """h[:, 0] of a [n, K, C] feature tensor in place: the other rows stay as they are."""
+    g = gen(6)
+    h = randn(g, 333, 9, 128)
+    before = h.clone()
+    b, sc, wp = randn(g, 333, 128), randn(g, 128), randn(g, 128)
+    y, u = m().norm_block(h[:, 0], b, scale=sc, w_post=wp, w_pre=wp, out=h[:, 0])
+    ref = R.norm(before[:, 0], b, sc, None, wp, wp, 1e-6, None, None)
+    R.check("y", h[:, 0], *ref["y"])
+    R.check("u", u, *ref["u"])
+    assert torch.equal(h[:, 1:], before[:, 1:])
+
+
+def test_no_rows_and_no_structures():
+    t = torch.float32
+    x, w = torch.empty(0, 64, device="cuda"), torch.ones(32, 64, device="cuda")
+    b = torch.ones(32, device="cuda")
+    assert m().linear(x, w, bias=b).shape == (0, 32)
+    dx, dw, db = m().linear_bwd(x, w, torch.empty(0, 32, device="cuda"), bias=b)
+    assert dx.shape == (0, 64) and bool((dw == 0).all()) and bool((db == 0).all())
+    wg, wd = torch.ones(96, 64, device="cuda"), torch.ones(64, 96, device="cuda")
+    assert m().gated_ffn(x, wg, wg, wd).shape == (0, 64)
+    g = m().gated_ffn_bwd(x, wg, wg, wd, x)
+    assert g[0].shape == (0, 64) and all(bool((v == 0).all()) for v in g[1:])
+    s = torch.ones(64, device="cuda")
+    y, u = m().norm_block(x, x, scale=s, w_post=s, w_pre=s)
+    assert y.shape == u.shape == (0, 64)
+    g = m().norm_block_bwd(x, x, x, du=x, scale=s, w_post=s, w_pre=s)
+    assert all(bool((g[k] == 0).all()) for k in ("dscale", "dw_post", "dw_pre"))
+    kw = dict(pos=torch.empty(0, 3, device="cuda"), slope=torch.ones(2, device="cuda"))
+    for n, sp in ((0, [0]), (0, [0, 0, 0]), (5, [0]), (5, [0, 0])):
+        q = torch.randn(n, 64, device="cuda", dtype=t)
+        kw["pos"] = torch.zeros(n, 3, device="cuda")
+        sptr = torch.tensor(sp, dtype=torch.int32, device="cuda")
+        keep, *d = [torch.full((n, 64), 2.0, device="cuda") for _ in range(4)]
+        out, saved = m().structure_attention(q, q, q, sptr, 2, out=keep, save=True, **kw)
+        g = m().structure_attention_bwd(q, q, q, sptr, 2, out, saved, q, dq=d[0], dk=d[1], dv=d[2], **kw)
+        assert all(bool((v == 2).all()) for v in (keep, *d)) and bool((g["dslope"] == 0).all())
+
+
+def test_python_refusals():
+    x, w = torch.zeros(8, 64, device="cuda"), torch.zeros(32, 64, device="cuda")
+    sp = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: m().linear(x.cpu(), w), lambda: m().linear(x, w.bfloat16()), lambda: m().linear(x.half(), w.half()),
+        lambda: m().linear(x, w, act="gelu"), lambda: m().linear(x, w, bias=torch.zeros(31, device="cuda")),
+        lambda: m().linear(x, w, residual=torch.zeros(7, 32, device="cuda")), lambda: m().linear(x.t().contiguous().t(), w),
+        lambda: m().linear(x, w[:, :32]), lambda: m().linear(x[0], w),
+        lambda: m().gated_ffn(x, w, w[:16], w.t().contiguous()),
+        lambda: m().norm_block(x, x[:4]), lambda: m().norm_block(x, x, scale=torch.ones(64)),
+        lambda: m().structure_attention(x, x, x, sp.long(), 2), lambda: m().structure_attention(x, x[:4], x, sp, 2),
+        lambda: m().structure_attention(x, x, x, sp, 2, mask=torch.ones(7, dtype=torch.bool, device="cuda")),
+    ]
+    for k, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            print("not refused:", k, flush=True)
+    odd = [
+        lambda: m().linear(torch.zeros(8, 66, device="cuda")[:, :64], w),           # row stride of 264 bytes
+        lambda: m().linear(torch.zeros(8, 65, device="cuda")[:, 1:], w),            # rows not 16-byte aligned
+        lambda: m().linear(x[:1].expand(8, 64), w),                                 # row stride 0
+        lambda: m().gated_ffn(x, w, w, w.t().contiguous(), act="none"),
+        lambda: m().structure_attention(x, x, x, sp, 8), lambda: m().structure_attention(x, x, x, sp, 2, cap=-1.0),
+        lambda: m().structure_attention(x, x, x, sp, 2, pos=torch.zeros(8, 3, device="cuda")),
+    ]
+    t = torch.zeros(64, 64, device="cuda")
+    sv = torch.zeros(8 * 2, device="cuda")
+    odd += [  # outputs that another part of the call still reads
+        lambda: m().linear(x, t, out=x), lambda: m().gated_ffn(x, t, t, t, out=x),
+        lambda: m().structure_attention(x, x, x, sp, 2, out=x),
+        lambda: m().structure_attention_bwd(x, x, x, sp, 2, x, sv, x, dq=x),
+        lambda: m().structure_attention_bwd(x, x, x, sp, 2, x, sv, x, dk=t[:8], dv=t[:8]),
+    ]
+    for k, f in enumerate(odd):
+        with pytest.raises(m().MPError) as e:
+            f()
+            print("not refused:", k, flush=True)
+        assert e.value.code == m().MP_ERR_ARG
+
+
 # ------------------------------------------------------------------------------ gradients as differences
 def test_gradients_against_differences():
     """<gradient, direction> against central differences of the float64 definitions along the

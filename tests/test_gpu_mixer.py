@@ -101,3 +101,53 @@ def test_mixer_errors():
     with pytest.raises(mdmp.MPError) as e:
         mdmp.energy_forces_mixer(mdmp.Model(cfg2, w2), mixer, g, dev(sptr))
     assert e.value.code == mdmp.MP_ERR_ARG
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_captured_evaluation_replays(bf16):
+    """The whole evaluation captured once and replayed, with other work between, gives the same bits."""
+    import ctypes
+    import torch
+    from molecular_dynamics_amd import mdmp
+    pos, sp, sptr, cfg, w = MC.batch(12, 1, 70, 54, 64, 2, 4, 2, bf16)
+    mw = MC.weights(64, 2, 2, 96, 66)
+    g = mdmp.build_neighbors_batched(dev(pos), dev(sp), dev(sptr), cfg.cutoff, 0.5)
+    model = mdmp.Model(cfg, w)
+    mixer = mdmp.Mixer(model, 2, 2, 96, mw, cap=4.0)
+    ptr = dev(sptr)
+    E, F = mdmp.energy_forces_mixer(model, mixer, g, ptr)
+    nb = ctypes.c_size_t(0)
+    mdmp._check(mdmp._lib.mp_energy_forces_mixer_ws(model.h, mixer.h, g.n, len(sptr) - 1, g.n_edges,
+                                                    ctypes.byref(nb)), "ws")
+    ws = mdmp._ws(nb.value)
+    e2, f2 = torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(g.n, 3, device="cuda")
+    gs = g.struct()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mdmp._check(mdmp._lib.mp_energy_forces_mixer(model.h, mixer.h, ctypes.byref(gs), ptr.data_ptr(), len(sptr) - 1,
+                                                     None, e2.data_ptr(), f2.data_ptr(), None, ws.data_ptr(),
+                                                     ws.numel(), mdmp._stream()), "mp_energy_forces_mixer")
+    for _ in range(3):
+        e2.fill_(1)
+        f2.fill_(1)
+        graph.replay()
+        mdmp.energy_forces(model, g)
+        torch.cuda.synchronize()
+        assert float(e2.item()) == E and torch.equal(f2, F)
+
+
+def test_structures_that_do_not_cover_the_atoms_are_refused():
+    import torch
+    from molecular_dynamics_amd import mdmp
+    pos, sp, sptr, cfg, w = MC.batch(6, 2, 20, 55, 16, 1, 2, 1, False)
+    g = mdmp.build_neighbors_batched(dev(pos), dev(sp), dev(sptr), cfg.cutoff, 0.5)
+    model = mdmp.Model(cfg, w)
+    mixer = mdmp.Mixer(model, 1, 1, 64, MC.weights(16, 1, 1, 64, 67))
+    n = len(pos)
+    E, F = mdmp.energy_forces_mixer(model, mixer, g, dev(sptr))
+    for bad in ([0, n - 1], [1, n], [0, n + 1], [0, n // 2 + 1, n // 2, n]):
+        with pytest.raises(mdmp.MPError) as e:
+            mdmp.energy_forces_mixer(model, mixer, g, torch.tensor(bad, dtype=torch.int32, device="cuda"))
+        assert e.value.code == mdmp.MP_ERR_ARG
+    E2, F2 = mdmp.energy_forces_mixer(model, mixer, g, dev(sptr))
+    assert E2 == E and torch.equal(F2, F)
