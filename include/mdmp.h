@@ -376,7 +376,7 @@ typedef struct {
 /* ws: needed where mp_structure_attention_ws reports bytes (few long structures, whose
  * other side is split over blocks); 0 bytes: may be null.
  * saved (nullable): float32 of mp_structure_attention_saved count, what the backward
- * pass needs of this call (with it, bf16 attention weights enter the sum unrounded, so
+ * pass needs of this call (with it, bf16 weights are formed and summed more exactly, so
  * out may differ from that of a call without it in its last bit). */
 int mp_structure_attention_saved(int32_t n, int32_t channels, int32_t heads, int32_t feat_dtype, int64_t* floats);
 int mp_structure_attention_ws(int32_t n, int32_t n_struct, int32_t channels, int32_t heads, size_t* bytes);

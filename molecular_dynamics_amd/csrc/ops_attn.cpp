@@ -59,6 +59,8 @@ int attn_args(const char* who, const mp_attention_args* a, AttnArgs& A) {
   A.cap = a->cap;
   A.splits = 1;
   if (a->n == 0 || a->n_struct == 0) return MP_OK;
+  const int size = std::max(1, a->n / a->n_struct), lsub = 31 - __builtin_clz(size);
+  A.lsub = (float)lsub, A.p_scale = std::ldexp(1.0f, -lsub);
   if (!a->struct_ptr) return arg_error(std::string(who) + ": null struct_ptr");
   if (!a->q || !a->k || !a->v) return arg_error(std::string(who) + ": null q, k or v");
   const int C = a->channels, es = a->feat_dtype == 1 ? 2 : 4;

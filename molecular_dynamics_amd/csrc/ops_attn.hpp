@@ -46,6 +46,11 @@ struct AttnArgs {
   double to_fix;    // 2^32 / box_L, 0: open
   float unit;       // length of one unit of a coordinate difference (box_L / 2^32, or 1)
   float scale;      // 1 / sqrt(d)
+  // log-sums are held less lsub, about log2 of a structure's size, where it would take their digits:
+  // with 4,096 atoms they are near 12, x - lse is rounded to 2^-21 before the exponential, and dpos
+  // lost half of float32's quality (3.5e-6 off).  The backward passes' weights are then 2^lsub p, and
+  // p_scale = 2^-lsub enters their results once.
+  float lsub, p_scale;
   float cap;        // 0: none
   void *out, *dq, *dk, *dv;
   float *lse, *o32;    // saved: [n][H] base-2 log-sum, [n][C] unrounded output (bf16 only)
@@ -85,15 +90,28 @@ __device__ __forceinline__ void diff(const P3& own, const u4& o, bool fix, float
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// tanh(y).  1 - 2 / (e^2y + 1) has an absolute error of about 1e-7; float32 features take the
-// series (to y^9, 8e-9 at the border) where that is no longer small against y.
-template <class T>
-__device__ __forceinline__ float tanh_of(float y) {
-  const float e = 1.0f - 2.0f * rcp(ex2(y * (2.0f * kLog2e)) + 1.0f);
-  if constexpr (sizeof(T) == 2) return e;
-  const float w = y * y;
-  const float p = fmaf(w, fmaf(w, fmaf(w, fmaf(w, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
-  return fabsf(y) < 0.25f ? y * p : e;
+// tanh of N values.  Up to 1 the continued fraction y (945 + 105 y^2 + y^4) / (945 + 420 y^2 + 15 y^4)
+// (6e-8 off at 1, relative to y below), which keeps the digits of small values; beyond it, where a wave
+// has any such value, 1 - 2 / (e^2y + 1), whose error of about 1e-7 is absolute.
+template <int N>
+__device__ __forceinline__ void tanh_all(float (&y)[N]) {
+  float t[N], most = 0.f;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const float w = y[q] * y[q];
+    t[q] = y[q] * fmaf(w, fmaf(w, 1.0f / 945.0f, 1.0f / 9.0f), 1.0f) *
+           rcp(fmaf(w, fmaf(w, 1.0f / 63.0f, 4.0f / 9.0f), 1.0f));
+    most = fmaxf(most, fabsf(y[q]));
+  }
+  if (__any(most > 1.0f)) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const float e = 1.0f - 2.0f * rcp(ex2(y[q] * (2.0f * kLog2e)) + 1.0f);
+      t[q] = fabsf(y[q]) > 1.0f ? e : t[q];
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) y[q] = t[q];
 }
 
 // a value that is equal in every lane, as a scalar
@@ -249,24 +267,31 @@ constexpr int chunk_of(int h) {
   return DH >= MF<T>::CK ? h * (DH / MF<T>::CK) : h / 2;
 }
 
-// Scores in the reference of a lane's query: x = log2(e) s + b.  bf16 features: tanh(y) =
-// 1 - 2 / (e^2y + 1), whose leading 1 is the same for every key and left out of x (and so out of
-// the saved log-sums: the backward passes form x by this function too).
+// Scores in the reference of a lane's query: x = log2(e) s + b.  A forward pass over bf16 features
+// that nothing follows (FAST) takes tanh(y) = 1 - 2 / (e^2y + 1), whose leading 1 is the same for
+// every key and left out of x: one product and sum less, but x is then off by cap times 2e-7, which
+// the float32 gradients of a training pass would show (dpos 1e-6 off instead of 2e-7 at cap 20).
 struct Score {
   float sc, k;  // x = k f(sc S) + b
   bool cap;
 };
-template <class T>
+template <bool FAST>
 __device__ __forceinline__ Score score_of(const AttnArgs& A) {
   if (!(A.cap > 0)) return Score{A.scale * kLog2e, 1.0f, false};
-  if constexpr (sizeof(T) == 2) return Score{A.scale / A.cap * (2.0f * kLog2e), -2.0f * A.cap * kLog2e, true};
+  if constexpr (FAST) return Score{A.scale / A.cap * (2.0f * kLog2e), -2.0f * A.cap * kLog2e, true};
   return Score{A.scale / A.cap, A.cap * kLog2e, true};
 }
-// the capped part of x over k: bf16 1 / (e^2y + 1) = (1 - tanh y) / 2, float32 tanh y
-template <class T>
-__device__ __forceinline__ float cap_of(float s, float sc) {
-  if constexpr (sizeof(T) == 2) return rcp(ex2(s * sc) + 1.0f);
-  return tanh_of<T>(s * sc);
+// the capped part of x over k: tanh y; FAST 1 / (e^2y + 1) = (1 - tanh y) / 2
+template <bool FAST>
+__device__ __forceinline__ void cap_all(f4& x, float sc) {
+  float y[4] = {x.x * sc, x.y * sc, x.z * sc, x.w * sc};
+  if constexpr (FAST) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] = rcp(ex2(y[q]) + 1.0f);
+  } else {
+    tanh_all(y);
+  }
+  x = f4{y[0], y[1], y[2], y[3]};
 }
 
 // The distances of a step's pairs: float32 in lengths, so that the slope in base 2 is rounded once;
@@ -328,7 +353,8 @@ void k_attn_fwd(AttnArgs A) {
   f4 acc[C / 16];
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
-  const Score Z = score_of<T>(A);
+  constexpr bool FAST = BF && !SAVE;
+  const Score Z = score_of<FAST>(A);
   typename M::F ones;
   if constexpr (BF) ones = __builtin_bit_cast(typename M::F, u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
 
@@ -397,9 +423,7 @@ void k_attn_fwd(AttnArgs A) {
         const float sl = dist ? slope2<T>(A, A.slope[h]) : 0.f;
         if (Z.cap) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[t][q] = cap_of<T>(x[t][q], Z.sc);
+          for (int t = 0; t < NT; ++t) cap_all<FAST>(x[t], Z.sc);
         }
         const float kk = Z.cap ? Z.k : Z.sc;
 #pragma unroll
@@ -504,23 +528,19 @@ void k_attn_fwd(AttnArgs A) {
       st4((T*)A.out + (int64_t)row * A.ldo + c, acc[ct]);
       if (A.o32) st4(A.o32 + (int64_t)row * C + c, acc[ct]);
     }
-    if (A.lse && g == 0) A.lse[(int64_t)row * H + h] = any ? m[h] + log2f(l[h].x) : INFINITY;
+    if (A.lse && g == 0) A.lse[(int64_t)row * H + h] = any ? m[h] + (log2f(l[h].x) - A.lsub) : INFINITY;
   }
 }
 
 // Score, softmax weight and score gradient of one lane's 4 pairs:
-//   p = 2^(x - lse), dl = p (dp - dsum); ds = dl times the cap's slope 1 - tanh^2
-template <class T>
+//   p = 2^(x - lse) (2^lsub times the weight), dl = p (dp - dsum); ds = dl times the cap's slope 1 - tanh^2
 __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4 dp, f4 r, float slope, f4 lse, f4 dsum,
                                           bool all, uint32_t on, f4& p, f4& dl, f4& ds) {
   f4 f;
   if (Z.cap) {
+    cap_all<false>(sraw, Z.sc);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      sraw[q] = cap_of<T>(sraw[q], Z.sc);
-      // 1 - tanh^2, with u = (1 - tanh) / 2: 4 u (1 - u)
-      f[q] = sizeof(T) == 2 ? 4.0f * fmaf(-sraw[q], sraw[q], sraw[q]) : fmaf(-sraw[q], sraw[q], 1.0f);
-    }
+    for (int q = 0; q < 4; ++q) f[q] = fmaf(-sraw[q], sraw[q], 1.0f);
   }
   const float kk = Z.cap ? Z.k : Z.sc;
 #pragma unroll
@@ -538,19 +558,38 @@ __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4
   }
 }
 
-// p += sum over the pairs of wgt (other - own) / r, nothing where r = 0 (other - own in units)
+// p += sum over the pairs of wgt (other - own) / r, nothing where r = 0 (other - own in units).
+// Of the two images at exactly half a box the one towards the other atom's coordinate as wrapped is
+// taken, so that the two atoms of a pair get opposite gradients (float32 coordinates meet there:
+// about one pair in 2^24).  A lane looks for such pairs by the least of its differences.
 template <int NT>
 __device__ __forceinline__ void add_pairs(float (&p)[3], const f4 (&wgt)[NT], const f4 (&r)[NT], const P3& own,
                                           const u4* ps, bool fix, int g) {
+  const int32_t kHalf = INT32_MIN;
+  int32_t least = 0;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
+      const u4 o = ps[16 * t + 4 * g + q];
       float dx, dy, dz;
-      diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
+      diff(own, o, fix, dx, dy, dz);
+      least = min(least, min((int32_t)(o.x - own.x), min((int32_t)(o.y - own.y), (int32_t)(o.z - own.z))));
       const float f = r[t][q] > 0.f ? wgt[t][q] * rcp(r[t][q]) : 0.f;
       p[0] = fmaf(f, dx, p[0]), p[1] = fmaf(f, dy, p[1]), p[2] = fmaf(f, dz, p[2]);
     }
+  if (fix && __any(least == kHalf)) {  // they were taken as -2^31: 2^32 more towards a larger coordinate
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const u4 o = ps[16 * t + 4 * g + q];
+        const float f = r[t][q] > 0.f ? wgt[t][q] * rcp(r[t][q]) * 4294967296.0f : 0.f;
+        if ((int32_t)(o.x - own.x) == kHalf && o.x > own.x) p[0] += f;
+        if ((int32_t)(o.y - own.y) == kHalf && o.y > own.y) p[1] += f;
+        if ((int32_t)(o.z - own.z) == kHalf && o.z > own.z) p[2] += f;
+      }
+  }
 }
 
 // ------------------------------------------------------------------------------ row pass
@@ -611,7 +650,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
   float px[3] = {0.f, 0.f, 0.f};
-  const Score Z = score_of<T>(A);
+  const Score Z = score_of<false>(A);
 
   StepTile<T, C, RS, NTH> tk, tv;
   typename M::F vf[NT][NC];
@@ -671,7 +710,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
           const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
           f4 p, dl;
           const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
-          pair_grad<T>(Z, dist, x, dp, r[t], sl2, L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl,
+          pair_grad(Z, dist, x, dp, r[t], sl2, L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl,
                        ds[t]);
           if (dist) {
 #pragma unroll
@@ -707,21 +746,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) v += s_s[w][tid];
-      A.dslope_part[block * H + tid] = sizeof(T) == 4 ? v : v * A.unit;
+      A.dslope_part[block * H + tid] = (sizeof(T) == 4 ? v : v * A.unit) * A.p_scale;
     }
   }
 #pragma unroll
-  for (int a = 0; a < 3; ++a) px[a] = r_unit<T>(A) * gsum(px[a]);
+  for (int a = 0; a < 3; ++a) px[a] = r_unit<T>(A) * A.p_scale * gsum(px[a]);
   if (row >= e) return;
   const int64_t at = (int64_t)blockIdx.y * A.n + row;
+  const float gs = A.scale * A.p_scale;
   if (A.dpos && g < 3) (A.splits > 1 ? A.p_row + 3 * at : A.dpos + 3 * (int64_t)row)[g] = g == 0 ? px[0] : g == 1 ? px[1] : px[2];
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) {
     const int c = 16 * ct + 4 * g;
     if (A.splits > 1)
-      *(f4*)(A.p_dq + at * C + c) = acc[ct] * A.scale;
+      *(f4*)(A.p_dq + at * C + c) = acc[ct] * gs;
     else
-      st4((T*)A.dq + (int64_t)row * A.lddq + c, acc[ct] * A.scale);
+      st4((T*)A.dq + (int64_t)row * A.lddq + c, acc[ct] * gs);
   }
 }
 
@@ -753,7 +793,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) ak[ct] = av[ct] = f4{0.f, 0.f, 0.f, 0.f};
   float px[3] = {0.f, 0.f, 0.f};
-  const Score Z = score_of<T>(A);
+  const Score Z = score_of<false>(A);
 
   StepTile<T, C, RS, NTH> tq, to;
   P3 kp{0u, 0u, 0u};
@@ -828,7 +868,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
           const f4 x = head_mma<T, DH, NC>(z, qf, kf[0], h, g), dp = head_mma<T, DH, NC>(z, of, vf[0], h, g);
           const f4 L = *(const f4*)(s_ls[b][0][h] + 16 * t + 4 * g), S = *(const f4*)(s_ls[b][1][h] + 16 * t + 4 * g);
           f4 dl;
-          pair_grad<T>(Z, dist, x, dp, r[t], sl2, L, S, all_own, own_bits, p[t], dl, ds[t]);
+          pair_grad(Z, dist, x, dp, r[t], sl2, L, S, all_own, own_bits, p[t], dl, ds[t]);
           if (dist) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
@@ -852,9 +892,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
     }
   }
 #pragma unroll
-  for (int a = 0; a < 3; ++a) px[a] = r_unit<T>(A) * gsum(px[a]);
+  for (int a = 0; a < 3; ++a) px[a] = r_unit<T>(A) * A.p_scale * gsum(px[a]);
   if (row >= e) return;
   const int64_t at = (int64_t)blockIdx.y * A.n + row;
+  const float gs = A.scale * A.p_scale;
   if (A.dpos && g < 3) {
     const float v = g == 0 ? px[0] : g == 1 ? px[1] : px[2];
     if (A.splits > 1)
@@ -866,11 +907,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
   for (int ct = 0; ct < C / 16; ++ct) {
     const int c = 16 * ct + 4 * g;
     if (A.splits > 1) {
-      *(f4*)(A.p_dk + at * C + c) = ak[ct] * A.scale;
-      *(f4*)(A.p_dv + at * C + c) = av[ct];
+      *(f4*)(A.p_dk + at * C + c) = ak[ct] * gs;
+      *(f4*)(A.p_dv + at * C + c) = av[ct] * A.p_scale;
     } else {
-      st4((T*)A.dk + (int64_t)row * A.lddk + c, ak[ct] * A.scale);
-      st4((T*)A.dv + (int64_t)row * A.lddv + c, av[ct]);
+      st4((T*)A.dk + (int64_t)row * A.lddk + c, ak[ct] * gs);
+      st4((T*)A.dv + (int64_t)row * A.lddv + c, av[ct] * A.p_scale);
     }
   }
 }
@@ -908,7 +949,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs A, int C, int H) {
     if (A.o32) st4(A.o32 + row * C + c + 4 * t, o[t]);
   }
   st_row<T>((T*)A.out + row * A.ldo + c, o);
-  if (A.lse && c % (C / H) == 0) A.lse[row * H + h] = any ? mm + log2f(ll) : INFINITY;
+  if (A.lse && c % (C / H) == 0) A.lse[row * H + h] = any ? mm + (log2f(ll) - A.lsub) : INFINITY;
 }
 
 // dq, dk, dv (blockIdx.y 0, 1, 2) and dpos (3): sums over the splits, in split order

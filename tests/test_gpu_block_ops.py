@@ -296,6 +296,22 @@ def test_structure_attention_coincident_atoms():
         R.check(name, g[name], *ref[name])
 
 
+@pytest.mark.parametrize("dt,sizes", [("f32", [50, 64, 3]), ("f32", [700]), ("bf16", [40, 40]), ("bf16", [300])])
+def test_structure_attention_half_a_box(dt, sizes):
+    """Coordinates on a grid of an eighth of the box: many pairs exactly half a box apart in some
+    direction.  The gradient points along the coordinates' own difference there, so a pair's two are
+    opposite, and equal positions have none."""
+    n, q, k, v, do, sptr, kw = structure_case(sizes, 64, 2, dt, True, 0.0, None, 0.0, 41)
+    kw["pos"] = torch.randint(0, 8, (n, 3), generator=gen(42)).float().cuda()
+    kw["slope"], kw["L"] = torch.tensor([0.3, 0.7], device="cuda"), 8.0
+    ref = R.attention(q, k, v, sptr, 2, dout=do, save=True, **kw)
+    out, saved = m().structure_attention(q, k, v, sptr, 2, save=True, **kw)
+    g = m().structure_attention_bwd(q, k, v, sptr, 2, out, saved, do, **kw)
+    R.check("out", out, *ref["out"])
+    for name in ("dq", "dk", "dv", "dpos", "dslope"):
+        R.check(name, g[name], *ref[name])
+
+
 def test_structure_attention_large_cap():
     """cap = 200 in bf16: the cap's own arithmetic error grows with it (in the bound)"""
     n, q, k, v, do, sptr, kw = structure_case([90, 33], 64, 2, "bf16", True, 200.0, None, 0.0, 31)
