@@ -52,6 +52,7 @@ struct AttnArgs {
   // p_scale = 2^-lsub enters their results once.
   float lsub, p_scale;
   float cap;        // 0: none
+  float tp[6], cap_near, cap_exp;  // the cap's polynomial, the scores it holds for, factor of the exponential beyond
   void *out, *dq, *dk, *dv;
   float *lse, *o32;    // saved: [n][H] base-2 log-sum, [n][C] unrounded output (bf16 only)
   float *dpos, *dslope_part, *dsum;  // [n][3]; [splits][slots][H]; [n][H] sum_c dout out
@@ -89,30 +90,6 @@ __device__ __forceinline__ void diff(const P3& own, const u4& o, bool fix, float
 }
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
-
-// tanh of N values.  Up to 1 the continued fraction y (945 + 105 y^2 + y^4) / (945 + 420 y^2 + 15 y^4)
-// (6e-8 off at 1, relative to y below), which keeps the digits of small values; beyond it, where a wave
-// has any such value, 1 - 2 / (e^2y + 1), whose error of about 1e-7 is absolute.
-template <int N>
-__device__ __forceinline__ void tanh_all(float (&y)[N]) {
-  float t[N], most = 0.f;
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    const float w = y[q] * y[q];
-    t[q] = y[q] * fmaf(w, fmaf(w, 1.0f / 945.0f, 1.0f / 9.0f), 1.0f) *
-           rcp(fmaf(w, fmaf(w, 1.0f / 63.0f, 4.0f / 9.0f), 1.0f));
-    most = fmaxf(most, fabsf(y[q]));
-  }
-  if (__any(most > 1.0f)) {
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-      const float e = 1.0f - 2.0f * rcp(ex2(y[q] * (2.0f * kLog2e)) + 1.0f);
-      t[q] = fabsf(y[q]) > 1.0f ? e : t[q];
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < N; ++q) y[q] = t[q];
-}
 
 // a value that is equal in every lane, as a scalar
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -267,31 +244,63 @@ constexpr int chunk_of(int h) {
   return DH >= MF<T>::CK ? h * (DH / MF<T>::CK) : h / 2;
 }
 
-// Scores in the reference of a lane's query: x = log2(e) s + b.  A forward pass over bf16 features
-// that nothing follows (FAST) takes tanh(y) = 1 - 2 / (e^2y + 1), whose leading 1 is the same for
-// every key and left out of x: one product and sum less, but x is then off by cap times 2e-7, which
-// the float32 gradients of a training pass would show (dpos 1e-6 off instead of 2e-7 at cap 20).
-struct Score {
-  float sc, k;  // x = k f(sc S) + b
-  bool cap;
-};
-template <bool FAST>
-__device__ __forceinline__ Score score_of(const AttnArgs& A) {
-  if (!(A.cap > 0)) return Score{A.scale * kLog2e, 1.0f, false};
-  if constexpr (FAST) return Score{A.scale / A.cap * (2.0f * kLog2e), -2.0f * A.cap * kLog2e, true};
-  return Score{A.scale / A.cap, A.cap * kLog2e, true};
-}
-// the capped part of x over k: tanh y; FAST 1 / (e^2y + 1) = (1 - tanh y) / 2
-template <bool FAST>
-__device__ __forceinline__ void cap_all(f4& x, float sc) {
-  float y[4] = {x.x * sc, x.y * sc, x.z * sc, x.w * sc};
-  if constexpr (FAST) {
+// Scores in base 2: x = k f(S) + b with S the product of a query and a key: f = S without a cap, else
+// f = tanh(y), y = S / (sqrt(d) cap).  Up to |y| = 0.75 tanh is S times a polynomial of NP terms in S^2,
+// whose coefficients (tanh_terms, with the powers of S's factor and, in the forward, k in them) the
+// host makes; beyond, in a step where a wave has any such score, 1 - 2 / (e^2y + 1) (an absolute error
+// of 1e-7, 2e-7 of tanh there).  Neither exponential nor reciprocal, at a quarter of the rate, is needed for
+// most steps: 16,411 atoms bf16, cap 20: CLUSTER us against 657 with them.
+constexpr float kCapNear = 0.75f;
+template <int NP>
+__device__ __forceinline__ float cap_near(const AttnArgs& A, float s) {  // the factor of s
+  const float w = s * s;
+  float f = A.tp[NP - 1];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) y[q] = rcp(ex2(y[q]) + 1.0f);
-  } else {
-    tanh_all(y);
+  for (int z = NP - 2; z >= 0; --z) f = fmaf(w, f, A.tp[z]);
+  return f;
+}
+__device__ __forceinline__ bool far_off(const AttnArgs& A, f4 x) {
+  return fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))) > A.cap_near;
+}
+// f such that s f = k tanh(y); a far score becomes 1 and f its value
+template <int NP, int NT>
+__device__ __forceinline__ void cap_factors(const AttnArgs& A, float k, f4 (&s)[NT], f4 (&f)[NT]) {
+  bool far = false;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    far |= far_off(A, s[t]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f[t][q] = cap_near<NP>(A, s[t][q]);
   }
-  x = f4{y[0], y[1], y[2], y[3]};
+  if (__any(far)) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float e = k * (1.0f - 2.0f * rcp(ex2(s[t][q] * A.cap_exp) + 1.0f));
+        const bool on = fabsf(s[t][q]) > A.cap_near;
+        f[t][q] = on ? e : f[t][q];
+        s[t][q] = on ? 1.0f : s[t][q];
+      }
+  }
+}
+// tanh(y) = y (c_0 + c_1 y^2 + ...) up to 0.75 with the least relative error for so many terms: 3e-8, and
+// 1.1e-5 in a forward pass over bf16 features that nothing follows: at a capped score of 20 that is
+// 3e-4 of a weight, which is then rounded to 2^-9
+template <int NP>
+inline const double* tanh_terms() {
+  static const double c4[4] = {0.99998898, -0.33269670, 0.12742689, -0.03545268};
+  static const double c6[6] = {0.99999997, -0.33332959, 0.13325406, -0.05334442, 0.01958290, -0.00471625};
+  return NP == 4 ? c4 : c6;
+}
+// the fields of A that the cap's polynomial takes (scale: of its result)
+template <int NP>
+void set_cap(AttnArgs& A, double scale) {
+  const double f = (double)A.scale / A.cap;
+  double pw = f * scale;
+  for (int z = 0; z < NP; ++z, pw *= f * f) A.tp[z] = (float)(tanh_terms<NP>()[z] * pw);
+  A.cap_near = (float)(kCapNear / f);
+  A.cap_exp = (float)(2.0 * f * kLog2e);
 }
 
 // The distances of a step's pairs: float32 in lengths, so that the slope in base 2 is rounded once;
@@ -306,15 +315,21 @@ __device__ __forceinline__ float slope2(const AttnArgs& A, float slope) {
 }
 template <class T, int NT>
 __device__ __forceinline__ void distances(f4 (&r)[NT], const AttnArgs& A, const P3& own, const u4* ps, bool fix, int g) {
+  auto all = [&](auto periodic) {  // one branch a step: in each pair it would part every LDS read from the others
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float dx, dy, dz;
-      diff(own, ps[16 * t + 4 * g + q], fix, dx, dy, dz);
-      r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
-      if constexpr (sizeof(T) == 4) r[t][q] *= A.unit;
-    }
+      for (int q = 0; q < 4; ++q) {
+        float dx, dy, dz;
+        diff(own, ps[16 * t + 4 * g + q], decltype(periodic)::value, dx, dy, dz);
+        r[t][q] = __builtin_amdgcn_sqrtf(fmaf(dx, dx, fmaf(dy, dy, dz * dz)));
+        if constexpr (sizeof(T) == 4) r[t][q] *= A.unit;
+      }
+  };
+  if (fix)
+    all(std::true_type{});
+  else
+    all(std::false_type{});
 }
 // Waves per SIMD that the register budgets aim at.  More heads hold more running sums and
 // statistics: 8 heads at three waves (forward) or 4 heads of 16 channels at three (backward) spill
@@ -323,7 +338,9 @@ __device__ __forceinline__ void distances(f4 (&r)[NT], const AttnArgs& A, const 
 #define ATTN_BWD_WAVES (C == 128 || (C == 64 && C / DH > 2) ? 2 : 3)
 
 // ------------------------------------------------------------------------------ forward
-template <class T, int C, int DH, int NW, bool SAVE>
+// CAP is a template parameter: with a branch in its place the uncapped form took 12% longer too (16,384
+// molecules 105 us against 90), the capped scores being merged into its registers.
+template <class T, int C, int DH, int NW, bool SAVE, bool CAP>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_FWD_WAVES)))
 void k_attn_fwd(AttnArgs A) {
   using M = MF<T>;
@@ -353,8 +370,8 @@ void k_attn_fwd(AttnArgs A) {
   f4 acc[C / 16];
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
-  constexpr bool FAST = BF && !SAVE;
-  const Score Z = score_of<FAST>(A);
+  constexpr int NP = BF && !SAVE ? 4 : 6;
+  const float sc = A.scale * kLog2e;
   typename M::F ones;
   if constexpr (BF) ones = __builtin_bit_cast(typename M::F, u4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
 
@@ -410,7 +427,7 @@ void k_attn_fwd(AttnArgs A) {
       if (dist) distances<T, NT>(r, A, own, ps, fix, g);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        f4 x[NT];
+        f4 x[NT], f[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           if constexpr (KL) {
@@ -419,17 +436,14 @@ void k_attn_fwd(AttnArgs A) {
               kf[t][ch] = *(const typename M::F*)(ks + (16 * t + i) * RS + ch * CK + EV * g);
           }
           x[t] = head_mma<T, DH, NC>(f4{0.f, 0.f, 0.f, 0.f}, kf[t], qf[0], h, g);
+          f[t] = f4{sc, sc, sc, sc};
         }
+        if constexpr (CAP) cap_factors<NP, NT>(A, A.cap * kLog2e, x, f);
         const float sl = dist ? slope2<T>(A, A.slope[h]) : 0.f;
-        if (Z.cap) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) cap_all<FAST>(x[t], Z.sc);
-        }
-        const float kk = Z.cap ? Z.k : Z.sc;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) x[t][q] = fmaf(kk, x[t][q], fmaf(-sl, r[t][q], -m[h]));
+          for (int q = 0; q < 4; ++q) x[t][q] = fmaf(x[t][q], f[t][q], fmaf(-sl, r[t][q], -m[h]));
         if (part) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -534,15 +548,17 @@ void k_attn_fwd(AttnArgs A) {
 
 // Score, softmax weight and score gradient of one lane's 4 pairs:
 //   p = 2^(x - lse) (2^lsub times the weight), dl = p (dp - dsum); ds = dl times the cap's slope 1 - tanh^2
-__device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4 dp, f4 r, float slope, f4 lse, f4 dsum,
-                                          bool all, uint32_t on, f4& p, f4& dl, f4& ds) {
+template <bool CAP>
+__device__ __forceinline__ void pair_grad(const AttnArgs& A, float kk, bool dist, f4 sraw, f4 dp, f4 r,
+                                          float slope, f4 lse, f4 dsum, bool all, uint32_t on, f4& p, f4& dl, f4& ds) {
   f4 f;
-  if (Z.cap) {
-    cap_all<false>(sraw, Z.sc);
+  if constexpr (CAP) {
+    f4 s1[1] = {sraw}, f1[1];
+    cap_factors<6, 1>(A, 1.0f, s1, f1);
+    sraw = s1[0] * f1[0];
 #pragma unroll
     for (int q = 0; q < 4; ++q) f[q] = fmaf(-sraw[q], sraw[q], 1.0f);
   }
-  const float kk = Z.cap ? Z.k : Z.sc;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const float x = fmaf(kk, sraw[q], dist ? fmaf(-slope, r[q], -lse[q]) : -lse[q]);
@@ -550,7 +566,7 @@ __device__ __forceinline__ void pair_grad(const Score& Z, bool dist, f4 sraw, f4
     dl[q] = p[q] * (dp[q] - dsum[q]);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) ds[q] = Z.cap ? dl[q] * f[q] : dl[q];
+  for (int q = 0; q < 4; ++q) ds[q] = CAP ? dl[q] * f[q] : dl[q];
   if (!all) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -596,7 +612,7 @@ __device__ __forceinline__ void add_pairs(float (&p)[3], const f4 (&wgt)[NT], co
 // For 16 queries: dsum_i = sum_c dout out (per head), dq_i = scale sum_j ds_ij k_j, the queries'
 // side of the position gradient, and the block's partial of dslope.  out enters unrounded (o32)
 // so that dsum, and with it the float32 gradients, do not carry bf16's rounding.
-template <class T, int C, int DH, int NW>
+template <class T, int C, int DH, int NW, bool CAP>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BWD_WAVES))) void k_attn_row(AttnArgs A) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = C + lds_pad<T>(), EV = M::EV, NTH = 64 * NW;
@@ -650,7 +666,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) acc[ct] = f4{0.f, 0.f, 0.f, 0.f};
   float px[3] = {0.f, 0.f, 0.f};
-  const Score Z = score_of<false>(A);
+  const float kk = (CAP ? A.cap : A.scale) * kLog2e;
 
   StepTile<T, C, RS, NTH> tk, tv;
   typename M::F vf[NT][NC];
@@ -710,7 +726,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
           const f4 x = head_mma<T, DH, NC>(z, kf, qf[0], h, g), dp = head_mma<T, DH, NC>(z, vf[t], of[0], h, g);
           f4 p, dl;
           const f4 L = f4{lse[h], lse[h], lse[h], lse[h]}, S = f4{dsum[h], dsum[h], dsum[h], dsum[h]};
-          pair_grad(Z, dist, x, dp, r[t], sl2, L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl,
+          pair_grad<CAP>(A, kk, dist, x, dp, r[t], sl2, L, S, on == all_live<CK>(), (uint32_t)on >> (4 * g) >> (16 * t), p, dl,
                        ds[t]);
           if (dist) {
 #pragma unroll
@@ -768,7 +784,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
 // ------------------------------------------------------------------------------ column pass
 // For 16 keys: dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij dout_i, and the keys' side of the
 // position gradient, added to what the row pass wrote.
-template <class T, int C, int DH, int NW>
+template <class T, int C, int DH, int NW, bool CAP>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BWD_WAVES))) void k_attn_col(AttnArgs A) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, NT = M::NT, CK = M::CK, H = C / DH, RS = C + lds_pad<T>(), EV = M::EV, NTH = 64 * NW;
@@ -793,7 +809,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) ak[ct] = av[ct] = f4{0.f, 0.f, 0.f, 0.f};
   float px[3] = {0.f, 0.f, 0.f};
-  const Score Z = score_of<false>(A);
+  const float kk = (CAP ? A.cap : A.scale) * kLog2e;
 
   StepTile<T, C, RS, NTH> tq, to;
   P3 kp{0u, 0u, 0u};
@@ -868,7 +884,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
           const f4 x = head_mma<T, DH, NC>(z, qf, kf[0], h, g), dp = head_mma<T, DH, NC>(z, of, vf[0], h, g);
           const f4 L = *(const f4*)(s_ls[b][0][h] + 16 * t + 4 * g), S = *(const f4*)(s_ls[b][1][h] + 16 * t + 4 * g);
           f4 dl;
-          pair_grad(Z, dist, x, dp, r[t], sl2, L, S, all_own, own_bits, p[t], dl, ds[t]);
+          pair_grad<CAP>(A, kk, dist, x, dp, r[t], sl2, L, S, all_own, own_bits, p[t], dl, ds[t]);
           if (dist) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
@@ -1000,33 +1016,34 @@ int launch_join(const AttnArgs& A, int C, int H, bool bwd, hipStream_t st) {
 int launch_attn_bf16(const AttnArgs& A, int C, int dh, bool split, int what, hipStream_t st);
 int launch_attn_f32(const AttnArgs& A, int C, int dh, bool split, int what, hipStream_t st);
 
+template <class T, int C, int DH, int NW, bool CAP>
+void launch_attn_k(AttnArgs A, int what, hipStream_t st) {
+  const dim3 blocks((unsigned)(A.n / (16 * NW) + A.n_struct), (unsigned)A.splits);
+  constexpr bool SAVES = sizeof(T) == 2;  // float32 has no second form
+  if constexpr (CAP) {
+    if (what > 0)
+      set_cap<6>(A, 1.0);
+    else if (A.lse || !SAVES)
+      set_cap<6>(A, (double)A.cap * kLog2e);
+    else
+      set_cap<4>(A, (double)A.cap * kLog2e);
+  }
+  if (what == 1)
+    k_attn_row<T, C, DH, NW, CAP><<<blocks, 64 * NW, 0, st>>>(A);
+  else if (what == 2)
+    k_attn_col<T, C, DH, NW, CAP><<<blocks, 64 * NW, 0, st>>>(A);
+  else if (A.lse)
+    k_attn_fwd<T, C, DH, NW, SAVES, CAP><<<blocks, 64 * NW, 0, st>>>(A);
+  else
+    k_attn_fwd<T, C, DH, NW, false, CAP><<<blocks, 64 * NW, 0, st>>>(A);
+}
+
 template <class T, int C, int DH>
 int launch_attn_c(const AttnArgs& A, bool split, int what, hipStream_t st) {
-  constexpr int NW = 4;
-  const dim3 blocks((unsigned)(A.n / (split ? 16 * NW : 16) + A.n_struct), (unsigned)A.splits);
-  constexpr bool SAVES = sizeof(T) == 2;  // float32 has no second form
-  auto go = [&](void (*save)(AttnArgs), void (*plain)(AttnArgs), int threads) {
-    (A.lse ? save : plain)<<<blocks, threads, 0, st>>>(A);
-  };
-  switch (what) {
-    case 0:
-      if (split)
-        go(k_attn_fwd<T, C, DH, NW, SAVES>, k_attn_fwd<T, C, DH, NW, false>, 64 * NW);
-      else
-        go(k_attn_fwd<T, C, DH, 1, SAVES>, k_attn_fwd<T, C, DH, 1, false>, 64);
-      break;
-    case 1:
-      if (split)
-        k_attn_row<T, C, DH, NW><<<blocks, 64 * NW, 0, st>>>(A);
-      else
-        k_attn_row<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
-      break;
-    default:
-      if (split)
-        k_attn_col<T, C, DH, NW><<<blocks, 64 * NW, 0, st>>>(A);
-      else
-        k_attn_col<T, C, DH, 1><<<blocks, 64, 0, st>>>(A);
-  }
+  if (A.cap > 0)
+    split ? launch_attn_k<T, C, DH, 4, true>(A, what, st) : launch_attn_k<T, C, DH, 1, true>(A, what, st);
+  else
+    split ? launch_attn_k<T, C, DH, 4, false>(A, what, st) : launch_attn_k<T, C, DH, 1, false>(A, what, st);
   MP_CHECK_LAUNCH();
   if (A.splits > 1 && what != 1) return launch_join<T>(A, C, C / DH, what == 2, st);
   return MP_OK;

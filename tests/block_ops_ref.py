@@ -180,7 +180,7 @@ def attention(q, k, v, sptr, heads, pos=None, slope=None, L=0.0, mask=None, cap=
         if cap:
             th = torch.tanh(t / cap)
             t = cap * th
-            et = et * (1 - th * th) + cap * K * (1.0 if dt == torch.bfloat16 and not save else th.abs()) + E * t.abs()
+            et = et * (1 - th * th) + cap * th.abs() * (K + (1.2e-5 if dt == torch.bfloat16 and not save else 0)) + E * t.abs()
         if pos is not None:
             p = pos[s:e].clone()
             delta = p[None] - p[:, None]        # x_j - x_i
