@@ -335,7 +335,7 @@ __device__ __forceinline__ void distances(f4 (&r)[NT], const AttnArgs& A, const 
 // statistics: 8 heads at three waves (forward) or 4 heads of 16 channels at three (backward) spill
 // (11,000 atoms bf16: 720 us against 577; 1,571 against 1,382).
 #define ATTN_FWD_WAVES (C == 128 && (C / DH > 4 || sizeof(T) == 4) ? 2 : 3)
-#define ATTN_BWD_WAVES (C == 128 || (C == 64 && C / DH > 2) ? 2 : 3)
+#define ATTN_BWD_WAVES (C == 128 || (C == 64 && C / DH > 1) ? 2 : 3)
 
 // ------------------------------------------------------------------------------ forward
 // CAP is a template parameter: with a branch in its place the uncapped form took 12% longer too (16,384

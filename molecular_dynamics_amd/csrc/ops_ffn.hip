@@ -306,16 +306,20 @@ __device__ __forceinline__ void hidden_grad(float zg, float zu, float dh, ActAB 
 // chunk), the hidden gradients in registers, and D[c][a] += Wg^T dzg + Wu^T dzu (the same
 // rows of Wg and Wu, read transposed).  SPLIT as in the forward, each wave with a chunk of its
 // own in LDS.
+template <class T, int C, bool SPLIT>
+constexpr int ffn_dx_lds() {
+  constexpr int SLAB = SPLIT ? 64 * (C + 4) * 4 : 0;
+  constexpr int CHUNKS = (SPLIT ? 4 : 2) * Chunk<T, C, SPLIT ? 64 : 256, true>::SIZE * (int)sizeof(T);
+  return SLAB > CHUNKS ? SLAB : CHUNKS;
+}
 template <class T, int C, int AT, bool SPLIT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(SPLIT ? 1 : 2, 2))) void k_ffn_dx(FfnArgs A) {
+__device__ __forceinline__ void ffn_dx(const FfnArgs& A, int block, char* s_raw) {
   using M = MF<T>;
   using CH = Chunk<T, C, SPLIT ? 64 : 256, true>;
   constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = CH::RS, RD = CH::RD, OS = C + 4;
-  constexpr int SLAB = SPLIT ? 64 * OS * 4 : 0, CHUNKS = (SPLIT ? 4 : 2) * CH::SIZE * (int)sizeof(T);
-  __shared__ __align__(16) char s_raw[SLAB > CHUNKS ? SLAB : CHUNKS];
   T* s = (T*)s_raw;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
-  const int64_t a0 = SPLIT ? (int64_t)blockIdx.x * 16 : ((int64_t)blockIdx.x * 4 + wave) * (16 * AT);
+  const int64_t a0 = SPLIT ? (int64_t)block * 16 : ((int64_t)block * 4 + wave) * (16 * AT);
   typename M::F xf[AT][NC], df[AT][NC];
   load_rows<T, C, AT>(xf, A.x, A.ldx, a0, A.n, i, g);
   load_rows<T, C, AT>(df, A.dy, A.ldy, a0, A.n, i, g);
@@ -407,19 +411,28 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(SPLIT ? 1 :
   }
 }
 
+template <class T, int C, int AT, bool SPLIT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(SPLIT ? 1 : 2, 2))) void k_ffn_dx(FfnArgs A) {
+  __shared__ __align__(16) char s_raw[ffn_dx_lds<T, C, SPLIT>()];
+  ffn_dx<T, C, AT, SPLIT>(A, blockIdx.x, s_raw);
+}
+
 // dWg, dWu, dWd over one split of the rows.  A wave owns 16 hidden units: their rows of Wg,
 // Wu and Wd^T stay in registers, CK atoms' x and dy pass through LDS.  The hidden values are
 // formed with the atoms as rows, which is tile order for the contraction over atoms:
 //   dWg[hid][c] += dzg^T x,  dWu[hid][c] += dzu^T x,  dWd[c][hid] += dy^T h,
 // x and dy read transposed from LDS.
 template <class T, int C>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn_dw(FfnArgs A) {
+constexpr int ffn_dw_lds() {
+  return 4 * MF<T>::CK * (C + lds_pad<T>()) * (int)sizeof(T);
+}
+template <class T, int C>
+__device__ __forceinline__ void ffn_dw(const FfnArgs& A, int bx, int by, char* s_raw) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + lds_pad<T>();
-  __shared__ __align__(16) T s_x[2][CK * RS];
-  __shared__ __align__(16) T s_d[2][CK * RS];
+  T *s_x = (T*)s_raw, *s_d = s_x + 2 * CK * RS;  // two buffers each
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int hw = blockIdx.x * 64 + 16 * wave, hid = hw + i;
+  const int hw = bx * 64 + 16 * wave, hid = hw + i;
   const bool on = hw < A.hidden;
   typename M::F fg[NC], fu[NC], fd[NC];
   if (on) {
@@ -437,7 +450,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   f4 ag[C / 16], au[C / 16], ad[C / 16];
 #pragma unroll
   for (int ct = 0; ct < C / 16; ++ct) ag[ct] = au[ct] = ad[ct] = f4{0.f, 0.f, 0.f, 0.f};
-  const int64_t r0 = (int64_t)blockIdx.y * A.rows_per_split, r1 = min(A.n, r0 + A.rows_per_split);
+  const int64_t r0 = (int64_t)by * A.rows_per_split, r1 = min(A.n, r0 + A.rows_per_split);
   Tile<T, CK, C, RS, 256> tx, td;
   auto fetch = [&](int64_t r) {
     const int rows = (int)min<int64_t>(CK, r1 - r);
@@ -446,15 +459,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   };
   if (r0 < r1) {
     fetch(r0);
-    tx.put(s_x[0], threadIdx.x);
-    td.put(s_d[0], threadIdx.x);
+    tx.put(s_x, threadIdx.x);
+    td.put(s_d, threadIdx.x);
   }
   __syncthreads();
   int b = 0;
   for (int64_t r = r0; r < r1; r += CK, b ^= 1) {
     if (r + CK < r1) fetch(r + CK);
     if (on) {
-      const T *xs = s_x[b], *ds = s_d[b];
+      const T *xs = s_x + b * CK * RS, *ds = s_d + b * CK * RS;
       f4 h[NT], zg[NT], zu[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -488,13 +501,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       }
     }
     if (r + CK < r1) {
-      tx.put(s_x[b ^ 1], threadIdx.x);
-      td.put(s_d[b ^ 1], threadIdx.x);
+      tx.put(s_x + (b ^ 1) * CK * RS, threadIdx.x);
+      td.put(s_d + (b ^ 1) * CK * RS, threadIdx.x);
     }
     __syncthreads();
   }
   if (!on) return;
-  float* p = A.part + (int64_t)blockIdx.y * 3 * C * A.hidden;
+  float* p = A.part + (int64_t)by * 3 * C * A.hidden;
   float* pu = p + (int64_t)C * A.hidden;
   float* pd = pu + (int64_t)C * A.hidden;
 #pragma unroll
@@ -507,6 +520,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
 }
 
+template <class T, int C>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn_dw(FfnArgs A) {
+  __shared__ __align__(16) char s_raw[ffn_dw_lds<T, C>()];
+  ffn_dw<T, C>(A, blockIdx.x, blockIdx.y, s_raw);
+}
+
+// dx and the weight gradients of few rows in one launch: neither fills the card alone.  The first
+// dx_blocks blocks form dx.
+template <class T, int C>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_ffn_bwd_few(FfnArgs A, int dx_blocks,
+                                                                                               int nb) {
+  constexpr int X = ffn_dx_lds<T, C, true>(), W = ffn_dw_lds<T, C>();
+  __shared__ __align__(16) char s_raw[X > W ? X : W];
+  const int b = (int)blockIdx.x - dx_blocks;
+  if (b < 0)
+    ffn_dx<T, C, 1, true>(A, blockIdx.x, s_raw);
+  else
+    ffn_dw<T, C>(A, b % nb, b / nb, s_raw);
+}
+
 // Splits of the rows for the weight gradients: about 512 blocks in all, each with at least
 // 64 rows (a split costs three partial matrices written and read once; 4,096 rows of 64 float32,
 // 256 hidden: 16.5 us and 6.4 for the sum, with at least 128 rows 20.4 and 5.3)
@@ -515,12 +548,20 @@ int64_t ffn_splits(int64_t n, int hidden) {
   return std::max<int64_t>(1, std::min<int64_t>(512 / nb, cdiv(n, 64)));
 }
 
+// Whether dx and the weight gradients go in one launch, whose blocks all hold dx's LDS: float32, 256
+// hidden of 64, with the sum: 17 us and 26 in two launches at 512 rows, 32 and 35 at 4,096; 512 of 128:
+// 52 and 71 at 512, 62 and 78 at 2,048, but 160 and 155 at 8,000 (bf16 41 and 45, 65 and 60).
+bool ffn_both(int64_t n, int C) { return n * C <= 384 << 10; }
+// what: 0 forward, 1 dx, 2 weight gradients, 3 both (few rows)
 template <class T, int C>
 int launch_ffn_c(FfnArgs A, int what, hipStream_t st) {
   constexpr int AT = sizeof(T) == 2 ? 2 : 1;
-  if (what == 2) {
-    const int64_t S = ffn_splits(A.n, A.hidden);
-    A.rows_per_split = cdiv(cdiv(A.n, S), MF<T>::CK) * MF<T>::CK;
+  const int64_t S = ffn_splits(A.n, A.hidden);
+  A.rows_per_split = cdiv(cdiv(A.n, S), MF<T>::CK) * MF<T>::CK;
+  if (what == 3) {
+    const int nx = (int)cdiv(A.n, 16), nb = (int)cdiv(A.hidden, 64);
+    k_ffn_bwd_few<T, C><<<(unsigned)(nx + nb * S), 256, 0, st>>>(A, nx, nb);
+  } else if (what == 2) {
     k_ffn_dw<T, C><<<dim3((unsigned)cdiv(A.hidden, 64), (unsigned)S), 256, 0, st>>>(A);
   } else {
     // Few rows: the hidden units are split over the waves of a block.  128 channels, 512 hidden
@@ -633,9 +674,13 @@ extern "C" int mp_gated_ffn_bwd(int32_t n, int32_t channels, int32_t hidden, int
     A.part = (float*)ws;
   }
   ProfScope p("gated_ffn_bwd", st);
-  if (n > 0 && dx) MP_TRY(ops::launch_ffn(A, channels, dt == 1, 1, st));
-  if (!grads) return MP_OK;
-  if (n > 0) MP_TRY(ops::launch_ffn(A, channels, dt == 1, 2, st));
+  if (n > 0 && dx && grads && ops::ffn_both(n, channels)) {
+    MP_TRY(ops::launch_ffn(A, channels, dt == 1, 3, st));
+  } else {
+    if (n > 0 && dx) MP_TRY(ops::launch_ffn(A, channels, dt == 1, 1, st));
+    if (!grads) return MP_OK;
+    if (n > 0) MP_TRY(ops::launch_ffn(A, channels, dt == 1, 2, st));
+  }
   const int64_t S = n > 0 ? ops::ffn_splits(n, hidden) : 0, N = (int64_t)channels * hidden;
   const ops::Segment seg[3] = {{0, N, dwg, dt == 1}, {N, N, dwu, dt == 1}, {2 * N, N, dwd, dt == 1}};
   return ops::reduce_rows(A.part, S, 3 * N, seg, 3, st);
