@@ -21,9 +21,13 @@
 // Masked atoms and rows past the structure are staged as zeros and their scores set to -inf,
 // so nothing they hold (NaN, infinities) reaches another atom.
 //
-// Bound: VALU (per score one exp, with a cap exp and reciprocal more, at a quarter of the
-// rate, beside ~10 plain operations), not MFMA: at 32 channels per head a score costs 128
-// matrix operations, 1/8 of its VALU time.
+// Bound: VALU.  A score costs one exp at a quarter of the rate and about a dozen plain operations
+// beside 128 matrix operations (32 channels a head), 1/8 of its VALU time.  Measured, four heads of 32:
+//   16,384 molecules of 8-32 atoms, bf16, forward     86 us  (its bytes at a copy's rate: 69)
+//   16,411 atoms in one structure, bf16, capped, fwd 577 us  + join 14  (1.08e9 scores, 483 VALU
+//                                                    instructions a wave for 16 x 32 pairs, four heads)
+//   4,096 molecules of 1-40 atoms, bf16, capped: fwd 40-45, row pass 59, column pass 53 us
+//   4,096 atoms, one periodic box, float32: fwd 123, row 177, col 206 us, joins 16 and 20
 #pragma once
 #include <algorithm>
 
