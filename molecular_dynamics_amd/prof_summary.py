@@ -160,8 +160,8 @@ def kernel_source_hash():
 
 
 def short_name(name):
-    n = name.replace("void ", "").split("(")[0]
-    return n.replace("mdmp::", "")
+    n = name.replace("void ", "").replace("(anonymous namespace)::", "").split("(")[0]
+    return n.replace("mdmp::", "").replace("ops::", "").replace("unsigned short", "bf16")
 
 
 def stats(path, cmd, top):
