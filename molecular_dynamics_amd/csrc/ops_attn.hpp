@@ -186,14 +186,6 @@ struct StepTile {
     for (int j = 0; j < IT; ++j) *(u4*)(dst + (tid / VPR + j * RJ) * RS + (tid % VPR) * EV) = v[j];
   }
 };
-// all waves of a block, or one wave, have written or read their LDS
-template <int NW>
-__device__ __forceinline__ void step_sync() {
-  if constexpr (NW == 1)
-    wave_sync();
-  else
-    lds_barrier();
-}
 // chunks c0 .. c1 - 1 of the operands of NTL tiles
 template <class T, int C, int NTL>
 __device__ __forceinline__ void load_frags(typename MF<T>::F (&f)[NTL][C / MF<T>::CK], const T* src, int64_t ld,

@@ -12,6 +12,7 @@ import math
 import os
 
 import numpy as np
+import torch  # noqa: F401  before the library, which then shares PyTorch's HIP runtime; after it there would be two
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmdmp.so")

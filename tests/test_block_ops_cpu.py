@@ -174,3 +174,14 @@ def test_structure_attention_refusals():
     refused(bwd(dq=ODD), "rows of dq")
     refused(bwd(ws=None), "workspace")
     refused(bwd(nb=n.value - 1), "workspace too small")
+
+
+def test_one_hip_runtime_whatever_is_imported_first():
+    """The binding imported before torch must not bring a second HIP runtime into the process (device
+    calls of one of the two then find no device)."""
+    import subprocess
+    import sys
+    code = ("from molecular_dynamics_amd import mdmp; import torch; "
+            "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split()[-1] == "1", r.stdout + r.stderr

@@ -312,9 +312,13 @@ def test_structure_attention_half_a_box(dt, sizes):
         R.check(name, g[name], *ref[name])
 
 
-def test_structure_attention_large_cap():
-    """cap = 200 in bf16: the cap's own arithmetic error grows with it (in the bound)"""
-    n, q, k, v, do, sptr, kw = structure_case([90, 33], 64, 2, "bf16", True, 200.0, None, 0.0, 31)
+@pytest.mark.parametrize("cap", [1e-3, 0.3, 200.0, 1e4])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_structure_attention_caps(dt, cap):
+    """The ends of the cap's range: every score past the polynomial, scores on both sides of its end, none."""
+    n, q, k, v, do, sptr, kw = structure_case([90, 33], 64, 2, dt, True, cap, None, 0.0, 31)
+    ref = R.attention(q, k, v, sptr, 2, **kw)
+    R.check("out", m().structure_attention(q, k, v, sptr, 2, **kw), *ref["out"])
     ref = R.attention(q, k, v, sptr, 2, dout=do, save=True, **kw)
     out, saved = m().structure_attention(q, k, v, sptr, 2, save=True, **kw)
     g = m().structure_attention_bwd(q, k, v, sptr, 2, out, saved, do, **kw)
