@@ -145,6 +145,18 @@ struct Tile {
   }
 };
 
+// What rounding left of the tiles that p packs, as a second operand: p and it are the tiles to 2^-17.
+// Worth its products where few rows leave the matrix cores idle; float32 rounds nothing.
+template <class T>
+__device__ __forceinline__ typename MF<T>::F rest_of(typename MF<T>::F p, const f4* t) {
+  using M = MF<T>;
+  f4 r[M::NT];
+  M::unpack(p, r);
+#pragma unroll
+  for (int z = 0; z < M::NT; ++z) r[z] = t[z] - r[z];
+  return M::pack(r);
+}
+
 // EV consecutive elements of a row as float / from float
 template <class T>
 __device__ __forceinline__ void st_row(T* p, const f4* t) {

@@ -283,8 +283,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     ffn_in<T, C, 1>(zg, zu, xf, [&](int t, int ch) { return *(const typename M::F*)(wg + nat_row<T>(t, i) * C + ch * CK); },
                     [&](int t, int ch) { return *(const typename M::F*)(wu + nat_row<T>(t, i) * C + ch * CK); });
     ffn_act<T, 1>(h, zg, zu, A.ab);
-    ffn_down<T, C, 1>(
-        acc, h, [&](int p, int t) { return *(const typename M::F*)(wd + (int64_t)(p * CK + nat_row<T>(t, i)) * A.hidden); });
+    const typename M::F h2 = rest_of<T>(h[0], zg[0]);  // the hidden units as two operands
+#pragma unroll
+    for (int p = 0; p < NC; ++p)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const typename M::F f = *(const typename M::F*)(wd + (int64_t)(p * CK + nat_row<T>(t, i)) * A.hidden);
+        if constexpr (sizeof(T) == 2) acc[0][p][t] = M::mma(acc[0][p][t], f, h2);
+        acc[0][p][t] = M::mma(acc[0][p][t], f, h[0]);
+      }
   }
   float* slab = s_o + (16 * wave + i) * OS;
 #pragma unroll
@@ -383,9 +390,13 @@ __device__ __forceinline__ void ffn_dx(const FfnArgs& A, int block, char* s_raw)
       du[at] = M::pack(zu[at]);
     }
     // hidden unit EV g + j of the operands is LDS row 16 t + 4 g + r: tile order
+    constexpr bool FINE = SPLIT && sizeof(T) == 2;
+    typename M::F dg2, du2;
+    if constexpr (FINE) dg2 = rest_of<T>(dg[0], zg[0]), du2 = rest_of<T>(du[0], zu[0]);
 #pragma unroll
     for (int ct = 0; ct < C / 16; ++ct) {
       const typename M::F fg = ldt<RS>(wg, 0, 16 * ct, lane), fu = ldt<RS>(wu, 0, 16 * ct, lane);
+      if constexpr (FINE) acc[0][ct] = M::mma(M::mma(acc[0][ct], fg, dg2), fu, du2);
 #pragma unroll
       for (int at = 0; at < AT; ++at) acc[at][ct] = M::mma(M::mma(acc[at][ct], fg, dg[at]), fu, du[at]);
     }
@@ -431,7 +442,7 @@ template <class T, int C>
 constexpr int ffn_dw_lds() {
   return 4 * MF<T>::CK * (C + lds_pad<T>()) * (int)sizeof(T);
 }
-template <class T, int C>
+template <class T, int C, bool FEW>
 __device__ __forceinline__ void ffn_dw(const FfnArgs& A, int bx, int by, char* s_raw) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + lds_pad<T>();
@@ -497,9 +508,17 @@ __device__ __forceinline__ void ffn_dw(const FfnArgs& A, int bx, int by, char* s
         }
       }
       const typename M::F ph = M::pack(h), pg = M::pack(zg), pu = M::pack(zu);
+      constexpr bool FINE = FEW && sizeof(T) == 2;
+      typename M::F ph2, pg2, pu2;
+      if constexpr (FINE) ph2 = rest_of<T>(ph, h), pg2 = rest_of<T>(pg, zg), pu2 = rest_of<T>(pu, zu);
 #pragma unroll
       for (int ct = 0; ct < C / 16; ++ct) {
         const typename M::F fx = ldt<RS>(xs, 0, 16 * ct, lane), fy = ldt<RS>(ds, 0, 16 * ct, lane);
+        if constexpr (FINE) {
+          ag[ct] = M::mma(ag[ct], pg2, fx);
+          au[ct] = M::mma(au[ct], pu2, fx);
+          ad[ct] = M::mma(ad[ct], fy, ph2);
+        }
         ag[ct] = M::mma(ag[ct], pg, fx);
         au[ct] = M::mma(au[ct], pu, fx);
         ad[ct] = M::mma(ad[ct], fy, ph);
@@ -528,7 +547,7 @@ __device__ __forceinline__ void ffn_dw(const FfnArgs& A, int bx, int by, char* s
 template <class T, int C>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ffn_dw(FfnArgs A) {
   __shared__ __align__(16) char s_raw[ffn_dw_lds<T, C>()];
-  ffn_dw<T, C>(A, blockIdx.x, blockIdx.y, s_raw);
+  ffn_dw<T, C, false>(A, blockIdx.x, blockIdx.y, s_raw);
 }
 
 // dx and the weight gradients of few rows in one launch: neither fills the card alone.  The first
@@ -542,7 +561,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   if (b < 0)
     ffn_dx<T, C, 1, true>(A, blockIdx.x, s_raw);
   else
-    ffn_dw<T, C>(A, b % nb, b / nb, s_raw);
+    ffn_dw<T, C, true>(A, b % nb, b / nb, s_raw);
 }
 
 // Splits of the rows for the weight gradients: about 512 blocks in all, each with at least
@@ -553,10 +572,16 @@ int64_t ffn_splits(int64_t n, int hidden) {
   return std::max<int64_t>(1, std::min<int64_t>(512 / nb, cdiv(n, 64)));
 }
 
+// Few rows: the hidden units are split over the waves of a block.  128 channels, 512 hidden
+// units: bf16 27 us split and 28 not at 8,000 rows, 61 and 30 at 20,000; float32 50 and 108 at
+// 8,000, 109 and 114 at 20,000.  There bf16's hidden units and their gradients enter the second
+// products as two operands each (rest_of), so outputs carry one rounding and
+// not three: 3 to 5 % of the backward, nothing of the forward.
+bool ffn_few(int64_t n, bool bf16) { return n < (bf16 ? 8192 : 20480); }
 // Whether dx and the weight gradients go in one launch, whose blocks all hold dx's LDS: float32, 256
 // hidden of 64, with the sum: 17 us and 26 in two launches at 512 rows, 32 and 35 at 4,096; 512 of 128:
 // 52 and 71 at 512, 62 and 78 at 2,048, but 160 and 155 at 8,000 (bf16 41 and 45, 65 and 60).
-bool ffn_both(int64_t n, int C) { return n * C <= 384 << 10; }
+bool ffn_both(int64_t n, int C, bool bf16) { return n * C <= 384 << 10 && ffn_few(n, bf16); }
 // what: 0 forward, 1 dx, 2 weight gradients, 3 both (few rows)
 template <class T, int C>
 int launch_ffn_c(FfnArgs A, int what, hipStream_t st) {
@@ -569,10 +594,7 @@ int launch_ffn_c(FfnArgs A, int what, hipStream_t st) {
   } else if (what == 2) {
     k_ffn_dw<T, C><<<dim3((unsigned)cdiv(A.hidden, 64), (unsigned)S), 256, 0, st>>>(A);
   } else {
-    // Few rows: the hidden units are split over the waves of a block.  128 channels, 512 hidden
-    // units: bf16 27 us split and 28 not at 8,000 rows, 61 and 30 at 20,000; float32 50 and 108 at
-    // 8,000, 109 and 114 at 20,000.
-    const bool few = A.n < (sizeof(T) == 2 ? 8192 : 20480);
+    const bool few = ffn_few(A.n, sizeof(T) == 2);
     const unsigned blocks = (unsigned)cdiv(A.n, few ? 16 : 64 * AT);
     if (what == 0) {
       if (few)
@@ -679,7 +701,7 @@ extern "C" int mp_gated_ffn_bwd(int32_t n, int32_t channels, int32_t hidden, int
     A.part = (float*)ws;
   }
   ProfScope p("gated_ffn_bwd", st);
-  if (n > 0 && dx && grads && ops::ffn_both(n, channels)) {
+  if (n > 0 && dx && grads && ops::ffn_both(n, channels, dt == 1)) {
     MP_TRY(ops::launch_ffn(A, channels, dt == 1, 3, st));
   } else {
     if (n > 0 && dx) MP_TRY(ops::launch_ffn(A, channels, dt == 1, 1, st));
