@@ -276,13 +276,14 @@ int mp_energy_forces_heads(const mp_model* m, const mp_heads* heads, const mp_gr
  * matrices are of feat_dtype (0 float32, 1 bfloat16); vectors of parameters,
  * positions and slopes and the gradients of those are float32.  bfloat16: products
  * take bf16 operands with float32 accumulation, everything else is float32, and
- * each output is rounded once; an intermediate that is the operand of a second
- * product (hidden units, attention weights, their gradients) is rounded to bf16 on
- * the way in.  channels C: 16 (float32 only), 32, 64 or 128.  n is at most 2^26;
- * n = 0 is allowed: no row is touched and parameter gradients are zeros.  Outputs
- * must not overlap inputs or one another unless a call says so (column slices of one
- * matrix do not).  All calls only enqueue work (no host sync, no allocation, no
- * memset nodes, so they can be captured) and give equal bits for equal inputs.  ws: device scratch of at least the _ws call's bytes, 16-byte
+ * each output is rounded once; hidden units and gradients of pre-activations, where
+ * there are many rows, and attention weights outside a training pass are rounded to
+ * bf16 as the operand of their second product.  channels C: 16 (float32 only), 32, 64
+ * or 128.  n is at most 2^26; n = 0 is allowed: no row is touched and parameter
+ * gradients are zeros.  Outputs must not overlap inputs or one another unless a call
+ * says so (column slices of one matrix do not).  All calls only enqueue work (no host
+ * sync, no allocation, no memset nodes, so they can be captured) and give equal bits
+ * for equal inputs.  ws: device scratch of at least the _ws call's bytes, 16-byte
  * aligned, used by one call at a time. */
 #define MP_ACT_NONE 0
 #define MP_ACT_SILU 1

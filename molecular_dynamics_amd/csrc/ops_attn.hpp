@@ -26,7 +26,7 @@
 //   16,384 molecules of 8-32 atoms, bf16, forward     86 us  (its bytes at a copy's rate: 69)
 //   16,411 atoms in one structure, bf16, capped, fwd 577 us  + join 14  (1.08e9 scores, 483 VALU
 //                                                    instructions a wave for 16 x 32 pairs, four heads)
-//   4,096 molecules of 1-40 atoms, bf16, capped: fwd 40-45, row pass 59, column pass 53 us
+//   4,096 molecules of 1-40 atoms, bf16, capped: fwd 40-45, row pass 60, column pass 56 us
 //   4,096 atoms, one periodic box, float32: fwd 123, row 177, col 206 us, joins 16 and 20
 #pragma once
 #include <algorithm>
@@ -732,9 +732,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
             }
           }
         }
-        const typename M::F pd = M::pack(ds);
+        const typename M::F pd = M::pack(ds), pd2 = rest_of<T>(pd, ds);
 #pragma unroll
-        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) acc[ct] = M::mma(acc[ct], ldt<RS>(ks, 0, 16 * ct, lane), pd);
+        for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
+          const typename M::F f = ldt<RS>(ks, 0, 16 * ct, lane);
+          if constexpr (sizeof(T) == 2) acc[ct] = M::mma(acc[ct], f, pd2);
+          acc[ct] = M::mma(acc[ct], f, pd);
+        }
       }
       if (A.dpos) add_pairs<NT>(px, wgt, r, own, ps, fix, g);
     }
@@ -778,6 +782,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
 }
 
 // ------------------------------------------------------------------------------ column pass
+// Here and in the row pass bf16 weights and score gradients enter as two operands (rest_of): dq, dk and
+// dv carry the rounding of the output alone (4,096 molecules: 62 -> 62 and 55 -> 57 us).
 // For 16 keys: dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij dout_i, and the keys' side of the
 // position gradient, added to what the row pass wrote.
 template <class T, int C, int DH, int NW, bool CAP>
@@ -886,11 +892,16 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(ATTN_BW
             for (int q = 0; q < 4; ++q) wgt[t][q] = fmaf(sl, dl[q], wgt[t][q]);
           }
         }
-        const typename M::F pp = M::pack(p), pd = M::pack(ds);
+        const typename M::F pp = M::pack(p), pd = M::pack(ds), pp2 = rest_of<T>(pp, p), pd2 = rest_of<T>(pd, ds);
 #pragma unroll
         for (int ct = h * DH / 16; ct < (h + 1) * DH / 16; ++ct) {
-          av[ct] = M::mma(av[ct], ldt<RS>(os, 0, 16 * ct, lane), pp);
-          ak[ct] = M::mma(ak[ct], ldt<RS>(qs, 0, 16 * ct, lane), pd);
+          const typename M::F fo = ldt<RS>(os, 0, 16 * ct, lane), fq = ldt<RS>(qs, 0, 16 * ct, lane);
+          if constexpr (sizeof(T) == 2) {
+            av[ct] = M::mma(av[ct], fo, pp2);
+            ak[ct] = M::mma(ak[ct], fq, pd2);
+          }
+          av[ct] = M::mma(av[ct], fo, pp);
+          ak[ct] = M::mma(ak[ct], fq, pd);
         }
       }
       if (A.dpos) add_pairs<NT>(px, wgt, r, own, ps, fix, g);

@@ -215,6 +215,11 @@ __device__ __forceinline__ void linear_dx(const LinArgs& A, int block, char* s_r
           d[t][r] *= e;
         }
       dz = M::pack(d);
+      if constexpr (SPLIT && sizeof(T) == 2) {  // few rows: dz as two operands
+        const typename M::F dz2 = rest_of<T>(dz, d);
+#pragma unroll
+        for (int ct = 0; ct < C / 16; ++ct) dx[ct] = M::mma(dx[ct], ldt<RS>(w, 0, 16 * ct, lane), dz2);
+      }
     }
 #pragma unroll
     for (int ct = 0; ct < C / 16; ++ct) dx[ct] = M::mma(dx[ct], ldt<RS>(w, 0, 16 * ct, lane), dz);
@@ -250,7 +255,7 @@ template <class T, int C>
 constexpr int linear_dw_lds() {
   return 2 * MF<T>::CK * (C + kDwOut + 2 * lds_pad<T>()) * (int)sizeof(T);
 }
-template <class T, int C>
+template <class T, int C, bool FEW>
 __device__ __forceinline__ void linear_dw(const LinArgs& A, int bx, int by, char* s_raw) {
   using M = MF<T>;
   constexpr int NC = C / M::CK, EV = M::EV, NT = M::NT, CK = M::CK, RS = C + lds_pad<T>();
@@ -319,6 +324,11 @@ __device__ __forceinline__ void linear_dw(const LinArgs& A, int bx, int by, char
           }
         }
         dz = M::pack(d);
+        if constexpr (FEW && sizeof(T) == 2) {
+          const typename M::F dz2 = rest_of<T>(dz, d);
+#pragma unroll
+          for (int ct = 0; ct < C / 16; ++ct) acc[ct] = M::mma(acc[ct], dz2, ldt<RS>(xs, 0, 16 * ct, lane));
+        }
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) db += (d[t].x + d[t].y) + (d[t].z + d[t].w);
@@ -342,7 +352,7 @@ __device__ __forceinline__ void linear_dw(const LinArgs& A, int bx, int by, char
 template <class T, int C>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k_linear_dw(LinArgs A) {
   __shared__ __align__(16) char s_raw[linear_dw_lds<T, C>()];
-  linear_dw<T, C>(A, blockIdx.x, blockIdx.y, s_raw);
+  linear_dw<T, C, false>(A, blockIdx.x, blockIdx.y, s_raw);
 }
 
 // dx and dW of few rows in one launch: neither fills the card alone.  The first dx_blocks blocks
@@ -356,7 +366,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
   if (b < 0)
     linear_dx<T, C, true>(A, blockIdx.x, s_raw);
   else
-    linear_dw<T, C>(A, b % nb, b / nb, s_raw);
+    linear_dw<T, C, true>(A, b % nb, b / nb, s_raw);
 }
 
 // Splits of the rows for dW: about 512 blocks in all, each with at least 32 rows (a split
