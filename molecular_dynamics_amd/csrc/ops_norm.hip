@@ -13,7 +13,7 @@ namespace {
 //   u  = w_pre y ms(y)^-1/2    (from y before it is rounded to the feature type)
 // A row lives in LR = C / V adjacent lanes, V values (16 bytes) each, so the two means are
 // exchanges inside those lanes and every tensor is read or written once, 16 bytes a lane.
-// Bound: HBM.  1,048,576 rows of 128 bf16 without a gate: 192 us, 5.6 TB/s; 131,072 of float32 with one:
+// Bound: HBM.  1,048,576 rows of 128 bf16 without a gate: 192-204 us, 5.3-5.6 TB/s; 131,072 of float32 with one:
 // forward 53 us (6.3 TB/s), backward 87 (6.2).
 template <class T, int V>
 struct Row {
